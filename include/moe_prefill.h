@@ -68,6 +68,12 @@ typedef enum moe_act_dtype {
   MOE_ACT_FP8_E4M3_ROW = 1 /* x and h quantised per row to E4M3 with an fp32 scale */
 } moe_act_dtype;
 
+/* Element types of rows that come in more than one. */
+typedef enum moe_dtype {
+  MOE_DT_BF16 = 0,
+  MOE_DT_F32 = 1
+} moe_dtype;
+
 #define MOE_MAX_EXPERTS 256
 #define MOE_MAX_TOPK 16
 
@@ -293,6 +299,39 @@ int moe_route_topk(const float *logits, const float *bias, int T, int E, int k,
  */
 int moe_quant_rows_fp8(const void *x, int rows, int cols, uint8_t *q, float *s,
                        moe_stream_t stream);
+
+/* ------------------------------------------------------------ residual addition and norm
+ * The step ahead of the layer: the residual stream takes the previous
+ * layer's output, and the layer gets its root-mean-square norm, in bf16 (for
+ * the router and the bf16 path) and / or as E4M3 rows (for the fp8 path):
+ *
+ *   v = residual + x                     (fp32; v = x if residual is NULL)
+ *   residual_out = v                     rounded to its type (to nearest even)
+ *   n = v * weight / sqrt(mean(v^2) + eps)   over each row's d elements
+ *   y = bf16_rne(n)
+ *   s[i] = max_c |n[i,c]| / 448 (1 for an all-zero row),  q = e4m3_rne_saturate(n / s)
+ *
+ * Each output is rounded once, from fp32: q is formed from n, not from y.
+ * The mean is taken in fp64.  A row that holds a NaN or an infinity gets
+ * NaN where the formulas give it; other rows are unaffected.
+ *
+ * x            [rows, d], x_dtype (moe_dtype)
+ * residual     [rows, d], residual_dtype, or NULL
+ * residual_out [rows, d], residual_dtype (without residual: x_dtype), or NULL;
+ *              may be residual itself (or x itself, of one type)
+ * weight       [d], weight_dtype
+ * y            bf16 [rows, d] or NULL;  q uint8 [rows, d] with s fp32 [rows], or both NULL
+ *              (at least one of y and q).  Apart from residual_out no
+ *              output may overlap an input or another output.
+ * Errors: MOE_EINVAL (null x or weight, no output, q without s or s without
+ *         q, rows < 1, d < 1, eps not positive and finite), MOE_EUNSUPPORTED
+ *         (unknown type, d not a multiple of 8 or above 16384,
+ *         residual_out without residual of another type than x), MOE_EALIGN,
+ *         MOE_EHIP.
+ */
+int moe_add_rmsnorm(const void *x, int x_dtype, const void *residual, void *residual_out,
+                    int residual_dtype, const void *weight, int weight_dtype, float eps, int rows,
+                    int d, void *y, uint8_t *q, float *s, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,7 @@ from ._lib import (MOE_ACT_BF16, MOE_ACT_FP8_E4M3_ROW, MOE_W_BF16, MOE_W_FP8_E4M
                    LibraryNotBuilt, MoeFfnDesc)
 
 __all__ = [
-    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "combine", "combine_shared", "quant_rows_fp8", "MoEPrefill", "RouteTable",
+    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "MoEPrefill", "RouteTable",
     "ffn_desc", "ffn_plan", "ffn_gate_up", "ffn_down", "LibraryNotBuilt", "load_library",
 ]
 
@@ -291,6 +291,87 @@ def quant_rows_fp8(x, q=None, s=None):
     rc = lib.moe_quant_rows_fp8(_ptr(x), rows, cols, _ptr(q), _ptr(s), _stream())
     _lib.check(rc, "moe_quant_rows_fp8")
     return q, s
+
+
+def _need_rows(t, name, shape, dtypes, device):
+    """A contiguous tensor of the given shape, of one of the given types and
+    on the given device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_current(t, name):
+    """The device of t, which has to be the current one: the kernels run on
+    its current stream."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU device")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, which is not the current device")
+    return dev
+
+
+def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, y=None, q=None,
+                s=None, want_bf16=True, want_fp8=False):
+    """moe_add_rmsnorm: v = residual + x, and the root-mean-square norm of v.
+
+    x [rows, d] and residual (optional) are bf16 or fp32, weight [d] likewise.
+    Returns (y, residual_out, q, s): the norm in bf16, the sum v in the
+    residual's type, E4M3 codes (uint8) and row scales of the norm -- None for
+    what is not wanted.  residual_out may be residual itself; without a
+    residual it is written only if given (then v is x).  No rows: nothing is
+    launched."""
+    torch = _torch()
+    lib = _lib.load()
+    dev = _on_current(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must have 2 dims, got {x.dim()}")
+    shape, kinds = x.shape, (torch.bfloat16, torch.float32)
+    rows, d = shape
+    _need_rows(x, "x", shape, kinds, dev)
+    _need_rows(weight, "weight", shape[1:], kinds, dev)
+    if residual is not None:
+        _need_rows(residual, "residual", shape, kinds, dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+    if residual_out is not None:
+        _need_rows(residual_out, "residual_out", shape,
+                   ((x if residual is None else residual).dtype,), dev)
+    if y is None:
+        if want_bf16:
+            y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need_rows(y, "y", shape, (torch.bfloat16,), dev)
+    if q is not None:
+        _need_rows(q, "q", shape, (torch.uint8,), dev)
+    elif want_fp8 or s is not None:
+        q = torch.empty(shape, dtype=torch.uint8, device=dev)
+    if s is not None:
+        _need_rows(s, "s", shape[:1], (torch.float32,), dev)
+    elif q is not None:
+        s = torch.empty(rows, dtype=torch.float32, device=dev)
+    if rows == 0:
+        return y, residual_out, q, s
+    f32 = torch.float32
+    rdt = (x if residual is None else residual).dtype
+    rc = lib.moe_add_rmsnorm(x.data_ptr(), int(x.dtype == f32), _ptr(residual),
+                             _ptr(residual_out), int(rdt == f32), weight.data_ptr(),
+                             int(weight.dtype == f32), eps, rows, d, _ptr(y), _ptr(q), _ptr(s),
+                             _stream())
+    _lib.check(rc, "moe_add_rmsnorm")
+    return y, residual_out, q, s
 
 
 class MoEPrefill:

@@ -20,6 +20,8 @@ MOE_ROUTE_NOALLOC_MAX_ROUTES = 1 << 20
 
 MOE_W_BF16 = 0
 MOE_W_FP8_E4M3_B128 = 1
+MOE_DT_BF16 = 0
+MOE_DT_F32 = 1
 MOE_ACT_BF16 = 0
 MOE_ACT_FP8_E4M3_ROW = 1
 
@@ -29,7 +31,7 @@ EXPORTED = [
     "moe_grouped_ffn_workspace", "moe_grouped_ffn",
     "moe_ffn_plan", "moe_ffn_gate_up", "moe_ffn_down",
     "moe_combine", "moe_quant_rows_fp8", "moe_route_topk", "moe_combine_shared",
-    "moe_route_build_noalloc",
+    "moe_route_build_noalloc", "moe_add_rmsnorm",
 ]
 
 
@@ -87,6 +89,9 @@ def load() -> ctypes.CDLL:
     lib.moe_combine_shared.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
     lib.moe_route_topk.restype = i32
     lib.moe_route_topk.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp]
+    lib.moe_add_rmsnorm.restype = i32
+    lib.moe_add_rmsnorm.argtypes = [vp, i32, vp, vp, i32, vp, i32, ctypes.c_float, i32, i32, vp,
+                                    vp, vp, vp]
     _lib = lib
     return lib
 

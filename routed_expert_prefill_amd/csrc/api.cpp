@@ -331,4 +331,33 @@ int moe_quant_rows_fp8(const void *x, int rows, int cols, uint8_t *q, float *s,
                                             static_cast<hipStream_t>(stream)));
 }
 
+int moe_add_rmsnorm(const void *x, int x_dtype, const void *residual, void *residual_out,
+                    int residual_dtype, const void *weight, int weight_dtype, float eps, int rows,
+                    int d, void *y, uint8_t *q, float *s, moe_stream_t stream) {
+  if (!x || !weight || (!y && !q) || (q == nullptr) != (s == nullptr)) return MOE_EINVAL;
+  if (rows < 1 || d < 1 || !(eps > 0.0f) || !(eps < 3.40282347e38f)) return MOE_EINVAL;
+  const auto known = [](int t) { return t == MOE_DT_BF16 || t == MOE_DT_F32; };
+  if (!known(x_dtype) || !known(weight_dtype) || !known(residual_dtype)) return MOE_EUNSUPPORTED;
+  if (!residual && residual_out && residual_dtype != x_dtype) return MOE_EUNSUPPORTED;
+  if (d % 8 != 0 || d > moe::norm_max_cols()) return MOE_EUNSUPPORTED;
+  const void *ptrs[] = {x, residual, residual_out, weight, y, q, s};
+  for (const void *p : ptrs)
+    if (p && misaligned(p)) return MOE_EALIGN;
+  moe::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.residual_out = residual_out;
+  a.weight = weight;
+  a.y = static_cast<uint16_t *>(y);
+  a.q = q;
+  a.s = s;
+  a.eps = eps;
+  a.rows = rows;
+  a.d = d;
+  a.x_f32 = x_dtype == MOE_DT_F32;
+  a.w_f32 = weight_dtype == MOE_DT_F32;
+  a.res_kind = !residual ? 0 : residual_dtype == MOE_DT_F32 ? 2 : 1;
+  return status_from(moe::launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

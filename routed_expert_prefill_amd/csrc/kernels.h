@@ -35,6 +35,23 @@ int quant_max_cols();
 hipError_t launch_quant_rows(const uint16_t *x, int rows, const int32_t *rows_dev, int cols,
                              uint8_t *q, float *s, int grid_cap, hipStream_t stream);
 
+// Residual addition and root-mean-square norm of rows (norm.hip).
+struct NormArgs {
+  const void *x;         // [rows, d] bf16, or fp32 if x_f32
+  const void *residual;  // [rows, d]; res_kind 0: none, 1: bf16, 2: fp32
+  void *residual_out;    // as residual (as x without one), or null
+  const void *weight;    // [d] bf16, or fp32 if w_f32
+  uint16_t *y;           // bf16 [rows, d] or null
+  uint8_t *q;            // E4M3 codes [rows, d] or null
+  float *s;              // [rows], with q
+  float eps;
+  int rows, d;
+  bool x_f32, w_f32;
+  int res_kind;
+};
+int norm_max_cols();
+hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t stream);
+
 // Tile list of the grouped FFN from the expert offsets (one thread per
 // expert); also zeroes the work-queue heads.
 hipError_t launch_grouped_schedule(const int32_t *offsets, int E, Schedule *sch, Tile *tiles,

@@ -1,0 +1,45 @@
+"""The C ABI of the norm and of the 4-bit expert calls on the host: bad
+arguments are rejected with the documented status before the GPU is touched
+(no call here passes validation)."""
+import os
+
+import pytest
+
+from routed_expert_prefill_amd import _lib
+
+A = 0x10000000  # a 16-byte-aligned fake device address (never dereferenced)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        import __graft_entry__
+
+        __graft_entry__.build()
+    return _lib.load()
+
+
+def test_add_rmsnorm_errors(lib):
+    def f(x=A, xt=0, r=0, ro=0, rt=0, w=A, wt=0, eps=1e-6, rows=4, d=256, y=A, q=0, s=0):
+        return lib.moe_add_rmsnorm(x or None, xt, r or None, ro or None, rt, w or None, wt, eps,
+                                   rows, d, y or None, q or None, s or None, None)
+
+    assert f(x=0) == _lib.MOE_EINVAL
+    assert f(w=0) == _lib.MOE_EINVAL
+    assert f(y=0) == _lib.MOE_EINVAL  # no output
+    assert f(q=A) == _lib.MOE_EINVAL  # codes without scales
+    assert f(s=A) == _lib.MOE_EINVAL  # scales without codes
+    assert f(rows=0) == _lib.MOE_EINVAL
+    assert f(d=0) == _lib.MOE_EINVAL
+    for eps in (0.0, -1e-6, float("nan"), float("inf")):
+        assert f(eps=eps) == _lib.MOE_EINVAL
+    assert f(xt=2) == _lib.MOE_EUNSUPPORTED
+    assert f(wt=-1) == _lib.MOE_EUNSUPPORTED
+    assert f(rt=3) == _lib.MOE_EUNSUPPORTED
+    assert f(ro=A, rt=1) == _lib.MOE_EUNSUPPORTED  # no residual: residual_out has x's type
+    assert f(d=252) == _lib.MOE_EUNSUPPORTED
+    assert f(d=16392) == _lib.MOE_EUNSUPPORTED
+    for name in ("x", "r", "ro", "w", "y"):
+        assert f(**{name: A + 8}) == _lib.MOE_EALIGN
+    assert f(q=A + 8, s=A) == _lib.MOE_EALIGN
+    assert f(q=A, s=A + 4) == _lib.MOE_EALIGN
