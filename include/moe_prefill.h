@@ -59,7 +59,8 @@ typedef enum moe_status {
 /* Weight storage formats. */
 typedef enum moe_weight_dtype {
   MOE_W_BF16 = 0,          /* bf16 weights */
-  MOE_W_FP8_E4M3_B128 = 1  /* OCP E4M3FN codes, one fp32 scale per 128x128 block */
+  MOE_W_FP8_E4M3_B128 = 1, /* OCP E4M3FN codes, one fp32 scale per 128x128 block */
+  MOE_W_MXFP4 = 2          /* OCP MXFP4: E2M1 codes, one E8M0 scale per 32 elements of a row */
 } moe_weight_dtype;
 
 /* Activation formats fed to the GEMMs. */
@@ -87,7 +88,8 @@ typedef struct moe_ffn_desc {
   int32_t d;            /* model width, multiple of 128 */
   int32_t f;            /* expert FFN width, multiple of 128 */
   int32_t weight_dtype; /* moe_weight_dtype */
-  int32_t act_dtype;    /* moe_act_dtype; FP8_E4M3_ROW iff weights are FP8_E4M3_B128 */
+  int32_t act_dtype;    /* moe_act_dtype; FP8_E4M3_ROW iff weights are FP8_E4M3_B128
+                           (bf16 activations with bf16 and MXFP4 weights) */
 } moe_ffn_desc;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -164,10 +166,14 @@ int moe_route_build_noalloc(const int32_t *topk_ids, const uint8_t *route_mask, 
  * offsets       int32 [E+2], sorted_routes int32 [T*k]: from moe_route_build
  * w_gate, w_up  [E,f,d]  (row n of expert e holds output feature n; d contiguous)
  * w_down        [E,d,f]
- *               bf16, or E4M3 codes (uint8) for MOE_W_FP8_E4M3_B128
+ *               bf16, E4M3 codes (uint8) for MOE_W_FP8_E4M3_B128, or E2M1
+ *               codes for MOE_W_MXFP4: uint8 [E,f,d/2] and [E,d,f/2], column
+ *               c of a row in bits 4 (c % 2) .. +3 of byte c / 2
  * s_gate, s_up  fp32 [E, f/128, d/128]; s_down fp32 [E, d/128, f/128]:
  *               block scales, element [n,c] of expert e is multiplied by
  *               s[e, n/128, c/128].  NULL for bf16 weights.
+ *               For MOE_W_MXFP4: E8M0 bytes, uint8 [E, f, d/32] and [E, d, f/32];
+ *               element [n,c] is multiplied by 2^(s[e, n, c/32] - 127) (255: NaN).
  * y             fp32 [T*k, d]
  * workspace     at least moe_grouped_ffn_workspace(desc) bytes; holds the
  *               tile schedule, h and (fp8) the quantised activations.
@@ -176,13 +182,16 @@ int moe_route_build_noalloc(const int32_t *topk_ids, const uint8_t *route_mask, 
  * rows are quantised as s = fp32(max|v|)/448, q = e4m3_rne_saturate(v / s)
  * (IEEE fp32 division; an all-zero row gets s = 1, q = 0), and the GEMMs
  * consume decode(q) * s.
+ *
+ * MXFP4 mode (weights MXFP4, activations BF16): the formulas above with the
+ * weights' exact values, which are bf16 numbers; no other rounding is added.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
  */
 size_t moe_grouped_ffn_workspace(const moe_ffn_desc *desc /* host */);
 int moe_grouped_ffn(const moe_ffn_desc *desc /* host */, const void *x, const int32_t *offsets,
                     const int32_t *sorted_routes, const void *w_gate, const void *w_up,
-                    const void *w_down, const float *s_gate, const float *s_up,
-                    const float *s_down, float *y, void *workspace, size_t workspace_bytes,
+                    const void *w_down, const void *s_gate, const void *s_up,
+                    const void *s_down, float *y, void *workspace, size_t workspace_bytes,
                     moe_stream_t stream);
 
 /* ------------------------------------------------------------ FFN stages
@@ -207,10 +216,10 @@ int moe_ffn_plan(const moe_ffn_desc *desc /* host */, const void *x, const int32
                  void *workspace, size_t workspace_bytes, moe_stream_t stream);
 int moe_ffn_gate_up(const moe_ffn_desc *desc /* host */, const void *x,
                     const int32_t *sorted_routes, const void *w_gate, const void *w_up,
-                    const float *s_gate, const float *s_up, void *workspace,
+                    const void *s_gate, const void *s_up, void *workspace,
                     size_t workspace_bytes, moe_stream_t stream);
 int moe_ffn_down(const moe_ffn_desc *desc /* host */, const int32_t *offsets, const void *w_down,
-                 const float *s_down, float *y, void *workspace, size_t workspace_bytes,
+                 const void *s_down, float *y, void *workspace, size_t workspace_bytes,
                  moe_stream_t stream);
 
 /* ------------------------------------------------------------ combine

@@ -121,6 +121,25 @@ def quant_rows_fp8(rows_f32: np.ndarray):
     return q, s
 
 
+E2M1_VALUES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def mxfp4_decode(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """OCP MXFP4 rows -> fp64 values.
+
+    codes uint8 [..., cols / 2]: column c in bits 4 (c % 2) .. +3 of byte
+    c / 2; bit 3 of a code is the sign, the rest indexes E2M1_VALUES.  scales
+    uint8 [..., cols / 32]: E8M0, 2^(byte - 127) for 32 columns, 255 is NaN.
+    """
+    c = np.asarray(codes, dtype=np.uint8)
+    s = np.asarray(scales, dtype=np.uint8)
+    table = np.array(E2M1_VALUES + tuple(-v for v in E2M1_VALUES), dtype=np.float64)
+    v = np.stack([table[c & 15], table[c >> 4]], axis=-1)
+    v = v.reshape(s.shape + (32,))
+    e = np.where(s == 255, np.nan, np.ldexp(1.0, s.astype(np.int64) - 127))
+    return (v * e[..., None]).reshape(c.shape[:-1] + (c.shape[-1] * 2,))
+
+
 def silu(z: np.ndarray) -> np.ndarray:
     """silu(z) = z / (1 + exp(-z)) in fp64."""
     z = np.asarray(z, dtype=np.float64)

@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional
 
 from . import _lib
 from ._lib import (MOE_ACT_BF16, MOE_ACT_FP8_E4M3_ROW, MOE_W_BF16, MOE_W_FP8_E4M3_B128,
-                   LibraryNotBuilt, MoeFfnDesc)
+                   MOE_W_MXFP4, LibraryNotBuilt, MoeFfnDesc)
 
 __all__ = [
     "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "MoEPrefill", "RouteTable",
@@ -136,19 +136,50 @@ def route_build_noalloc(topk_ids, route_mask, E: int, out: Optional[RouteTable] 
     return out
 
 
-def ffn_desc(T: int, k: int, E: int, d: int, f: int, fp8: bool = False) -> MoeFfnDesc:
-    return MoeFfnDesc(T, k, E, d, f, MOE_W_FP8_E4M3_B128 if fp8 else MOE_W_BF16,
-                      MOE_ACT_FP8_E4M3_ROW if fp8 else MOE_ACT_BF16)
+def ffn_desc(T: int, k: int, E: int, d: int, f: int, fp8: bool = False,
+             weights: Optional[str] = None) -> MoeFfnDesc:
+    """Shapes and formats of a layer; weights: "bf16", "fp8" or "mxfp4"
+    (default: by fp8)."""
+    if weights is None:
+        weights = "fp8" if fp8 else "bf16"
+    if weights not in _WEIGHTS:
+        raise ValueError(f"weights must be one of {sorted(_WEIGHTS)}, got {weights!r}")
+    if fp8 and weights != "fp8":
+        raise ValueError(f"fp8=True contradicts weights={weights!r}")
+    return MoeFfnDesc(T, k, E, d, f, *_WEIGHTS[weights])
+
+
+# weight and activation formats by name
+_WEIGHTS = {"bf16": (MOE_W_BF16, MOE_ACT_BF16),
+            "fp8": (MOE_W_FP8_E4M3_B128, MOE_ACT_FP8_E4M3_ROW),
+            "mxfp4": (MOE_W_MXFP4, MOE_ACT_BF16)}
+
+
+def _need_mx4(E, d, f, w_gate, w_up, w_down, s_gate, s_up, s_down):
+    """Codes and scales of MXFP4 weights: [E, rows, cols/2] and [E, rows, cols/32]."""
+    torch = _torch()
+    for name, w, s, rows, cols in (("gate", w_gate, s_gate, f, d), ("up", w_up, s_up, f, d),
+                                   ("down", w_down, s_down, d, f)):
+        _need(w, "w_" + name, torch.uint8, 3)
+        _need(s, "s_" + name, torch.uint8, 3)
+        if w.shape != (E, rows, cols // 2) or s.shape != (E, rows, cols // 32):
+            raise ValueError(f"w_{name} must have shape {(E, rows, cols // 2)} and s_{name} "
+                             f"{(E, rows, cols // 32)}, got {tuple(w.shape)} and {tuple(s.shape)}")
 
 
 def grouped_ffn(x, offsets, sorted_routes, w_gate, w_up, w_down, k: int, s_gate=None,
                 s_up=None, s_down=None, y=None, workspace=None):
-    """moe_grouped_ffn: y[i] = Wd . bf16(silu(Wg . x) * (Wu . x)) per sorted row i."""
+    """moe_grouped_ffn: y[i] = Wd . bf16(silu(Wg . x) * (Wu . x)) per sorted row i.
+
+    Weights bf16; E4M3 codes (uint8) with fp32 block scales; or MXFP4 codes
+    (uint8, two columns to a byte) with E8M0 scales (uint8, one for 32 columns
+    of a row)."""
     torch = _torch()
     lib = _lib.load()
-    fp8 = w_gate.dtype == torch.uint8
+    mx4 = w_gate.dtype == torch.uint8 and s_gate is not None and s_gate.dtype == torch.uint8
+    fp8 = w_gate.dtype == torch.uint8 and not mx4
     _need(x, "x", torch.bfloat16, 2)
-    wdt = torch.uint8 if fp8 else torch.bfloat16
+    wdt = torch.uint8 if fp8 or mx4 else torch.bfloat16
     for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
         _need(w, name, wdt, 3)
     _need(offsets, "offsets", torch.int32, 1)
@@ -158,11 +189,13 @@ def grouped_ffn(x, offsets, sorted_routes, w_gate, w_up, w_down, k: int, s_gate=
             _need(s, name, torch.float32, 3)
     T, d = x.shape
     E, f, d2 = w_gate.shape
-    if d2 != d or tuple(w_up.shape) != (E, f, d) or tuple(w_down.shape) != (E, d, f):
+    if mx4:
+        _need_mx4(E, d, f, w_gate, w_up, w_down, s_gate, s_up, s_down)
+    elif d2 != d or tuple(w_up.shape) != (E, f, d) or tuple(w_down.shape) != (E, d, f):
         raise ValueError("weight shapes must be w_gate/w_up [E,f,d] and w_down [E,d,f]")
     if offsets.numel() != E + 2 or sorted_routes.numel() != T * k:
         raise ValueError("offsets must have E+2 entries and sorted_routes T*k")
-    desc = ffn_desc(T, k, E, d, f, fp8)
+    desc = ffn_desc(T, k, E, d, f, weights="mxfp4" if mx4 else "fp8" if fp8 else "bf16")
     if y is None:
         y = torch.empty(T * k, d, dtype=torch.float32, device=x.device)
     _need(y, "y", torch.float32, 2)
@@ -376,12 +409,20 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, 
 
 class MoEPrefill:
     """The whole path -- route build, grouped FFN, combine -- with buffers kept
-    across calls (nothing is allocated per call after construction)."""
+    across calls (nothing is allocated per call after construction).
 
-    def __init__(self, T: int, k: int, E: int, d: int, f: int, fp8: bool = False, device="cuda"):
+    weights: "bf16", "fp8" or "mxfp4" (default: by fp8).  out_dtype:
+    torch.float32 (default) or torch.bfloat16."""
+
+    def __init__(self, T: int, k: int, E: int, d: int, f: int, fp8: bool = False, device="cuda",
+                 weights: Optional[str] = None, out_dtype=None):
         torch = _torch()
         lib = _lib.load()
-        self.T, self.k, self.E, self.d, self.f, self.fp8 = T, k, E, d, f, fp8
+        if out_dtype not in (None, torch.float32, torch.bfloat16):
+            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+        self.T, self.k, self.E, self.d, self.f = T, k, E, d, f
+        self.weights = weights or ("fp8" if fp8 else "bf16")
+        self.fp8 = self.weights == "fp8"
         dev = torch.device(device)
         R = T * k
         self.rt = RouteTable(
@@ -392,10 +433,10 @@ class MoEPrefill:
         )
         self.rb_ws = torch.empty(max(lib.moe_route_build_workspace(T, k, E), 256),
                                  dtype=torch.uint8, device=dev)
-        self.desc = ffn_desc(T, k, E, d, f, fp8)
+        self.desc = ffn_desc(T, k, E, d, f, fp8, weights)
         self.ffn_ws = _ffn_ws(self.desc, dev, None)
         self.y = torch.empty(R, d, dtype=torch.float32, device=dev)
-        self.out = torch.empty(T, d, dtype=torch.float32, device=dev)
+        self.out = torch.empty(T, d, dtype=out_dtype or torch.float32, device=dev)
         # offsets[E]: rows of y the FFN writes.  The combine reads no route at
         # or past it, so active routes whose ids lie outside [0, E) -- which
         # the route build sends to the trailing bin -- add exact zeros, as
@@ -403,10 +444,11 @@ class MoEPrefill:
         self.row_limit = self.rt.offsets[E:E + 1]
 
     def __call__(self, x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate=None,
-                 s_up=None, s_down=None, stage_events=None):
-        """One pass of the path.  stage_events: optional torch events recorded
-        on the current stream: 2 events around the gate/up stage, or 6 --
-        before the route build and after each of route build, FFN plan,
+                 s_up=None, s_down=None, stage_events=None, shared=None):
+        """One pass of the path.  shared: fp32 rows [T, d] of the shared
+        expert, added to the routed sum.  stage_events: optional torch events
+        recorded on the current stream: 2 events around the gate/up stage, or
+        6 -- before the route build and after each of route build, FFN plan,
         gate/up, down and combine."""
         ev = stage_events
         if ev is not None and len(ev) == 2:
@@ -417,8 +459,8 @@ class MoEPrefill:
         if ev is None:
             grouped_ffn(x, rt.offsets, rt.sorted_routes, w_gate, w_up, w_down, self.k, s_gate,
                         s_up, s_down, y=self.y, workspace=self.ffn_ws)
-            return combine(self.y, rt.route_rows, topk_w, route_mask, out=self.out,
-                           row_limit=self.row_limit)
+            return self._combine(rt, topk_w, route_mask, shared)
+
         def mark(i):
             if ev[i] is not None:
                 ev[i].record()
@@ -430,7 +472,17 @@ class MoEPrefill:
         mark(3)
         ffn_down(self.desc, rt.offsets, w_down, s_down, self.y, self.ffn_ws)
         mark(4)
-        out = combine(self.y, rt.route_rows, topk_w, route_mask, out=self.out,
-                      row_limit=self.row_limit)
+        out = self._combine(rt, topk_w, route_mask, shared)
         mark(5)
         return out
+
+    def _combine(self, rt, topk_w, route_mask, shared):
+        torch = _torch()
+        if shared is None and self.out.dtype == torch.float32:
+            return combine(self.y, rt.route_rows, topk_w, route_mask, out=self.out,
+                           row_limit=self.row_limit)
+        f32 = self.out.dtype == torch.float32
+        combine_shared(self.y, rt.route_rows, topk_w, route_mask, shared=shared,
+                       out=self.out if f32 else None, out_bf16=None if f32 else self.out,
+                       want_fp32=f32, row_limit=self.row_limit)
+        return self.out

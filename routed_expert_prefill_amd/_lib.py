@@ -20,6 +20,7 @@ MOE_ROUTE_NOALLOC_MAX_ROUTES = 1 << 20
 
 MOE_W_BF16 = 0
 MOE_W_FP8_E4M3_B128 = 1
+MOE_W_MXFP4 = 2
 MOE_DT_BF16 = 0
 MOE_DT_F32 = 1
 MOE_ACT_BF16 = 0

@@ -61,7 +61,7 @@ bool ffn_desc_status(const moe_ffn_desc *d, int *st) {
   }
   const bool w8 = d->weight_dtype == MOE_W_FP8_E4M3_B128;
   const bool a8 = d->act_dtype == MOE_ACT_FP8_E4M3_ROW;
-  const bool wok = d->weight_dtype == MOE_W_BF16 || w8;
+  const bool wok = d->weight_dtype == MOE_W_BF16 || d->weight_dtype == MOE_W_MXFP4 || w8;
   const bool aok = d->act_dtype == MOE_ACT_BF16 || a8;
   if (!wok || !aok || w8 != a8) {
     *st = MOE_EUNSUPPORTED;
@@ -175,18 +175,20 @@ namespace {
 // Shared body of moe_grouped_ffn and its stage calls.
 int ffn_call(const moe_ffn_desc *desc, int stages, const void *x, const int32_t *offsets,
              const int32_t *sorted_routes, const void *w_gate, const void *w_up,
-             const void *w_down, const float *s_gate, const float *s_up, const float *s_down,
+             const void *w_down, const void *s_gate, const void *s_up, const void *s_down,
              float *y, void *workspace, size_t workspace_bytes, moe_stream_t stream) {
   int st;
   if (!ffn_desc_status(desc, &st)) return st;
   const bool fp8 = desc->weight_dtype == MOE_W_FP8_E4M3_B128;
+  const bool mx4 = desc->weight_dtype == MOE_W_MXFP4;
+  const bool scaled = fp8 || mx4;
   const bool plan = stages & moe::kStagePlan, gu = stages & moe::kStageGateUp,
              dn = stages & moe::kStageDown;
   // pointers each requested stage reads or writes
   if (plan && (!offsets || (fp8 && !x))) return MOE_EINVAL;
-  if (gu && (!x || !sorted_routes || !w_gate || !w_up || (fp8 && (!s_gate || !s_up))))
+  if (gu && (!x || !sorted_routes || !w_gate || !w_up || (scaled && (!s_gate || !s_up))))
     return MOE_EINVAL;
-  if (dn && (!offsets || !w_down || !y || (fp8 && !s_down))) return MOE_EINVAL;
+  if (dn && (!offsets || !w_down || !y || (scaled && !s_down))) return MOE_EINVAL;
   const void *ptrs[] = {x, offsets, sorted_routes, w_gate, w_up, w_down, s_gate, s_up, s_down, y,
                         workspace};
   for (const void *p : ptrs)
@@ -197,6 +199,30 @@ int ffn_call(const moe_ffn_desc *desc, int stages, const void *x, const int32_t 
   char *ws = static_cast<char *>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int R = desc->T * desc->k;
+  if (mx4) {
+    moe::FfnLaunchMx4 L{};
+    L.x = static_cast<const uint16_t *>(x);
+    L.offsets = offsets;
+    L.sorted_routes = sorted_routes;
+    L.wg = static_cast<const uint8_t *>(w_gate);
+    L.wu = static_cast<const uint8_t *>(w_up);
+    L.wd = static_cast<const uint8_t *>(w_down);
+    L.sg = static_cast<const uint8_t *>(s_gate);
+    L.su = static_cast<const uint8_t *>(s_up);
+    L.sd = static_cast<const uint8_t *>(s_down);
+    L.y = y;
+    L.h = reinterpret_cast<uint16_t *>(ws + lay.h);
+    L.sch = reinterpret_cast<moe::Schedule *>(ws + lay.sched);
+    L.tiles = reinterpret_cast<moe::Tile *>(ws + lay.tiles);
+    L.num_cus = num_cus_current_device();
+    L.T = desc->T;
+    L.k = desc->k;
+    L.E = desc->E;
+    L.d = desc->d;
+    L.f = desc->f;
+    L.R = R;
+    return status_from(moe::launch_ffn_mx4(L, stages, s));
+  }
   if (!fp8) {
     moe::FfnLaunch L{};
     L.x = static_cast<const uint16_t *>(x);
@@ -227,9 +253,9 @@ int ffn_call(const moe_ffn_desc *desc, int stages, const void *x, const int32_t 
   L.wg = static_cast<const uint8_t *>(w_gate);
   L.wu = static_cast<const uint8_t *>(w_up);
   L.wd = static_cast<const uint8_t *>(w_down);
-  L.sg = s_gate;
-  L.su = s_up;
-  L.sd = s_down;
+  L.sg = static_cast<const float *>(s_gate);
+  L.su = static_cast<const float *>(s_up);
+  L.sd = static_cast<const float *>(s_down);
   L.y = y;
   L.h = reinterpret_cast<uint16_t *>(ws + lay.h);
   L.qh = reinterpret_cast<uint8_t *>(ws + lay.qh);
@@ -254,8 +280,8 @@ extern "C" {
 
 int moe_grouped_ffn(const moe_ffn_desc *desc, const void *x, const int32_t *offsets,
                     const int32_t *sorted_routes, const void *w_gate, const void *w_up,
-                    const void *w_down, const float *s_gate, const float *s_up,
-                    const float *s_down, float *y, void *workspace, size_t workspace_bytes,
+                    const void *w_down, const void *s_gate, const void *s_up,
+                    const void *s_down, float *y, void *workspace, size_t workspace_bytes,
                     moe_stream_t stream) {
   return ffn_call(desc, moe::kStageAll, x, offsets, sorted_routes, w_gate, w_up, w_down, s_gate,
                   s_up, s_down, y, workspace, workspace_bytes, stream);
@@ -268,14 +294,14 @@ int moe_ffn_plan(const moe_ffn_desc *desc, const void *x, const int32_t *offsets
 }
 
 int moe_ffn_gate_up(const moe_ffn_desc *desc, const void *x, const int32_t *sorted_routes,
-                    const void *w_gate, const void *w_up, const float *s_gate, const float *s_up,
+                    const void *w_gate, const void *w_up, const void *s_gate, const void *s_up,
                     void *workspace, size_t workspace_bytes, moe_stream_t stream) {
   return ffn_call(desc, moe::kStageGateUp, x, nullptr, sorted_routes, w_gate, w_up, nullptr,
                   s_gate, s_up, nullptr, nullptr, workspace, workspace_bytes, stream);
 }
 
 int moe_ffn_down(const moe_ffn_desc *desc, const int32_t *offsets, const void *w_down,
-                 const float *s_down, float *y, void *workspace, size_t workspace_bytes,
+                 const void *s_down, float *y, void *workspace, size_t workspace_bytes,
                  moe_stream_t stream) {
   return ffn_call(desc, moe::kStageDown, nullptr, offsets, nullptr, nullptr, nullptr, w_down,
                   nullptr, nullptr, s_down, y, workspace, workspace_bytes, stream);

@@ -99,6 +99,22 @@ struct FfnLaunchFp8 {
 };
 hipError_t launch_ffn_fp8(const FfnLaunchFp8 &L, int stages, hipStream_t stream);
 
+// Grouped FFN with MXFP4 weights and bf16 activations (ffn_mxfp4.hip).
+struct FfnLaunchMx4 {
+  const uint16_t *x;
+  const int32_t *offsets;
+  const int32_t *sorted_routes;
+  const uint8_t *wg, *wu, *wd;  // codes, two to a byte
+  const uint8_t *sg, *su, *sd;  // E8M0 scales
+  float *y;
+  uint16_t *h;
+  Schedule *sch;
+  Tile *tiles;
+  int T, k, E, d, f, R;
+  int num_cus;
+};
+hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream);
+
 // Per-row E4M3 quantisation of bf16 rows whose maxima are known: amax_bits[r]
 // holds the fp32 bits of max |x[r, :]|; same codes and scales as
 // launch_quant_rows.  rows_dev as there.

@@ -1,6 +1,7 @@
 """The C ABI of the norm and of the 4-bit expert calls on the host: bad
 arguments are rejected with the documented status before the GPU is touched
 (no call here passes validation)."""
+import ctypes
 import os
 
 import pytest
@@ -43,3 +44,27 @@ def test_add_rmsnorm_errors(lib):
         assert f(**{name: A + 8}) == _lib.MOE_EALIGN
     assert f(q=A + 8, s=A) == _lib.MOE_EALIGN
     assert f(q=A, s=A + 4) == _lib.MOE_EALIGN
+
+
+def _desc(T=32, k=6, E=16, d=512, f=256, w=_lib.MOE_W_MXFP4, a=_lib.MOE_ACT_BF16):
+    return _lib.MoeFfnDesc(T, k, E, d, f, w, a)
+
+
+def test_mxfp4_ffn_errors(lib):
+    def f(desc=None, x=A, wg=A, sg=A, su=A, sd=A, ws=A, wsb=1 << 40):
+        return lib.moe_grouped_ffn(ctypes.byref(desc or _desc()), x, A, A, wg, A, A, sg or None,
+                                   su or None, sd or None, A, ws or None, wsb, None)
+
+    q = lambda **kw: lib.moe_grouped_ffn_workspace(ctypes.byref(_desc(**kw)))  # noqa: E731
+    assert q() == q(w=_lib.MOE_W_BF16) > 0  # h alone, as with bf16 weights
+    assert q(a=_lib.MOE_ACT_FP8_E4M3_ROW) == 0 and q(w=3) == 0
+    for s in ("sg", "su", "sd"):
+        assert f(**{s: 0}) == _lib.MOE_EINVAL  # scales are needed
+        assert f(**{s: A + 8}) == _lib.MOE_EALIGN
+    assert f(desc=_desc(a=_lib.MOE_ACT_FP8_E4M3_ROW)) == _lib.MOE_EUNSUPPORTED
+    assert f(desc=_desc(d=192)) == _lib.MOE_EUNSUPPORTED
+    assert f(wg=A + 8) == _lib.MOE_EALIGN
+    assert f(ws=0) == _lib.MOE_EWORKSPACE and f(wsb=4096) == _lib.MOE_EWORKSPACE
+    d = ctypes.byref(_desc())
+    assert lib.moe_ffn_gate_up(d, A, A, A, A, None, A, A, 1 << 40, None) == _lib.MOE_EINVAL
+    assert lib.moe_ffn_down(d, A, A, None, A, A, 1 << 40, None) == _lib.MOE_EINVAL
