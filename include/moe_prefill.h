@@ -309,6 +309,40 @@ int moe_route_topk(const float *logits, const float *bias, int T, int E, int k,
 int moe_quant_rows_fp8(const void *x, int rows, int cols, uint8_t *q, float *s,
                        moe_stream_t stream);
 
+/* ------------------------------------------------------------ single tokens
+ * The routed experts for decoding: matrix-vector products with MXFP4
+ * weights straight from the router's ids, in two launches.  The result is
+ * that of moe_route_build, moe_grouped_ffn and moe_combine_shared on the
+ * same inputs (with the row limit), sums of products in another order:
+ *
+ *   routed[t] = sum over j ascending, route (t, j) read, of topk_w[t,j] *
+ *               Wd[e] . bf16_rne(silu(Wg[e] . x[t]) * (Wu[e] . x[t])),  e = topk_ids[t,j]
+ *   out[t] = routed[t] + shared[t],  out_bf16[t] = bf16_rne(out[t])
+ *
+ * A route is read when route_mask[r] != 0 (or route_mask is NULL) and its id
+ * lies in [0, E); any other adds an exact zero, its gate is not read, and a
+ * token with no route read gets +0.0 (plus its shared row).  The weights of an
+ * expert are read for the first route that names it.
+ *
+ * desc        weight_dtype MOE_W_MXFP4, act_dtype MOE_ACT_BF16, T * k at most
+ *             MOE_DECODE_MAX_ROUTES
+ * x           bf16 [T,d]; topk_ids int32 [T,k]; topk_w fp32 [T,k];
+ *             route_mask uint8 [T,k] or NULL; weights and scales as for
+ *             moe_grouped_ffn; shared fp32 [T,d] or NULL
+ * out         fp32 [T,d] or NULL; out_bf16 bf16 [T,d] or NULL (at least one)
+ * workspace   at least moe_decode_ffn_workspace(desc) bytes (h); contents on
+ *             entry are ignored
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED (also: other weights, more routes),
+ *         MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
+ */
+#define MOE_DECODE_MAX_ROUTES 64
+size_t moe_decode_ffn_workspace(const moe_ffn_desc *desc /* host */);
+int moe_decode_ffn(const moe_ffn_desc *desc /* host */, const void *x, const int32_t *topk_ids,
+                   const float *topk_w, const uint8_t *route_mask, const void *w_gate,
+                   const void *w_up, const void *w_down, const void *s_gate, const void *s_up,
+                   const void *s_down, const float *shared, float *out, void *out_bf16,
+                   void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------------ residual addition and norm
  * The step ahead of the layer: the residual stream takes the previous
  * layer's output, and the layer gets its root-mean-square norm, in bf16 (for

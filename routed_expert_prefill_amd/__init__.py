@@ -16,7 +16,7 @@ from ._lib import (MOE_ACT_BF16, MOE_ACT_FP8_E4M3_ROW, MOE_W_BF16, MOE_W_FP8_E4M
                    MOE_W_MXFP4, LibraryNotBuilt, MoeFfnDesc)
 
 __all__ = [
-    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "MoEPrefill", "RouteTable",
+    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "decode_ffn", "MoEPrefill", "RouteTable",
     "ffn_desc", "ffn_plan", "ffn_gate_up", "ffn_down", "LibraryNotBuilt", "load_library",
 ]
 
@@ -407,12 +407,66 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, 
     return y, residual_out, q, s
 
 
+def decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_up, s_down,
+               shared=None, out=None, out_dtype=None, workspace=None):
+    """moe_decode_ffn: the routed experts of a few tokens (T * k at most
+    MOE_DECODE_MAX_ROUTES) with MXFP4 weights, straight from the ids.
+
+    out [T, d] is fp32 or bf16; if it is not given, it is made in out_dtype
+    (torch.float32 by default).  The other arguments are those of route_build,
+    grouped_ffn and combine_shared."""
+    torch = _torch()
+    lib = _lib.load()
+    dev = _on_current(x, "x")
+    if x.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 3:
+        raise ValueError("x must have 2 dims and w_gate 3")
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("topk_ids must have 2 dims")
+    T, d = x.shape
+    E, f, _ = w_gate.shape
+    k = topk_ids.shape[1]
+    if T == 0:
+        raise ValueError("x must have at least one row")
+    _need_rows(x, "x", (T, d), (torch.bfloat16,), dev)
+    _need_rows(topk_ids, "topk_ids", (T, k), (torch.int32,), dev)
+    _need_rows(topk_w, "topk_w", (T, k), (torch.float32,), dev)
+    if route_mask is not None:
+        _need_rows(route_mask, "route_mask", (T, k), (torch.uint8,), dev)
+    for name, t, shape in (("w_gate", w_gate, (E, f, d // 2)), ("w_up", w_up, (E, f, d // 2)),
+                           ("w_down", w_down, (E, d, f // 2)), ("s_gate", s_gate, (E, f, d // 32)),
+                           ("s_up", s_up, (E, f, d // 32)), ("s_down", s_down, (E, d, f // 32))):
+        _need_rows(t, name, shape, (torch.uint8,), dev)
+    if shared is not None:
+        _need_rows(shared, "shared", (T, d), (torch.float32,), dev)
+    if out is None:
+        out = torch.empty(T, d, dtype=out_dtype or torch.float32, device=dev)
+    _need_rows(out, "out", (T, d), (torch.float32, torch.bfloat16), dev)
+    desc = ctypes.byref(ffn_desc(T, k, E, d, f, weights="mxfp4"))
+    if workspace is None:
+        workspace = torch.empty(max(lib.moe_decode_ffn_workspace(desc), 256), dtype=torch.uint8,
+                                device=dev)
+    f32 = out.dtype == torch.float32
+    rc = lib.moe_decode_ffn(desc, x.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
+                            _ptr(route_mask), w_gate.data_ptr(), w_up.data_ptr(),
+                            w_down.data_ptr(), s_gate.data_ptr(), s_up.data_ptr(),
+                            s_down.data_ptr(), _ptr(shared), out.data_ptr() if f32 else None,
+                            None if f32 else out.data_ptr(), workspace.data_ptr(),
+                            workspace.numel(), _stream())
+    _lib.check(rc, "moe_decode_ffn")
+    return out
+
+
 class MoEPrefill:
     """The whole path -- route build, grouped FFN, combine -- with buffers kept
     across calls (nothing is allocated per call after construction).
 
     weights: "bf16", "fp8" or "mxfp4" (default: by fp8).  out_dtype:
-    torch.float32 (default) or torch.bfloat16."""
+    torch.float32 (default) or torch.bfloat16.  With MXFP4 weights and at most
+    DECODE_ROUTES routes a pass is decode_ffn (unless stage events are asked
+    for): self.rt and self.y are then not written."""
+
+    # at most this many routes go through decode_ffn
+    DECODE_ROUTES = 64
 
     def __init__(self, T: int, k: int, E: int, d: int, f: int, fp8: bool = False, device="cuda",
                  weights: Optional[str] = None, out_dtype=None):
@@ -442,6 +496,7 @@ class MoEPrefill:
         # the route build sends to the trailing bin -- add exact zeros, as
         # masked ones do.
         self.row_limit = self.rt.offsets[E:E + 1]
+        self.decode = self.weights == "mxfp4" and R <= self.DECODE_ROUTES
 
     def __call__(self, x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate=None,
                  s_up=None, s_down=None, stage_events=None, shared=None):
@@ -451,6 +506,9 @@ class MoEPrefill:
         6 -- before the route build and after each of route build, FFN plan,
         gate/up, down and combine."""
         ev = stage_events
+        if self.decode and ev is None:
+            return decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_up,
+                              s_down, shared=shared, out=self.out, workspace=self.ffn_ws)
         if ev is not None and len(ev) == 2:
             ev = [None, None, ev[0], ev[1], None, None]  # around ffn_gate_up
         if ev is not None and ev[0] is not None:

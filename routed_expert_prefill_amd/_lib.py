@@ -17,6 +17,7 @@ MOE_EWORKSPACE = -4
 MOE_EHIP = -5
 MOE_ETOOLARGE = -6
 MOE_ROUTE_NOALLOC_MAX_ROUTES = 1 << 20
+MOE_DECODE_MAX_ROUTES = 64
 
 MOE_W_BF16 = 0
 MOE_W_FP8_E4M3_B128 = 1
@@ -33,6 +34,7 @@ EXPORTED = [
     "moe_ffn_plan", "moe_ffn_gate_up", "moe_ffn_down",
     "moe_combine", "moe_quant_rows_fp8", "moe_route_topk", "moe_combine_shared",
     "moe_route_build_noalloc", "moe_add_rmsnorm",
+    "moe_decode_ffn_workspace", "moe_decode_ffn",
 ]
 
 
@@ -93,6 +95,10 @@ def load() -> ctypes.CDLL:
     lib.moe_add_rmsnorm.restype = i32
     lib.moe_add_rmsnorm.argtypes = [vp, i32, vp, vp, i32, vp, i32, ctypes.c_float, i32, i32, vp,
                                     vp, vp, vp]
+    lib.moe_decode_ffn_workspace.restype = sz
+    lib.moe_decode_ffn_workspace.argtypes = [dp]
+    lib.moe_decode_ffn.restype = i32
+    lib.moe_decode_ffn.argtypes = [dp] + [vp] * 14 + [sz, vp]
     _lib = lib
     return lib
 

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_prefill.so")
 
 HIP_SOURCES = ["route_topk.hip", "route_build.hip", "combine.hip", "quant.hip", "ffn_grouped.hip",
-               "ffn_fp8.hip", "norm.hip", "ffn_mxfp4.hip"]
+               "ffn_fp8.hip", "norm.hip", "ffn_mxfp4.hip", "decode_mxfp4.hip"]
 HOST_SOURCES = ["api.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

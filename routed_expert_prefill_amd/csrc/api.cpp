@@ -75,6 +75,16 @@ bool ffn_desc_status(const moe_ffn_desc *d, int *st) {
   return true;
 }
 
+// What moe_decode_ffn takes: MXFP4 weights and few routes.
+int decode_desc_status(const moe_ffn_desc *d) {
+  static_assert(MOE_DECODE_MAX_ROUTES == moe::kDecodeMaxRoutes, "one limit");
+  int st;
+  if (!ffn_desc_status(d, &st)) return st;
+  if (d->weight_dtype != MOE_W_MXFP4 || d->T * d->k > MOE_DECODE_MAX_ROUTES)
+    return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
 FfnLayout ffn_layout(const moe_ffn_desc *d) {
   const size_t R = (size_t)d->T * d->k;
   const bool fp8 = d->weight_dtype == MOE_W_FP8_E4M3_B128;
@@ -384,6 +394,50 @@ int moe_add_rmsnorm(const void *x, int x_dtype, const void *residual, void *resi
   a.w_f32 = weight_dtype == MOE_DT_F32;
   a.res_kind = !residual ? 0 : residual_dtype == MOE_DT_F32 ? 2 : 1;
   return status_from(moe::launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_decode_ffn_workspace(const moe_ffn_desc *desc) {
+  if (decode_desc_status(desc) != MOE_OK) return 0;
+  return align_up((size_t)desc->T * desc->k * desc->f * 2);
+}
+
+int moe_decode_ffn(const moe_ffn_desc *desc, const void *x, const int32_t *topk_ids,
+                   const float *topk_w, const uint8_t *route_mask, const void *w_gate,
+                   const void *w_up, const void *w_down, const void *s_gate, const void *s_up,
+                   const void *s_down, const float *shared, float *out, void *out_bf16,
+                   void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+  const int st = decode_desc_status(desc);
+  if (st != MOE_OK) return st;
+  if (!x || !topk_ids || !topk_w || !w_gate || !w_up || !w_down || !s_gate || !s_up || !s_down ||
+      (!out && !out_bf16))
+    return MOE_EINVAL;
+  const void *ptrs[] = {x,     topk_ids, topk_w, route_mask, w_gate, w_up,     w_down,
+                        s_gate, s_up,    s_down, shared,     out,    out_bf16, workspace};
+  for (const void *p : ptrs)
+    if (p && misaligned(p)) return MOE_EALIGN;
+  if (!workspace || workspace_bytes < moe_decode_ffn_workspace(desc)) return MOE_EWORKSPACE;
+  moe::DecodeArgs a{};
+  a.x = static_cast<const uint16_t *>(x);
+  a.ids = topk_ids;
+  a.w = topk_w;
+  a.mask = route_mask;
+  a.wg = static_cast<const uint8_t *>(w_gate);
+  a.wu = static_cast<const uint8_t *>(w_up);
+  a.wd = static_cast<const uint8_t *>(w_down);
+  a.sg = static_cast<const uint8_t *>(s_gate);
+  a.su = static_cast<const uint8_t *>(s_up);
+  a.sd = static_cast<const uint8_t *>(s_down);
+  a.shared = shared;
+  a.h = static_cast<uint16_t *>(workspace);
+  a.out = out;
+  a.out_bf16 = static_cast<uint16_t *>(out_bf16);
+  a.T = desc->T;
+  a.k = desc->k;
+  a.E = desc->E;
+  a.d = desc->d;
+  a.f = desc->f;
+  a.R = desc->T * desc->k;
+  return status_from(moe::launch_decode_mx4(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -115,6 +115,22 @@ struct FfnLaunchMx4 {
 };
 hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream);
 
+// Routed experts for single tokens, MXFP4 weights (decode_mxfp4.hip).
+constexpr int kDecodeMaxRoutes = 64;
+struct DecodeArgs {
+  const uint16_t *x;    // [T, d]
+  const int32_t *ids;   // [T, k]
+  const float *w;       // [T, k]
+  const uint8_t *mask;  // [T, k] or null
+  const uint8_t *wg, *wu, *wd, *sg, *su, *sd;
+  const float *shared;  // [T, d] or null
+  uint16_t *h;          // [T * k, f]
+  float *out;           // [T, d] or null
+  uint16_t *out_bf16;   // [T, d] or null
+  int T, k, E, d, f, R;
+};
+hipError_t launch_decode_mx4(const DecodeArgs &a, hipStream_t stream);
+
 // Per-row E4M3 quantisation of bf16 rows whose maxima are known: amax_bits[r]
 // holds the fp32 bits of max |x[r, :]|; same codes and scales as
 // launch_quant_rows.  rows_dev as there.

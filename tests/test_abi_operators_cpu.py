@@ -68,3 +68,28 @@ def test_mxfp4_ffn_errors(lib):
     d = ctypes.byref(_desc())
     assert lib.moe_ffn_gate_up(d, A, A, A, A, None, A, A, 1 << 40, None) == _lib.MOE_EINVAL
     assert lib.moe_ffn_down(d, A, A, None, A, A, 1 << 40, None) == _lib.MOE_EINVAL
+
+
+def test_decode_errors(lib):
+    def f(desc=None, ws=A, wsb=1 << 30, **kw):
+        names = ("x", "ids", "w", "mask", "wg", "wu", "wd", "sg", "su", "sd", "shared", "out",
+                 "out_bf16")
+        p = {**dict.fromkeys(names, A), "mask": 0, "shared": 0, "out_bf16": 0, **kw}
+        return lib.moe_decode_ffn(ctypes.byref(desc or _desc(T=2)), *[p[n] or None for n in names],
+                                  ws or None, wsb, None)
+
+    q = lambda **kw: lib.moe_decode_ffn_workspace(ctypes.byref(_desc(**kw)))  # noqa: E731
+    assert q(T=1) >= 6 * 256 * 2
+    assert q(T=16, k=4) > 0 and q(T=13, k=5) == 0  # 64 routes, 65
+    assert q(T=2, w=0) == 0 and q(T=2, w=1, a=1) == 0 and q(T=0) == 0
+    for n in ("x", "ids", "w", "wg", "wu", "wd", "sg", "su", "sd", "out"):
+        assert f(**{n: 0}) == _lib.MOE_EINVAL, n
+        assert f(**{n: A + 8}) == _lib.MOE_EALIGN, n
+    for n in ("mask", "shared", "out_bf16"):
+        assert f(**{n: A + 8}) == _lib.MOE_EALIGN, n
+    assert f(desc=_desc(T=11)) == _lib.MOE_EUNSUPPORTED  # 66 routes
+    assert f(desc=_desc(T=2, w=_lib.MOE_W_BF16)) == _lib.MOE_EUNSUPPORTED
+    assert f(desc=_desc(T=2, d=320)) == _lib.MOE_EUNSUPPORTED
+    assert f(desc=_desc(T=0)) == _lib.MOE_EINVAL
+    assert f(ws=0) == _lib.MOE_EWORKSPACE and f(wsb=1024) == _lib.MOE_EWORKSPACE
+    assert lib.moe_decode_ffn(None, *[A] * 14, 1 << 30, None) == _lib.MOE_EINVAL

@@ -47,6 +47,7 @@ def _run(p, y_fill=float("nan"), **kw):
 
     E, ids, w, mask, x, W = p
     run = rep.MoEPrefill(*ids.shape, E, x.shape[1], W["wg"].shape[1], weights="mxfp4")
+    run.decode = False  # the grouped path for few routes too
     if y_fill is not None:
         run.y.fill_(y_fill)
     out = run(bf16_dev(x), np_dev(ids), np_dev(w), np_dev(mask), *_dev(W), **kw)
@@ -140,6 +141,7 @@ def test_bf16_output_and_shared_rows():
     _, f32 = _run(p, shared=np_dev(shared))
     assert np.array_equal(f32, (plain.astype(np.float32) + shared).astype(np.float64))
     run = rep.MoEPrefill(T, k, E, 384, 256, weights="mxfp4", out_dtype=torch.bfloat16)
+    run.decode = False
     out = run(bf16_dev(x), np_dev(ids), np_dev(w), np_dev(mask), *_dev(W), shared=np_dev(shared))
     want = torch.from_numpy(f32.astype(np.float32)).to(torch.bfloat16)
     assert torch.equal(out.cpu().view(torch.int16), want.view(torch.int16))
