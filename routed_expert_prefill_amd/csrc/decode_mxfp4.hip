@@ -22,19 +22,31 @@
 
 namespace moe {
 
-constexpr int kDecSteps = 8;   // steps of 128 columns whose loads a wave has in flight
-constexpr int kDecRows = 4;    // activation rows a wave holds in LDS
-constexpr int kDecCols = kDecSteps * 128;
-constexpr int kDecRowBytes = kDecCols * 2 + 16;  // padded: rows start in different banks
-constexpr int kDecGuWaves = 4;   // gate/up: the waves split the reduction
-constexpr int kDecDnWaves = 16;  // down: the waves split experts and reduction
+constexpr int kDecRows = 4;     // activation rows a wave holds in LDS
+constexpr int kDecGuWaves = 4;  // gate/up: the waves split the reduction
+constexpr int kDecDnWaves = 8;  // down: the waves split the experts
+// steps of 128 columns whose loads a wave has in flight (with two weight
+// tiles per step in gate/up, one in down)
+constexpr int kDecGuSteps = 8;
+constexpr int kDecDnSteps = 16;
+
+// LDS of a wave for U steps and TW weight tiles: activation rows, then the
+// weight rows' scales; both padded so that consecutive rows start in
+// different banks.
+template <int TW, int U>
+struct DecLds {
+  static constexpr int kRow = U * 256 + 16;
+  static constexpr int kScales = U * 4 + 16;
+  static constexpr int kBytes = kDecRows * kRow + TW * 16 * kScales;
+};
 
 // The expert of route `lane`, or -1 if the route is not read.
 __device__ __forceinline__ int dec_key(const DecodeArgs &a, int lane) {
-  if (lane >= a.R) return -1;
-  if (a.mask != nullptr && a.mask[lane] == 0) return -1;
-  const int id = a.ids[lane];
-  return id >= 0 && id < a.E ? id : -1;
+  const int r = min(lane, a.R - 1);
+  const int id = a.ids[r];
+  int on = 1;
+  if (a.mask != nullptr) on = a.mask[r];
+  return lane < a.R && on != 0 && id >= 0 && id < a.E ? id : -1;
 }
 
 __device__ __forceinline__ int dec_first(uint64_t set) { return __builtin_ctzll(set); }
@@ -45,78 +57,144 @@ __device__ __forceinline__ uint64_t dec_readlane64(uint64_t v, int lane) {
   return ((uint64_t)hi << 32) | lo;
 }
 
-// One wave's products of TW weight tiles of 16 rows with up to kDecRows
-// activation rows over steps [s0, s1): lane l holds weight row l % 16 of tile
-// i at codes[i], scales[i] (row starts), activation row m starts at rows[m]
-// for m < n.  acc[i] register r of lane l: weight row 4 (l / 16) + r,
-// activation row l % 16 (repeated past n).
-template <int TW>
-__device__ __forceinline__ void dec_products(const uint8_t *const (&codes)[TW],
-                                             const uint8_t *const (&scales)[TW],
-                                             const uint16_t *const (&rows)[kDecRows], int n,
-                                             int s0, int s1, uint8_t *lds, f32x4 (&acc)[TW]) {
+// One wave's products of TW weight tiles of 16 rows with NR activation rows
+// over U steps from step s: lane l holds weight row l % 16 of tile i at
+// codes[i], scales[i] (row starts); activation row m starts at element
+// rows[m] of x.  acc[i] register r of lane l: weight row 4 (l / 16) + r,
+// activation row l % 16 (the last one again past NR).  lds: DecLds<TW, MU>
+// of this wave, U <= MU.  Straight-line code, with every load issued ahead of the
+// first wait: a branch between the steps lets the compiler sink each step's
+// loads to it.
+template <int TW, int MU, int NR, int U>
+__device__ __forceinline__ void dec_steps(const uint8_t *const (&codes)[TW],
+                                          const uint8_t *const (&scales)[TW], const uint16_t *x,
+                                          const uint32_t (&rows)[kDecRows], int s, uint8_t *lds,
+                                          f32x4 (&acc)[TW]) {
+  using L = DecLds<TW, MU>;
+  constexpr int XL = (U + 3) / 4;  // loads of 16 bytes per lane and activation row
+  constexpr int SL = (U + 3) / 4;  // loads of scales: 4 bytes per step and weight row
   const int lane = lane_id();
-  const int c = lane >> 4;
-  const uint8_t *mine = lds + min(lane & 15, n - 1) * kDecRowBytes + c * 64;
-  for (int s = s0; s < s1; s += kDecSteps) {
-    const int steps = min(kDecSteps, s1 - s);
-    // activation columns of these steps, 16 bytes per lane and load
-    i32x4 xv[kDecRows][2];
+  const int c = lane >> 4, row = lane & 15;
+  i32x4 xv[NR][XL];
 #pragma unroll
-    for (int m = 0; m < kDecRows; ++m) {
-      if (m >= n) break;
+  for (int m = 0; m < NR; ++m)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int piece = lane + 64 * i;
-        if (piece < steps * 16)
-          xv[m][i] = *reinterpret_cast<const i32x4 *>(rows[m] + (size_t)s * 128 + piece * 8);
-      }
-    }
-    // all weight loads; steps past the end load the last one again
-    i32x4 raw[kDecSteps][TW];
-    uint32_t sc[kDecSteps][TW];
+    for (int i = 0; i < XL; ++i)
+      xv[m][i] = *reinterpret_cast<const i32x4 *>(x + rows[m] + (size_t)s * 128 +
+                                                  min(lane + 64 * i, U * 16 - 1) * 8);
+  uint32_t sc[TW][SL];  // lane group c takes steps c, 4 + c, ..
 #pragma unroll
-    for (int i = 0; i < kDecSteps; ++i) {
-      const size_t at = (size_t)min(s + i, s1 - 1);
+  for (int w = 0; w < TW; ++w)
 #pragma unroll
-      for (int w = 0; w < TW; ++w) {
-        raw[i][w] = *reinterpret_cast<const i32x4 *>(codes[w] + at * 64 + c * 16);
-        sc[i][w] = *reinterpret_cast<const uint32_t *>(scales[w] + at * 4);
-      }
-    }
+    for (int i = 0; i < SL; ++i)
+      sc[w][i] = *reinterpret_cast<const uint32_t *>(scales[w] +
+                                                     (size_t)(s + min(4 * i + c, U - 1)) * 4);
+  i32x4 raw[U][TW];
 #pragma unroll
-    for (int m = 0; m < kDecRows; ++m) {
-      if (m >= n) break;
+  for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int piece = lane + 64 * i;
-        if (piece < steps * 16)
-          *reinterpret_cast<i32x4 *>(lds + m * kDecRowBytes + piece * 16) = xv[m][i];
-      }
-    }
+    for (int w = 0; w < TW; ++w)
+      raw[i][w] = *reinterpret_cast<const i32x4 *>(codes[w] + (size_t)(s + i) * 64 + c * 16);
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < kDecSteps; ++i) {
-      if (i >= steps) break;
-      bf16x8 fx[4];
+  for (int m = 0; m < NR; ++m)
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      *reinterpret_cast<i32x4 *>(lds + m * L::kRow + (lane + 64 * i) * 16) = xv[m][i];
+  uint8_t *sc_lds = lds + kDecRows * L::kRow + row * L::kScales;
+#pragma unroll
+  for (int w = 0; w < TW; ++w)
+#pragma unroll
+    for (int i = 0; i < SL; ++i)
+      *reinterpret_cast<uint32_t *>(sc_lds + w * 16 * L::kScales + (4 * i + c) * 4) = sc[w][i];
+  i32x4 ss[TW][SL];
+#pragma unroll
+  for (int w = 0; w < TW; ++w)
+#pragma unroll
+    for (int i = 0; i < SL; ++i)
+      ss[w][i] = *reinterpret_cast<const i32x4 *>(sc_lds + w * 16 * L::kScales + 16 * i);
+  const uint8_t *mine = lds + min(row, NR - 1) * L::kRow + c * 64;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    bf16x8 fx[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      fx[j] = *reinterpret_cast<const bf16x8 *>(mine + i * 256 + j * 16);
+#pragma unroll
+    for (int w = 0; w < TW; ++w) {
+      const float scale = mx4_scale(((uint32_t)ss[w][i >> 2][i & 3] >> (8 * c)) & 0xffu);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        fx[j] = *reinterpret_cast<const bf16x8 *>(mine + i * 256 + j * 16);
-#pragma unroll
-      for (int w = 0; w < TW; ++w) {
-        const float scale = mx4_scale((sc[i][w] >> (8 * c)) & 0xffu);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[w] = mfma_bf16(mx4_decode8((uint32_t)raw[i][w][j], scale), fx[j], acc[w]);
-      }
+        acc[w] = mfma_bf16(mx4_decode8((uint32_t)raw[i][w][j], scale), fx[j], acc[w]);
     }
   }
+}
+
+// The same over steps [s0, s1).
+template <int TW, int MU, int NR>
+__device__ __forceinline__ void dec_products_n(const uint8_t *const (&codes)[TW],
+                                               const uint8_t *const (&scales)[TW],
+                                               const uint16_t *x, const uint32_t (&rows)[kDecRows],
+                                               int s0, int s1, uint8_t *lds, f32x4 (&acc)[TW]) {
+  // several rows' activations take the registers of some of the steps
+  constexpr int U = NR == 1 ? MU : 4;
+  int s = s0;
+  for (; s + U <= s1; s += U) dec_steps<TW, MU, NR, U>(codes, scales, x, rows, s, lds, acc);
+  if constexpr (U > 8) {
+    if (s + 8 <= s1) {
+      dec_steps<TW, MU, NR, 8>(codes, scales, x, rows, s, lds, acc);
+      s += 8;
+    }
+  }
+  if constexpr (U > 4) {
+    if (s + 4 <= s1) {
+      dec_steps<TW, MU, NR, 4>(codes, scales, x, rows, s, lds, acc);
+      s += 4;
+    }
+  }
+  if (s + 2 <= s1) {
+    dec_steps<TW, MU, NR, 2>(codes, scales, x, rows, s, lds, acc);
+    s += 2;
+  }
+  if (s < s1) dec_steps<TW, MU, NR, 1>(codes, scales, x, rows, s, lds, acc);
+}
+
+// The same for n = 1 .. kDecRows activation rows; rows past n repeat one.
+// A row's sums do not depend on n: the steps are taken in one order.
+template <int TW, int MU>
+__device__ __forceinline__ void dec_products(const uint8_t *const (&codes)[TW],
+                                             const uint8_t *const (&scales)[TW], const uint16_t *x,
+                                             const uint32_t (&rows)[kDecRows], int n, int s0,
+                                             int s1, uint8_t *lds, f32x4 (&acc)[TW]) {
+  if (n == 1)
+    dec_products_n<TW, MU, 1>(codes, scales, x, rows, s0, s1, lds, acc);
+  else
+    dec_products_n<TW, MU, kDecRows>(codes, scales, x, rows, s0, s1, lds, acc);
+}
+
+// The next activation rows of an expert's routes `set`, which loses them:
+// route[m], and the rows' starts (elements) in [.., width] rows indexed by
+// route / per.  Past n they repeat the first.
+__device__ __forceinline__ int dec_next_rows(uint64_t &set, int per, int width,
+                                             int (&route)[kDecRows], uint32_t (&rows)[kDecRows]) {
+  int n = 0;
+#pragma unroll
+  for (int m = 0; m < kDecRows; ++m) {
+    route[m] = route[0];
+    if (m == 0 || set) {
+      route[m] = dec_first(set);
+      set &= set - 1;
+      ++n;
+    }
+    rows[m] = (uint32_t)(route[m] / per) * (uint32_t)width;
+  }
+  return n;
 }
 
 // h[r, n0 .. n0 + 15] for every route r of one expert.  Workgroup (b, r): 16
 // features of the expert of route r, if r is the first route with it.
 __global__ __launch_bounds__(kDecGuWaves *kWave) void decode_gate_up_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t xs[kDecGuWaves][kDecRows * kDecRowBytes];
-  __shared__ f32x4 part[kDecGuWaves][2][kWave];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kDecGuWaves][DecLds<2, kDecGuSteps>::kBytes];
   const int lane = lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n0 = blockIdx.x * 16, r0 = blockIdx.y;
@@ -131,110 +209,91 @@ __global__ __launch_bounds__(kDecGuWaves *kWave) void decode_gate_up_kernel(Deco
   const uint8_t *codes[2] = {a.wg + row * (a.d / 2), a.wu + row * (a.d / 2)};
   const uint8_t *scales[2] = {a.sg + row * (a.d / 32), a.su + row * (a.d / 32)};
   while (set) {
-    // the next rows of this expert
-    const uint16_t *rows[kDecRows];
-    int route[kDecRows], n = 0;
-#pragma unroll
-    for (int m = 0; m < kDecRows; ++m) {
-      route[m] = 0;
-      rows[m] = a.x;
-      if (set) {
-        route[m] = dec_first(set);
-        rows[m] = a.x + (size_t)(route[m] / a.k) * a.d;
-        set &= set - 1;
-        ++n;
-      }
-    }
+    int route[kDecRows];
+    uint32_t rows[kDecRows];
+    const int n = dec_next_rows(set, a.k, a.d, route, rows);
     f32x4 acc[2] = {};
-    dec_products<2>(codes, scales, rows, n, s0, s1, xs[wv], acc);
-    part[wv][0][lane] = acc[0];
-    part[wv][1][lane] = acc[1];
+    dec_products<2, kDecGuSteps>(codes, scales, a.x, rows, n, s0, s1, lds[wv], acc);
+    // the waves' parts of the sums, where their activation rows were
+    f32x4 *part = reinterpret_cast<f32x4 *>(lds[wv]);
+    part[lane] = acc[0];
+    part[kWave + lane] = acc[1];
     __syncthreads();
-    // thread (wave g, lane l): the four features 4 (l / 16) .. + 3 of wave 0's
-    // layout, feature g of them, row l % 16
+    // wave g, lane l: feature 4 (l / 16) + g of activation row l % 16
     float g = 0.0f, u = 0.0f;
 #pragma unroll
     for (int w = 0; w < kDecGuWaves; ++w) {
-      g += part[w][0][lane][wv];
-      u += part[w][1][lane][wv];
+      const float *p = reinterpret_cast<const float *>(lds[w]) + lane * 4 + wv;
+      g += p[0];
+      u += p[kWave * 4];
     }
     const int m = lane & 15;
     if (m < n) {
       const int r = m == 0 ? route[0] : m == 1 ? route[1] : m == 2 ? route[2] : route[3];
       a.h[(size_t)r * a.f + n0 + 4 * (lane >> 4) + wv] = f32_to_bf16_bits(swiglu(g, u));
     }
-    __syncthreads();  // part is written again
+    __syncthreads();  // the parts make room for the next rows
   }
 }
 static_assert(kDecGuWaves == 4 && kDecRows == 4, "the epilogue's mapping");
 
-// out[t, n0 .. n0 + 15] for every token t.
+// out[t, n0 .. n0 + 15] for every token t: the experts go round the waves,
+// and the routes' sums meet in LDS.
 __global__ __launch_bounds__(kDecDnWaves *kWave) void decode_down_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t hs[kDecDnWaves][kDecRows * kDecRowBytes];
-  __shared__ f32x4 ys[2][kDecodeMaxRoutes][4];  // [half of the reduction][route][feature]
+  __shared__ __attribute__((aligned(16))) uint8_t
+      lds[kDecDnWaves][DecLds<1, kDecDnSteps>::kBytes];
+  __shared__ f32x4 ys[kDecodeMaxRoutes][4];  // [route][feature]
   __shared__ int read[kDecodeMaxRoutes];
+  __shared__ float gate[kDecodeMaxRoutes];
   const int lane = lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n0 = blockIdx.x * 16;
   const int key = dec_key(a, lane);
-  if (wv == 0) read[lane] = key >= 0;
+  if (wv == 0) {  // for the combine, whose loads would otherwise wait in a row
+    read[lane] = key >= 0;
+    gate[lane] = a.w[min(lane, a.R - 1)];
+  }
   uint64_t same = 0;  // the routes with this lane's expert
   for (int r = 0; r < a.R; ++r) {
     const uint64_t b = __ballot(key == __builtin_amdgcn_readlane(key, r));
     if (lane == r) same = b;
   }
   uint64_t lead = __ballot(key >= 0 && dec_first(same) == lane);
-  const int steps = a.f / 128, per = (steps + 1) / 2;
-  int turn = 0;  // units (an expert, a half of the reduction) go round the waves
-  while (lead) {
+  const int steps = a.f / 128;
+  for (int turn = 0; lead; ++turn) {
     const int r0 = dec_first(lead);
     lead &= lead - 1;
-    const int e = __builtin_amdgcn_readlane(key, r0);
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      if ((turn++ & (kDecDnWaves - 1)) != wv) continue;
-      const int s0 = half ? per : 0, s1 = half ? steps : per;
-      const size_t row = (size_t)e * a.d + n0 + (lane & 15);
-      const uint8_t *codes[1] = {a.wd + row * (a.f / 2)};
-      const uint8_t *scales[1] = {a.sd + row * (a.f / 32)};
-      uint64_t set = dec_readlane64(same, r0);
-      while (set) {
-        const uint16_t *rows[kDecRows];
-        int route[kDecRows], n = 0;
-#pragma unroll
-        for (int m = 0; m < kDecRows; ++m) {
-          route[m] = 0;
-          rows[m] = a.h;
-          if (set) {
-            route[m] = dec_first(set);
-            rows[m] = a.h + (size_t)route[m] * a.f;
-            set &= set - 1;
-            ++n;
-          }
-        }
-        f32x4 acc[1] = {};
-        dec_products<1>(codes, scales, rows, n, s0, s1, hs[wv], acc);
-        const int m = lane & 15;
-        if (m < n) {
-          const int r = m == 0 ? route[0] : m == 1 ? route[1] : m == 2 ? route[2] : route[3];
-          ys[half][r][lane >> 4] = acc[0];
-        }
+    if ((turn & (kDecDnWaves - 1)) != wv) continue;
+    const size_t row = (size_t)__builtin_amdgcn_readlane(key, r0) * a.d + n0 + (lane & 15);
+    const uint8_t *codes[1] = {a.wd + row * (a.f / 2)};
+    const uint8_t *scales[1] = {a.sd + row * (a.f / 32)};
+    uint64_t set = dec_readlane64(same, r0);
+    while (set) {
+      int route[kDecRows];
+      uint32_t rows[kDecRows];
+      const int n = dec_next_rows(set, 1, a.f, route, rows);
+      f32x4 acc[1] = {};
+      dec_products<1, kDecDnSteps>(codes, scales, a.h, rows, n, 0, steps, lds[wv], acc);
+      const int m = lane & 15;
+      if (m < n) {
+        const int r = m == 0 ? route[0] : m == 1 ? route[1] : m == 2 ? route[2] : route[3];
+        ys[r][lane >> 4] = acc[0];
       }
     }
   }
   __syncthreads();
   // the combine: routes of a token in ascending order from +0.0
-  const int t = threadIdx.x >> 4, i = threadIdx.x & 15;
-  if (t >= a.T) return;
-  float sum = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int r = t * a.k + j;
-    if (read[r]) sum = __builtin_fmaf(a.w[r], ys[0][r][i >> 2][i & 3] + ys[1][r][i >> 2][i & 3], sum);
+  for (int o = threadIdx.x; o < a.T * 16; o += kDecDnWaves * kWave) {
+    const int t = o >> 4, i = o & 15;
+    const size_t at = (size_t)t * a.d + n0 + i;
+    float sum = 0.0f, sh = 0.0f;
+    if (a.shared) sh = a.shared[at];
+    for (int r = t * a.k; r < (t + 1) * a.k; ++r)
+      if (read[r]) sum = __builtin_fmaf(gate[r], ys[r][i >> 2][i & 3], sum);
+    if (a.shared) sum += sh;
+    if (a.out) a.out[at] = sum;
+    if (a.out_bf16) a.out_bf16[at] = f32_to_bf16_bits(sum);
   }
-  const size_t o = (size_t)t * a.d + n0 + i;
-  if (a.shared) sum += a.shared[o];
-  if (a.out) a.out[o] = sum;
-  if (a.out_bf16) a.out_bf16[o] = f32_to_bf16_bits(sum);
 }
 
 hipError_t launch_decode_mx4(const DecodeArgs &a, hipStream_t stream) {
