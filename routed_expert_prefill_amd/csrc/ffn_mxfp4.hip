@@ -42,15 +42,18 @@ constexpr int kM4Threads = 512;
 constexpr int kM4Waves = kM4Threads / kWave;
 constexpr int kM4Ring = 160 * 1024;  // the whole LDS of a workgroup
 
-// Geometry of an item with 32 * AB activation rows, WR weight rows and KB
+// Geometry of an item with AR activation rows, WR weight rows and KB
 // 64-column blocks per stage.
-template <int AB, int WR, int KB>
+template <int AR, int WR, int KB>
 struct M4Ring {
-  static constexpr int kAct = 32 * AB * 128 * KB;
+  static constexpr int kAct = AR * 128 * KB;
   static constexpr int kCodes = WR * 32 * KB;
   static constexpr int kScaleRow = KB == 4 ? 8 : 4;  // bytes of scales per weight row
   static constexpr int kSlot = kAct + kCodes + WR * kScaleRow;
-  static constexpr int kDepth = (kM4Ring / kSlot) < 8 ? (kM4Ring / kSlot) : 8;
+  // tiles of at most 32 rows: waves 4-7 hand their sums to waves 0-3 behind the ring
+  static constexpr int kSums = AR <= 32 ? 4 * 4096 : 0;
+  static constexpr int kFit = (kM4Ring - kSums) / kSlot;
+  static constexpr int kDepth = kFit < 8 ? kFit : 8;
 };
 
 // 16-byte chunk c of the codes of weight row r is stored at this slot of the
@@ -70,44 +73,51 @@ __device__ __forceinline__ void dma4(const void *src, uint32_t lds_byte_addr) {
                : "memory");
 }
 
-// Wave wv multiplies TT activation tiles by TW weight tiles of 32 rows.
-template <int AB, int WR>
+// Wave wv multiplies TT activation tiles by TW weight tiles of 32 rows.  With
+// at most 32 activation rows (and 128 weight rows) four waves would do, so
+// the other four take the second half of each stage's columns.
+template <int AR>
 struct M4Layout {
-  static constexpr int TT = AB == 1 ? 1 : AB / 2;
-  static constexpr int TW = AB == 1 ? 1 : 2;
-  __device__ static bool active(int wv) { return AB > 1 || wv < WR / 32; }
-  __device__ static int atile(int wv, int tt) { return AB == 1 ? 0 : (wv >> 2) * TT + tt; }
-  __device__ static int wtile(int wv, int tw) { return AB == 1 ? wv : (wv & 3) * 2 + tw; }
+  static constexpr bool kSplit = AR <= 32;
+  static constexpr int TT = kSplit ? 1 : AR / 64;
+  static constexpr int TW = kSplit ? 1 : 2;
+  __device__ static int atile(int wv, int tt) { return kSplit ? 0 : (wv >> 2) * TT + tt; }
+  __device__ static int wtile(int wv, int tw) { return kSplit ? (wv & 3) : (wv & 3) * 2 + tw; }
 };
 
 __device__ __forceinline__ f32x4 m4_quad(const f32x16 &v, int g) {
   return f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
 }
 
+// nb feature blocks of one tile, streamed through one ring fill.
 // NT: codes through non-temporal loads (whole lines only: KB == 4).
-template <bool GATEUP, bool NT, int AB, int WR, int KB>
-__device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0, uint8_t *ring,
-                                        uint32_t ring_lds) {
+template <bool GATEUP, bool NT, int AR, int WR, int KB>
+__device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0, int nb_arg,
+                                        uint8_t *ring, uint32_t ring_lds) {
   static_assert(!NT || KB == 4, "half lines must not bypass the caches");
-  static_assert(AB == 1 || WR == 256, "taller tiles take 256 weight rows");
-  using L = M4Layout<AB, WR>;
-  using G = M4Ring<AB, WR, KB>;
+  using L = M4Layout<AR>;
+  using G = M4Ring<AR, WR, KB>;
+  static_assert(L::kSplit ? WR == 128 && KB == 4 : WR == 256 && AR % 64 == 0, "wave layout");
+  constexpr bool MB = L::kSplit;  // several blocks only where items are short
+  constexpr int FEAT = GATEUP ? WR / 2 : WR;  // output features per block
   constexpr int TT = L::TT, TW = L::TW;
-  constexpr int NA = KB * 4 * AB;      // activation loads: 8 rows of 128 bytes
+  constexpr int NA = KB * AR / 8;      // activation loads: 8 rows of 128 bytes
   constexpr int NW = WR * KB / 32;     // code loads: 1 KB
   constexpr int NC = G::kScaleRow * WR / 256;  // scale loads: 256 bytes
-  // load i of a kind goes to wave i % 8: JA + JW loads of every wave and one
-  // load of scales of the first NC waves per stage
-  static_assert(NA % kM4Waves == 0 && NW % kM4Waves == 0 && NC <= kM4Waves, "even shares");
-  constexpr int JA = NA / kM4Waves, JW = NW / kM4Waves;
+  // load i of a kind goes to wave i % 8, the loads of scales to the last NC waves
+  static_assert((NA % kM4Waves == 0 || NA < kM4Waves) && NW % kM4Waves == 0 && NC <= kM4Waves,
+                "shares");
+  constexpr int JA = (NA + kM4Waves - 1) / kM4Waves, JW = NW / kM4Waves;
   constexpr int NS = G::kDepth;
   static_assert(NS >= 2 && (JA + JW + 1) * (NS - 2) <= 32, "wait_vm counts to 32");
+  const int nb = MB ? nb_arg : 1;
   const int lane = lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int K = a.K;
   const int nst = (K / 64 + KB - 1) / KB;
   const bool half = KB == 4 && (K & 128) != 0;  // the last stage has two blocks only
-  const int cnt = JA + JW + (wv < NC ? 1 : 0);  // loads this wave issues per stage
+  const bool has_act = NA % kM4Waves == 0 || wv < NA, has_scales = wv >= kM4Waves - NC;
+  const int cnt = JW + (has_act ? JA : 0) + (has_scales ? 1 : 0);  // loads of this wave per stage
 
   auto wrow = [&](int wr, const uint8_t *p0, const uint8_t *p1, int row_bytes) {
     const uint8_t *w = p0;
@@ -126,8 +136,8 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
 #pragma unroll
   for (int j = 0; j < JA; ++j) {
     const int i = wv + kM4Waves * j;
-    const int kb = i / (4 * AB);
-    const int r = (i - kb * 4 * AB) * 8 + (lane >> 3);
+    const int kb = i / (AR / 8);
+    const int r = (i - kb * (AR / 8)) * 8 + (lane >> 3);
     const int row = t.row0 + min(r, t.nrows - 1);
     const size_t s = GATEUP ? (size_t)(a.sorted_routes[row] / a.k) : (size_t)row;
     act[j] = reinterpret_cast<const uint8_t *>(a.act + s * K) + kb * 128 +
@@ -144,17 +154,22 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   }
   {
     constexpr int SPR = G::kScaleRow / 4;  // lanes per row of scales
-    scales = wrow(min(wv, NC - 1) * (64 / SPR) + lane / SPR, a.s0, a.s1, K / 32) + (lane % SPR) * 4;
+    const int i = max(wv - (kM4Waves - NC), 0);
+    scales = wrow(i * (64 / SPR) + lane / SPR, a.s0, a.s1, K / 32) + (lane % SPR) * 4;
   }
-  auto issue = [&](int s, int slot) {
+  // loads of stage s of block b
+  auto issue = [&](int s, int b, int slot) {
     const uint32_t base = ring_lds + (uint32_t)(slot * G::kSlot) + (uint32_t)wv * 1024u;
     const bool cut = half && s == nst - 1;
-    const uint32_t act_off = (uint32_t)s * (128 * KB), code_off = (uint32_t)s * (32 * KB);
+    const uint32_t act_off = (uint32_t)s * (128 * KB);
+    const uint32_t code_off = (uint32_t)s * (32 * KB) + (MB ? (uint32_t)(b * FEAT) * (K / 2) : 0);
+    if (has_act) {
 #pragma unroll
-    for (int j = 0; j < JA; ++j) {
-      const uint8_t *p = act[j] + act_off;
-      if (KB == 4 && cut && (wv + kM4Waves * j) / (4 * AB) >= 2) p -= 256;
-      dma16(p, base + (uint32_t)j * (kM4Waves * 1024u));
+      for (int j = 0; j < JA; ++j) {
+        const uint8_t *p = act[j] + act_off;
+        if (KB == 4 && cut && (wv + kM4Waves * j) / (AR / 8) >= 2) p -= 256;
+        dma16(p, base + (uint32_t)j * (kM4Waves * 1024u));
+      }
     }
 #pragma unroll
     for (int j = 0; j < JW; ++j) {
@@ -166,41 +181,42 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
       else
         dma16(p, to);
     }
-    if (wv < NC) {
+    if (has_scales) {
       // two scales per block; KB == 1 loads the aligned four that hold them
-      const uint8_t *p = scales + (KB == 1 ? (s >> 1) * 4 : s * (2 * KB));
+      const uint8_t *p = scales + (KB == 1 ? (s >> 1) * 4 : s * (2 * KB)) +
+                         (MB ? (uint32_t)(b * FEAT) * (K / 32) : 0);
       if (KB == 4 && cut) p -= (lane & 1) * 4;
-      dma4(p, ring_lds + (uint32_t)(slot * G::kSlot + G::kAct + G::kCodes) + (uint32_t)wv * 256u);
+      dma4(p, ring_lds + (uint32_t)(slot * G::kSlot + G::kAct + G::kCodes) +
+                  (uint32_t)(wv - (kM4Waves - NC)) * 256u);
     }
   };
 
   const int rr = lane & 31, rh = lane >> 5;
   f32x16 acc[TW][TT];
+  auto zero_acc = [&]() {
 #pragma unroll
-  for (int tw = 0; tw < TW; ++tw)
+    for (int tw = 0; tw < TW; ++tw)
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
+      for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) acc[tw][tt][j] = 0.f;
+        for (int j = 0; j < 16; ++j) acc[tw][tt][j] = 0.f;
+  };
 
+  // the MFMAs of one ring stage
   auto mma_stage = [&](const uint8_t *buf, int s) {
-    if (!L::active(wv)) return;
-    uint32_t sc[TW][KB == 4 ? 2 : 1];
+    static_assert(L::kSplit || KB <= 2, "one word of scales per wave and stage");
+    uint32_t sc[TW];
 #pragma unroll
     for (int tw = 0; tw < TW; ++tw) {
       const uint8_t *p = buf + G::kAct + G::kCodes + (L::wtile(wv, tw) * 32 + rr) * G::kScaleRow;
-      if constexpr (KB == 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        sc[tw][0] = v.x >> (8 * rh);
-        sc[tw][1] = v.y >> (8 * rh);
-      } else {
-        sc[tw][0] = *reinterpret_cast<const uint32_t *>(p) >> (8 * rh + (KB == 1 ? 16 * (s & 1) : 0));
-      }
+      if (L::kSplit) p += (wv >> 2) * 4;
+      sc[tw] = *reinterpret_cast<const uint32_t *>(p) >> (8 * rh + (KB == 1 ? 16 * (s & 1) : 0));
     }
-    const int blocks = half && s == nst - 1 ? 2 : KB;
+    if (L::kSplit && wv >= 4 && half && s == nst - 1) return;  // no second half there
+    constexpr int KW = L::kSplit ? KB / 2 : KB;  // blocks of this wave
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      if (kb >= blocks) break;
+    for (int q = 0; q < KW; ++q) {
+      const int kb = L::kSplit ? (wv >> 2) * 2 + q : q;
       i32x4 raw[TW];
       float scale[TW];
 #pragma unroll
@@ -208,16 +224,16 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
         const int r = L::wtile(wv, tw) * 32 + rr;
         raw[tw] = *reinterpret_cast<const i32x4 *>(buf + G::kAct + r * (32 * KB) +
                                                    m4_slot<KB>(r, 2 * kb + rh) * 16);
-        scale[tw] = mx4_scale((sc[tw][kb >> 1] >> (16 * (kb & 1))) & 0xffu);
+        scale[tw] = mx4_scale((sc[tw] >> (16 * (q & 1))) & 0xffu);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         bf16x8 fa[TT];
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
-          const int r = L::atile(wv, tt) * 32 + rr;
-          fa[tt] = *reinterpret_cast<const bf16x8 *>(buf + kb * (32 * AB * 128) + r * 128 +
-                                                     ring_slot(rr, 4 * rh + j) * 16);
+          const int r = (L::atile(wv, tt) * 32 + rr) & (AR < 32 ? AR - 1 : -1);
+          fa[tt] = *reinterpret_cast<const bf16x8 *>(buf + kb * (AR * 128) + r * 128 +
+                                                     ring_slot(r, 4 * rh + j) * 16);
         }
 #pragma unroll
         for (int tw = 0; tw < TW; ++tw) {
@@ -229,55 +245,91 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     }
   };
 
-  wait_vm(0);
-  ring_barrier();  // every wave is done with the ring contents of the previous item
+  // results of the block at feature nb0
+  auto epilogue = [&](int nb0) {
+    if constexpr (L::kSplit) {
+      f32x4 *sums = reinterpret_cast<f32x4 *>(ring + kM4Ring - G::kSums) + (wv & 3) * 256 + lane;
+      if (wv >= 4) {
 #pragma unroll
-  for (int s = 0; s < NS - 1; ++s)
-    if (s < nst) issue(s, s);
-  int slot = 0;
-  for (int s = 0; s < nst; ++s) {
-    // this wave's loads of stage s are done; later stages may stay in flight
-    wait_vm(cnt * min(NS - 2, nst - 1 - s));
-    ring_barrier();  // stage s is in LDS for everyone; stage s - 1 is consumed
-    const int ahead = s + NS - 1;
-    if (ahead < nst) issue(ahead, slot == 0 ? NS - 1 : slot - 1);
-    mma_stage(ring + slot * G::kSlot, s);
-    slot = slot == NS - 1 ? 0 : slot + 1;
-  }
-  if (!L::active(wv)) return;
-  // register j of a 32x32 tile holds weight row 8*(j/4) + 4*rh + j%4, activation row rr
+        for (int g = 0; g < 4; ++g) sums[g * 64] = m4_quad(acc[0][0], g);
+      }
+      // the sums are written; the next ones are a barrier of every stage away
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      ring_barrier();
+      if (wv >= 4) return;
 #pragma unroll
-  for (int tt = 0; tt < TT; ++tt) {
-    const int r = L::atile(wv, tt) * 32 + rr;
-    if (r >= t.nrows) continue;
-    const size_t row = (size_t)(t.row0 + r);
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 v = sums[g * 64];
 #pragma unroll
-    for (int tw = 0; tw < TW; ++tw) {
-      const int wt = L::wtile(wv, tw);
-      if (GATEUP) {
-        // rows 0-15 of the tile are gate features 16 wt + [0,16), rows 16-31 the same up features
+        for (int i = 0; i < 4; ++i) acc[0][0][4 * g + i] += v[i];
+      }
+    }
+    // register j of a 32x32 tile holds weight row 8*(j/4) + 4*rh + j%4, activation row rr
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const f32x4 gv = m4_quad(acc[tw][tt], g), uv = m4_quad(acc[tw][tt], g + 2);
-          const int n = n0 + wt * 16 + g * 8 + rh * 4;
-          uint2 v;
-          v.x = (uint32_t)f32_to_bf16_bits(swiglu(gv[0], uv[0])) |
-                ((uint32_t)f32_to_bf16_bits(swiglu(gv[1], uv[1])) << 16);
-          v.y = (uint32_t)f32_to_bf16_bits(swiglu(gv[2], uv[2])) |
-                ((uint32_t)f32_to_bf16_bits(swiglu(gv[3], uv[3])) << 16);
-          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.N + n) = v;
-        }
-      } else {
+    for (int tt = 0; tt < TT; ++tt) {
+      const int r = L::atile(wv, tt) * 32 + rr;
+      if (r >= t.nrows) continue;
+      const size_t row = (size_t)(t.row0 + r);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int n = n0 + wt * 32 + g * 8 + rh * 4;
-          if (n < a.N)
-            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + row * a.N + n) =
-                m4_quad(acc[tw][tt], g);
+      for (int tw = 0; tw < TW; ++tw) {
+        const int wt = L::wtile(wv, tw);
+        if (GATEUP) {
+          // rows 0-15 of the tile are gate features 16 wt + [0,16), rows 16-31 the same up features
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const f32x4 gv = m4_quad(acc[tw][tt], g), uv = m4_quad(acc[tw][tt], g + 2);
+            const int n = nb0 + wt * 16 + g * 8 + rh * 4;
+            uint2 v;
+            v.x = (uint32_t)f32_to_bf16_bits(swiglu(gv[0], uv[0])) |
+                  ((uint32_t)f32_to_bf16_bits(swiglu(gv[1], uv[1])) << 16);
+            v.y = (uint32_t)f32_to_bf16_bits(swiglu(gv[2], uv[2])) |
+                  ((uint32_t)f32_to_bf16_bits(swiglu(gv[3], uv[3])) << 16);
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.N + n) = v;
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int n = nb0 + wt * 32 + g * 8 + rh * 4;
+            if (n < a.N)
+              *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + row * a.N + n) =
+                  m4_quad(acc[tw][tt], g);
+          }
         }
       }
     }
+  };
+
+  zero_acc();
+  wait_vm(0);
+  ring_barrier();  // every wave is done with the ring contents of the previous item
+  const int total = MB ? nb * nst : nst;
+  int is = 0, ib = 0;  // stage and block of the next stage to load
+  auto issue_next = [&](int slot) {
+    issue(is, ib, slot);
+    if (++is == nst && MB) {
+      is = 0;
+      ++ib;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s)
+    if (s < total) issue_next(s);
+  int slot = 0, cs = 0, cb = 0;  // stage and block being multiplied
+  for (int s = 0; s < total; ++s) {
+    // this wave's loads of stage s are done; later stages may stay in flight
+    // (stores of an earlier block, counted too, only make the wait longer)
+    wait_vm(cnt * min(NS - 2, total - 1 - s));
+    ring_barrier();  // stage s is in LDS for everyone; stage s - 1 is consumed
+    if (s + NS - 1 < total) issue_next(slot == 0 ? NS - 1 : slot - 1);
+    mma_stage(ring + slot * G::kSlot, MB ? cs : s);
+    slot = slot == NS - 1 ? 0 : slot + 1;
+    if (MB && ++cs == nst) {
+      epilogue(n0 + cb * FEAT);
+      cs = 0;
+      if (++cb < nb) zero_acc();
+    }
   }
+  if (!MB) epilogue(n0);
 }
 
 // A pointer through two words of LDS.
@@ -306,22 +358,36 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
   constexpr int kHalf = GATEUP ? 2 : 1;  // gate and up rows of one feature
   constexpr int FB = kM4WRows / kHalf, FS = kM4WRowsSmall / kHalf;  // features per item
   const int N = vreg(a.N);
+  const int grid = vreg((int)gridDim.x);
   const int nsmall = vreg(*a.n_small), nbig = vreg(*a.ntiles) - nsmall;
-  const int ptb = (N + FB - 1) / FB, pts = (N + FS - 1) / FS;
-  const int items_big = nbig * ptb, total = items_big + nsmall * pts;
-  TwoQueue queue(vreg(*a.n_multi) * ptb, total, GATEUP ? 6 : 9, vreg((int)gridDim.x));
+  const int ptb = (N + FB - 1) / FB, pts = N / FS;  // blocks of a tile
+  // 32-row tiles: four (two) blocks per item while every workgroup gets two
+  // items, and single ones at the end of the list, about two rounds of them
+  int nbs = pts % 4 == 0 ? 4 : pts % 2 == 0 ? 2 : 1;
+  while (nbs > 1 && nsmall * (pts / nbs) < 2 * grid) nbs >>= 1;
+  const int ntail = nbs > 1 ? min(nsmall, (2 * grid + pts - 1) / pts) : 0;
+  const int ptm = pts / nbs;
+  const int items_big = nbig * ptb, items_mid = items_big + (nsmall - ntail) * ptm;
+  const int total = items_mid + ntail * pts;
+  TwoQueue queue(vreg(*a.n_multi) * ptb, total, GATEUP ? 6 : 9, grid);
   for (;;) {
     if (threadIdx.x == 0) {
       const int it = queue.next(a.counter, a.counter_s);
-      int ti = -1, n0 = 0;
+      int ti = -1, n0 = 0, nb = 1;
       if (it < items_big) {
         ti = it / ptb;
         n0 = (it - ti * ptb) * FB;
-      } else if (it < total) {
-        const int q = (it - items_big) / pts;
+      } else if (it < items_mid) {
+        const int q = (it - items_big) / ptm;
         ti = nbig + q;
-        n0 = (it - items_big - q * pts) * FS;
+        n0 = (it - items_big - q * ptm) * FS * nbs;
+        nb = nbs;
+      } else if (it < total) {
+        const int q = (it - items_mid) / pts;
+        ti = nbig + nsmall - ntail + q;
+        n0 = (it - items_mid - q * pts) * FS;
       }
+      next_item[3] = nb;
       next_item[0] = ti;
       next_item[1] = n0;
       next_item[2] = a.K;
@@ -343,16 +409,21 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     ai.s1 = static_cast<const uint8_t *>(m4_get(next_item + 6));
     ai.out = m4_get(next_item + 8);
     const Tile t = a.tiles[ti];
+    const int nb = __builtin_amdgcn_readfirstlane(next_item[3]);
     switch (tile_class(t)) {
-      case 8: m4_item<GATEUP, false, 8, kM4WRows, 1>(ai, t, n0, ring, ring_lds); break;
-      case 6: m4_item<GATEUP, false, 6, kM4WRows, 1>(ai, t, n0, ring, ring_lds); break;
-      case 4: m4_item<GATEUP, false, 4, kM4WRows, 2>(ai, t, n0, ring, ring_lds); break;
-      case 2: m4_item<GATEUP, false, 2, kM4WRows, 2>(ai, t, n0, ring, ring_lds); break;
+      case 8: m4_item<GATEUP, false, 256, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
+      case 6: m4_item<GATEUP, false, 192, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
+      case 4: m4_item<GATEUP, false, 128, kM4WRows, 2>(ai, t, n0, 1, ring, ring_lds); break;
+      case 2: m4_item<GATEUP, false, 64, kM4WRows, 2>(ai, t, n0, 1, ring, ring_lds); break;
       default:
-        if (t.ablk & kTileStream)
-          m4_item<GATEUP, true, 1, kM4WRowsSmall, 4>(ai, t, n0, ring, ring_lds);
+        if (!(t.ablk & kTileStream))
+          m4_item<GATEUP, false, 32, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
+        else if (t.nrows > 16)
+          m4_item<GATEUP, true, 32, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
+        else if (t.nrows > 8)
+          m4_item<GATEUP, true, 16, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
         else
-          m4_item<GATEUP, false, 1, kM4WRowsSmall, 4>(ai, t, n0, ring, ring_lds);
+          m4_item<GATEUP, true, 8, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
         break;
     }
     // the ring (and the item in it) is rewritten only after every wave has
