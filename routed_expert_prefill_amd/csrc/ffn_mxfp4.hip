@@ -33,11 +33,10 @@ struct Mx4Args {
   const Tile *tiles;
   const int *ntiles;
   const int *n_small;  // 32-row tiles at the end of the tile list
-  const int *n_multi;  // tiles of experts with several tiles, at the start of the list
-  int *counter;        // compute-queue head (TwoQueue), zeroed by the schedule
-  int *counter_s;      // stream-queue head
+  unsigned long long *heads;  // of the work queues (M4Queues), zeroed by the plan
 };
 
+constexpr int kM4Queues = 8;
 constexpr int kM4Threads = 512;
 constexpr int kM4Waves = kM4Threads / kWave;
 constexpr int kM4Ring = 160 * 1024;  // the whole LDS of a workgroup
@@ -48,12 +47,24 @@ template <int AR, int WR, int KB>
 struct M4Ring {
   static constexpr int kAct = AR * 128 * KB;
   static constexpr int kCodes = WR * 32 * KB;
-  static constexpr int kScaleRow = KB == 4 ? 8 : 4;  // bytes of scales per weight row
-  static constexpr int kSlot = kAct + kCodes + WR * kScaleRow;
-  // tiles of at most 32 rows: waves 4-7 hand their sums to waves 0-3 behind the ring
-  static constexpr int kSums = AR <= 32 ? 4 * 4096 : 0;
-  static constexpr int kFit = (kM4Ring - kSums) / kSlot;
+  static constexpr int kSlot = kAct + kCodes;
+  // Scales come in groups of 16 bytes per weight row, for kGroup stages.  A
+  // group is loaded with its first stage and read until its last, so two
+  // buffers do if a group is at least as long as the ring (less one stage);
+  // items of several blocks, whose groups end with each block, have one
+  // buffer per slot.
+  static constexpr int kGroup = 8 / KB;
+  static constexpr int kScales = WR * 16;
+  static constexpr bool kSmall = AR <= 32;
+  // small tiles: waves 4-7 hand their sums to waves 0-3 behind the ring
+  static constexpr int kSums = kSmall ? 4 * 4096 : 0;
+  static constexpr int kFit = kSmall ? (kM4Ring - kSums) / (kSlot + kScales)
+                                     : (kM4Ring - 2 * kScales) / kSlot;
   static constexpr int kDepth = kFit < 8 ? kFit : 8;
+  static constexpr int kBuffers = kSmall ? kDepth : 2;
+  static_assert(kSmall || kGroup >= kDepth - 1, "two buffers of scales");
+  static constexpr int kScaleBase = kDepth * kSlot;
+  static_assert(kScaleBase + kBuffers * kScales + kSums <= kM4Ring, "fits");
 };
 
 // 16-byte chunk c of the codes of weight row r is stored at this slot of the
@@ -103,21 +114,21 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   constexpr int TT = L::TT, TW = L::TW;
   constexpr int NA = KB * AR / 8;      // activation loads: 8 rows of 128 bytes
   constexpr int NW = WR * KB / 32;     // code loads: 1 KB
-  constexpr int NC = G::kScaleRow * WR / 256;  // scale loads: 256 bytes
-  // load i of a kind goes to wave i % 8, the loads of scales to the last NC waves
-  static_assert((NA % kM4Waves == 0 || NA < kM4Waves) && NW % kM4Waves == 0 && NC <= kM4Waves,
-                "shares");
+  // load i of a kind goes to wave i % 8
+  static_assert((NA % kM4Waves == 0 || NA < kM4Waves) && NW % kM4Waves == 0, "shares");
   constexpr int JA = (NA + kM4Waves - 1) / kM4Waves, JW = NW / kM4Waves;
   constexpr int NS = G::kDepth;
-  static_assert(NS >= 2 && (JA + JW + 1) * (NS - 2) <= 32, "wait_vm counts to 32");
+  static_assert(NS >= 2 && (JA + JW) * (NS - 2) <= 32, "wait_vm counts to 32");
   const int nb = MB ? nb_arg : 1;
   const int lane = lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int K = a.K;
   const int nst = (K / 64 + KB - 1) / KB;
   const bool half = KB == 4 && (K & 128) != 0;  // the last stage has two blocks only
-  const bool has_act = NA % kM4Waves == 0 || wv < NA, has_scales = wv >= kM4Waves - NC;
-  const int cnt = JW + (has_act ? JA : 0) + (has_scales ? 1 : 0);  // loads of this wave per stage
+  const bool has_act = NA % kM4Waves == 0 || wv < NA;
+  // loads of this wave per stage, scales left out: where they are in flight
+  // the wait below ends a load later than it has to
+  const int cnt = JW + (has_act ? JA : 0);
 
   auto wrow = [&](int wr, const uint8_t *p0, const uint8_t *p1, int row_bytes) {
     const uint8_t *w = p0;
@@ -132,7 +143,7 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   };
   // this lane's source of each of its loads at stage 0.  In a half stage the
   // sources of the missing second half move back to the first (loaded, not used).
-  const uint8_t *act[JA], *codes[JW], *scales;
+  const uint8_t *act[JA], *codes[JW];
 #pragma unroll
   for (int j = 0; j < JA; ++j) {
     const int i = wv + kM4Waves * j;
@@ -152,11 +163,30 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     codes[j] = wrow(r, a.w0, a.w1, K / 2) + c * 16;
     code_back |= (c >= 4 ? 1 : 0) << j;
   }
-  {
-    constexpr int SPR = G::kScaleRow / 4;  // lanes per row of scales
-    const int i = max(wv - (kM4Waves - NC), 0);
-    scales = wrow(i * (64 / SPR) + lane / SPR, a.s0, a.s1, K / 32) + (lane % SPR) * 4;
-  }
+  // Scales of a group: where rows start on 16-byte borders, one load of 16
+  // bytes per lane and 64 rows by each of the last WR / 64 waves; elsewhere
+  // loads of 4 bytes per lane and 16 rows.  Both leave 16 bytes per row in LDS.
+  constexpr int SW = WR / 64;
+  const bool wide = (K & 511) == 0;
+  const int swv = wv - (kM4Waves - SW);
+  const int srow = wide ? max(swv, 0) * 64 + lane : wv * (WR / 8) + (lane >> 2);
+  const uint8_t *scales = wrow(srow, a.s0, a.s1, K / 32);
+  int group = 0;  // groups loaded so far
+  auto issue_scales = [&](int s, int b) {
+    const uint32_t to = ring_lds + (uint32_t)G::kScaleBase +
+                        (unsigned)group % (unsigned)G::kBuffers * G::kScales;
+    ++group;
+    uint32_t off = (uint32_t)s * (2 * KB) + (MB ? (uint32_t)(b * FEAT) * (K / 32) : 0);
+    if (wide) {
+      if (swv >= 0) dma16(scales + off, to + (uint32_t)swv * 1024u);
+    } else {
+      // words past the row's end are not there: the group's first instead
+      off += (s * KB + (lane & 3) * 2) * 64 < K ? (lane & 3) * 4 : 0;
+      dma4(scales + off, to + (uint32_t)wv * (WR * 2u));
+      if (WR == 256)
+        dma4(wrow(srow + 16, a.s0, a.s1, K / 32) + off, to + (uint32_t)wv * (WR * 2u) + 256u);
+    }
+  };
   // loads of stage s of block b
   auto issue = [&](int s, int b, int slot) {
     const uint32_t base = ring_lds + (uint32_t)(slot * G::kSlot) + (uint32_t)wv * 1024u;
@@ -181,14 +211,7 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
       else
         dma16(p, to);
     }
-    if (has_scales) {
-      // two scales per block; KB == 1 loads the aligned four that hold them
-      const uint8_t *p = scales + (KB == 1 ? (s >> 1) * 4 : s * (2 * KB)) +
-                         (MB ? (uint32_t)(b * FEAT) * (K / 32) : 0);
-      if (KB == 4 && cut) p -= (lane & 1) * 4;
-      dma4(p, ring_lds + (uint32_t)(slot * G::kSlot + G::kAct + G::kCodes) +
-                  (uint32_t)(wv - (kM4Waves - NC)) * 256u);
-    }
+    if (s % G::kGroup == 0) issue_scales(s, b);
   };
 
   const int rr = lane & 31, rh = lane >> 5;
@@ -202,44 +225,66 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
         for (int j = 0; j < 16; ++j) acc[tw][tt][j] = 0.f;
   };
 
-  // the MFMAs of one ring stage
-  auto mma_stage = [&](const uint8_t *buf, int s) {
-    static_assert(L::kSplit || KB <= 2, "one word of scales per wave and stage");
-    uint32_t sc[TW];
-#pragma unroll
-    for (int tw = 0; tw < TW; ++tw) {
-      const uint8_t *p = buf + G::kAct + G::kCodes + (L::wtile(wv, tw) * 32 + rr) * G::kScaleRow;
-      if (L::kSplit) p += (wv >> 2) * 4;
-      sc[tw] = *reinterpret_cast<const uint32_t *>(p) >> (8 * rh + (KB == 1 ? 16 * (s & 1) : 0));
-    }
+  // the MFMAs of one ring stage; sbuf: the buffer with its group of scales
+  auto mma_stage = [&](const uint8_t *buf, const uint8_t *sbuf, int s) {
     if (L::kSplit && wv >= 4 && half && s == nst - 1) return;  // no second half there
     constexpr int KW = L::kSplit ? KB / 2 : KB;  // blocks of this wave
+    const int kb0 = L::kSplit ? (wv >> 2) * 2 : 0;
+    // two scales per block and four to a word: the word of this wave's blocks
+    const int word = L::kSplit ? (s & 1) * 2 + (wv >> 2) : KB == 2 ? s & 3 : (s >> 1) & 3;
+    uint32_t sc[TW];
+    i32x4 raw[KW][TW];
 #pragma unroll
-    for (int q = 0; q < KW; ++q) {
-      const int kb = L::kSplit ? (wv >> 2) * 2 + q : q;
-      i32x4 raw[TW];
-      float scale[TW];
+    for (int tw = 0; tw < TW; ++tw) {
+      const int r = L::wtile(wv, tw) * 32 + rr;
+      sc[tw] = *reinterpret_cast<const uint32_t *>(sbuf + r * 16 + word * 4) >>
+               (8 * rh + (KB == 1 ? 16 * (s & 1) : 0));
 #pragma unroll
-      for (int tw = 0; tw < TW; ++tw) {
-        const int r = L::wtile(wv, tw) * 32 + rr;
-        raw[tw] = *reinterpret_cast<const i32x4 *>(buf + G::kAct + r * (32 * KB) +
-                                                   m4_slot<KB>(r, 2 * kb + rh) * 16);
-        scale[tw] = mx4_scale((sc[tw] >> (16 * (q & 1))) & 0xffu);
+      for (int q = 0; q < KW; ++q)
+        raw[q][tw] = *reinterpret_cast<const i32x4 *>(
+            buf + G::kAct + r * (32 * KB) + m4_slot<KB>(r, 2 * (kb0 + q) + rh) * 16);
+    }
+    auto load_act = [&](int q, int j, bf16x8 (&fa)[TT]) {
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        const int r = (L::atile(wv, tt) * 32 + rr) & (AR < 32 ? AR - 1 : -1);
+        fa[tt] = *reinterpret_cast<const bf16x8 *>(buf + (kb0 + q) * (AR * 128) + r * 128 +
+                                                   ring_slot(r, 4 * rh + j) * 16);
       }
+    };
+    if constexpr (L::kSplit) {
+      // everything the stage needs is read ahead: with one tile pair per wave
+      // a read in front of each MFMA left the wave waiting for LDS most of
+      // the time
+      bf16x8 fa[KW][4][TT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8 fa[TT];
+      for (int q = 0; q < KW; ++q)
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-          const int r = (L::atile(wv, tt) * 32 + rr) & (AR < 32 ? AR - 1 : -1);
-          fa[tt] = *reinterpret_cast<const bf16x8 *>(buf + kb * (AR * 128) + r * 128 +
-                                                     ring_slot(r, 4 * rh + j) * 16);
-        }
+        for (int j = 0; j < 4; ++j) load_act(q, j, fa[q][j]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int tw = 0; tw < TW; ++tw) {
-          const bf16x8 fw = mx4_decode8((uint32_t)raw[tw][j], scale[tw]);
+      for (int q = 0; q < KW; ++q) {
+        const float scale = mx4_scale((sc[0] >> (16 * q)) & 0xffu);
 #pragma unroll
-          for (int tt = 0; tt < TT; ++tt) acc[tw][tt] = mfma32_bf16(fw, fa[tt], acc[tw][tt]);
+        for (int j = 0; j < 4; ++j)
+          acc[0][0] = mfma32_bf16(mx4_decode8((uint32_t)raw[q][0][j], scale), fa[q][j][0], acc[0][0]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < KW; ++q) {
+        float scale[TW];
+#pragma unroll
+        for (int tw = 0; tw < TW; ++tw) scale[tw] = mx4_scale((sc[tw] >> (16 * q)) & 0xffu);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bf16x8 fa[TT];
+          load_act(q, j, fa);
+#pragma unroll
+          for (int tw = 0; tw < TW; ++tw) {
+            const bf16x8 fw = mx4_decode8((uint32_t)raw[q][tw][j], scale[tw]);
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) acc[tw][tt] = mfma32_bf16(fw, fa[tt], acc[tw][tt]);
+          }
         }
       }
     }
@@ -315,15 +360,18 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   for (int s = 0; s < NS - 1; ++s)
     if (s < total) issue_next(s);
   int slot = 0, cs = 0, cb = 0;  // stage and block being multiplied
+  int cg = 0;                    // buffer of its group of scales
   for (int s = 0; s < total; ++s) {
     // this wave's loads of stage s are done; later stages may stay in flight
     // (stores of an earlier block, counted too, only make the wait longer)
     wait_vm(cnt * min(NS - 2, total - 1 - s));
     ring_barrier();  // stage s is in LDS for everyone; stage s - 1 is consumed
     if (s + NS - 1 < total) issue_next(slot == 0 ? NS - 1 : slot - 1);
-    mma_stage(ring + slot * G::kSlot, MB ? cs : s);
+    mma_stage(ring + slot * G::kSlot, ring + G::kScaleBase + cg * G::kScales, cs);
     slot = slot == NS - 1 ? 0 : slot + 1;
-    if (MB && ++cs == nst) {
+    ++cs;
+    if (cs % G::kGroup == 0 || (MB && cs == nst)) cg = cg == G::kBuffers - 1 ? 0 : cg + 1;
+    if (MB && cs == nst) {
       epilogue(n0 + cb * FEAT);
       cs = 0;
       if (++cb < nb) zero_acc();
@@ -332,21 +380,221 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   if (!MB) epilogue(n0);
 }
 
-// A pointer through two words of LDS.
+// ------------------------------------------------------------------ few rows
+
+// A tile of at most 16 rows is a weight stream with little to multiply.  Its
+// activation rows go to LDS whole, once per item, and every wave then streams
+// weight rows of its own straight into registers, two chunks of kM4Steps
+// steps in turn (the next one's loads in flight while one is multiplied):
+// there is no barrier per stage, so no wave waits for another's loads, and
+// LDS serves the activations only.  (Through the ring, whose stages all waves
+// read at the same time, reads of activation tiles kept LDS busy for most of
+// a stage: MI355X, 401 tokens, gate/up 4.5 TB/s.)
+// Products are 16x16x32 MFMAs: a step is 128 columns, lane group c = l / 16
+// holds the codes of group c of a weight row l % 16 (16 bytes), and MFMA j
+// multiplies columns 8 j .. 8 j + 7 of the four groups.
+constexpr int kM4Steps = 4;
+constexpr int kM4DirectRows = 16;
+constexpr int kM4ScaleRow = kM4Steps * 4 + 16;  // a weight row's scales of a chunk in LDS, padded
+constexpr int kM4ScaleWave = 2 * 16 * kM4ScaleRow;
+constexpr int kM4DirectAct = kM4Ring - kM4Waves * kM4ScaleWave;  // LDS for activation rows
+
+// Row stride of the activation rows in LDS, padded: consecutive rows start
+// in different banks.
+__device__ __forceinline__ int m4_direct_stride(int K) { return 2 * K + 16; }
+__device__ __forceinline__ bool m4_direct_fits(const Tile &t, int K) {
+  return t.nrows <= kM4DirectRows && t.nrows * m4_direct_stride(K) <= kM4DirectAct;
+}
+
+// One chunk of a wave's two weight tiles of 16 rows.
+struct M4Chunk {
+  i32x4 raw[kM4Steps][2];
+  uint32_t sc[2];  // lane group c: the scales of step c
+};
+
+// Output features [n0, n1) of a tile.
+template <bool GATEUP>
+__device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n0, int n1,
+                                          uint8_t *lds) {
+  constexpr int FG = GATEUP ? 16 : 32;  // features of a wave's two weight tiles
+  const int lane = lane_id();
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane >> 4, row = lane & 15;
+  const int K = a.K, nk = K / 128;
+  const int stride = m4_direct_stride(K);
+  const int chunks = (nk + kM4Steps - 1) / kM4Steps;
+  const int groups = max(((n1 - n0) / FG - wv + kM4Waves - 1) / kM4Waves, 0);
+  const int total = groups * chunks;
+  uint8_t *sc_lds = lds + kM4DirectAct + wv * kM4ScaleWave + row * kM4ScaleRow;
+
+  auto load = [&](M4Chunk &q, int i) {
+    const int g = i / chunks, s = (i - g * chunks) * kM4Steps;
+    const int n = n0 + (wv + kM4Waves * g) * FG;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const size_t r = (size_t)t.e * a.N + n + row + (GATEUP ? 0 : 16 * w);
+      const uint8_t *codes = (GATEUP && w ? a.w1 : a.w0) + r * (K / 2) + c * 16;
+      const uint8_t *scales = (GATEUP && w ? a.s1 : a.s0) + r * (K / 32);
+      // steps past the end load the last one again
+      q.sc[w] = *reinterpret_cast<const uint32_t *>(scales + min(s + c, nk - 1) * 4);
+#pragma unroll
+      for (int u = 0; u < kM4Steps; ++u)
+        q.raw[u][w] = *reinterpret_cast<const i32x4 *>(codes + min(s + u, nk - 1) * 64);
+    }
+    asm volatile("" ::: "memory");  // issued here, not where they are used
+  };
+  f32x4 acc[2] = {};
+  const uint8_t *mine = lds + min(row, t.nrows - 1) * stride + c * 64;
+  auto multiply = [&](const M4Chunk &q, int i) {
+    const int g = i / chunks, ci = i - g * chunks, s = ci * kM4Steps;
+    i32x4 ss[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      *reinterpret_cast<uint32_t *>(sc_lds + w * 16 * kM4ScaleRow + c * 4) = q.sc[w];
+      ss[w] = *reinterpret_cast<const i32x4 *>(sc_lds + w * 16 * kM4ScaleRow);
+    }
+    const int steps = min(kM4Steps, nk - s);
+#pragma unroll
+    for (int u = 0; u < kM4Steps; ++u) {
+      if (u >= steps) break;
+      bf16x8 fx[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        fx[j] = *reinterpret_cast<const bf16x8 *>(mine + (s + u) * 256 + j * 16);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const float scale = mx4_scale(((uint32_t)ss[w][u] >> (8 * c)) & 0xffu);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[w] = mfma_bf16(mx4_decode8((uint32_t)q.raw[u][w][j], scale), fx[j], acc[w]);
+      }
+    }
+    if (ci + 1 < chunks) return;
+    // register r of lane l: weight row 4 (l / 16) + r, activation row l % 16
+    if (row < t.nrows) {
+      const int n = n0 + (wv + kM4Waves * g) * FG + 4 * c;
+      const size_t o = (size_t)(t.row0 + row) * a.N + n;
+      if (GATEUP) {
+        uint2 v;
+        v.x = (uint32_t)f32_to_bf16_bits(swiglu(acc[0][0], acc[1][0])) |
+              ((uint32_t)f32_to_bf16_bits(swiglu(acc[0][1], acc[1][1])) << 16);
+        v.y = (uint32_t)f32_to_bf16_bits(swiglu(acc[0][2], acc[1][2])) |
+              ((uint32_t)f32_to_bf16_bits(swiglu(acc[0][3], acc[1][3])) << 16);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + o) = v;
+      } else {
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + o) = acc[0];
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + o + 16) = acc[1];
+      }
+    }
+    acc[0] = f32x4{};
+    acc[1] = f32x4{};
+  };
+
+  M4Chunk qa, qb;
+  if (total > 0) load(qa, 0);
+  ring_barrier();  // every wave has read its item, which lies where the rows go
+  // wave w brings rows w and w + 8
+  for (int r = wv; r < t.nrows; r += kM4Waves) {
+    const int i = t.row0 + r;
+    const size_t s = GATEUP ? (size_t)(a.sorted_routes[i] / a.k) : (size_t)i;
+    for (int p0 = 0; p0 < K / 8; p0 += 8 * kWave) {
+      i32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = *reinterpret_cast<const i32x4 *>(a.act + s * K +
+                                                min(p0 + u * kWave + lane, K / 8 - 1) * 8);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        *reinterpret_cast<i32x4 *>(lds + r * stride + min(p0 + u * kWave + lane, K / 8 - 1) * 16) =
+            v[u];
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  ring_barrier();
+  // no load in the loop is conditional: where a path without it joined, the
+  // compiler would have to wait for all of them
+  if (total == 0) return;
+  int i = 0;
+#pragma unroll 1
+  for (; i + 2 < total; i += 2) {
+    load(qb, i + 1);
+    multiply(qa, i);
+    load(qa, i + 2);
+    multiply(qb, i + 1);
+  }
+  if (i + 1 < total) {
+    load(qb, i + 1);
+    multiply(qa, i);
+    multiply(qb, i + 1);
+  } else {
+    multiply(qa, i);
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+
+// A pointer to global memory through two words of LDS.
 __device__ __forceinline__ void m4_put(int *to, const void *p) {
   const uint64_t v = (uint64_t)(uintptr_t)p;
   to[0] = (int)(uint32_t)v;
   to[1] = (int)(uint32_t)(v >> 32);
 }
 __device__ __forceinline__ void *m4_get(const int *from) {
+  typedef __attribute__((address_space(1))) void global_t;  // or its accesses would be flat ones
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane(from[0]);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane(from[1]);
-  return reinterpret_cast<void *>((uintptr_t)(((uint64_t)hi << 32) | lo));
+  return (void *)(global_t *)(uintptr_t)(((uint64_t)hi << 32) | lo);
 }
 
-// Weight rows per item: 256, and 128 for 32-row tiles.
+// Weight rows per item: 256; for 32-row tiles 128, in two blocks.
 constexpr int kM4WRows = 256;
 constexpr int kM4WRowsSmall = 128;
+
+// Work dispatch.  Tile i of the list (tallest first) belongs to queue i % 8,
+// and workgroup b starts on queue b % 8: workgroups go round the eight XCDs
+// in that order, so the items of one tile, which share its activation rows,
+// run on one XCD and read them through one L2.  A queue is drawn from both
+// ends, by every other workgroup of an XCD from the back: where a list holds
+// tall tiles (bound by the matrix unit) and short ones (weight streams), some
+// compute units run the one kind beside the other.  A workgroup whose queue
+// is dry goes on to the next one.
+//
+// A head counts draws from the front (low word) and from the back (high
+// word) of its queue.  Every workgroup draws exactly once past the end of
+// every queue, so the draw that makes the count items + grid is the head's
+// last of the launch and sets it back to zero, as the plan left it.
+struct M4Queues {
+  unsigned long long *heads;
+  int nbig, nsmall, ptb, pts;
+  int q, left;
+  __device__ __forceinline__ M4Queues(unsigned long long *heads_, int nbig_, int nsmall_, int ptb_,
+                                      int pts_)
+      : heads(heads_), nbig(nbig_), nsmall(nsmall_), ptb(ptb_), pts(pts_) {
+    q = vreg((int)blockIdx.x) & (kM4Queues - 1);
+    left = kM4Queues;
+  }
+  // the next item: tile and which of its items; false if none is left
+  __device__ __forceinline__ bool next(int *tile, int *part) {
+    const bool back = (vreg((int)blockIdx.x) / kM4Queues) & 1;
+    for (; left > 0; --left, q = (q + 1) & (kM4Queues - 1)) {
+      const int tall = (nbig - q + kM4Queues - 1) / kM4Queues;  // tall tiles of this queue
+      const int all = (nbig + nsmall - q + kM4Queues - 1) / kM4Queues;
+      const int n = tall * ptb + (all - tall) * pts;
+      const unsigned long long v = atomicAdd(heads + q, back ? 1ull << 32 : 1ull);
+      const int f = (int)(uint32_t)v, b = (int)(v >> 32);
+      if (f + b < n) {
+        const int i = back ? n - 1 - b : f;
+        const int j = i < tall * ptb ? i / ptb : tall + (i - tall * ptb) / pts;
+        *part = i < tall * ptb ? i - j * ptb : i - tall * ptb - (j - tall) * pts;
+        *tile = q + j * kM4Queues;
+        return true;
+      }
+      if (f + b == n + (int)gridDim.x - 1)
+        __hip_atomic_store(heads + q, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    return false;
+  }
+};
 
 template <bool GATEUP>
 __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args a) {
@@ -356,40 +604,18 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
   int *next_item = reinterpret_cast<int *>(ring);
   const uint32_t ring_lds = lds_addr(ring);
   constexpr int kHalf = GATEUP ? 2 : 1;  // gate and up rows of one feature
-  constexpr int FB = kM4WRows / kHalf, FS = kM4WRowsSmall / kHalf;  // features per item
+  constexpr int FB = kM4WRows / kHalf;           // features per item of the taller tiles
+  constexpr int FS = 2 * kM4WRowsSmall / kHalf;  // and of the 32-row tiles
   const int N = vreg(a.N);
-  const int grid = vreg((int)gridDim.x);
   const int nsmall = vreg(*a.n_small), nbig = vreg(*a.ntiles) - nsmall;
-  const int ptb = (N + FB - 1) / FB, pts = N / FS;  // blocks of a tile
-  // 32-row tiles: four (two) blocks per item while every workgroup gets two
-  // items, and single ones at the end of the list, about two rounds of them
-  int nbs = pts % 4 == 0 ? 4 : pts % 2 == 0 ? 2 : 1;
-  while (nbs > 1 && nsmall * (pts / nbs) < 2 * grid) nbs >>= 1;
-  const int ntail = nbs > 1 ? min(nsmall, (2 * grid + pts - 1) / pts) : 0;
-  const int ptm = pts / nbs;
-  const int items_big = nbig * ptb, items_mid = items_big + (nsmall - ntail) * ptm;
-  const int total = items_mid + ntail * pts;
-  TwoQueue queue(vreg(*a.n_multi) * ptb, total, GATEUP ? 6 : 9, grid);
+  const int ptb = (N + FB - 1) / FB, pts = (N + FS - 1) / FS;  // items per tile
+  M4Queues queues(a.heads, nbig, nsmall, ptb, pts);
   for (;;) {
     if (threadIdx.x == 0) {
-      const int it = queue.next(a.counter, a.counter_s);
-      int ti = -1, n0 = 0, nb = 1;
-      if (it < items_big) {
-        ti = it / ptb;
-        n0 = (it - ti * ptb) * FB;
-      } else if (it < items_mid) {
-        const int q = (it - items_big) / ptm;
-        ti = nbig + q;
-        n0 = (it - items_big - q * ptm) * FS * nbs;
-        nb = nbs;
-      } else if (it < total) {
-        const int q = (it - items_mid) / pts;
-        ti = nbig + nsmall - ntail + q;
-        n0 = (it - items_mid - q * pts) * FS;
-      }
-      next_item[3] = nb;
-      next_item[0] = ti;
-      next_item[1] = n0;
+      int ti, part;
+      const bool some = queues.next(&ti, &part);
+      next_item[0] = some ? ti : -1;
+      next_item[1] = some ? part * (ti < nbig ? FB : FS) : 0;
       next_item[2] = a.K;
       m4_put(next_item + 4, a.s0);
       m4_put(next_item + 6, a.s1);
@@ -409,22 +635,22 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     ai.s1 = static_cast<const uint8_t *>(m4_get(next_item + 6));
     ai.out = m4_get(next_item + 8);
     const Tile t = a.tiles[ti];
-    const int nb = __builtin_amdgcn_readfirstlane(next_item[3]);
     switch (tile_class(t)) {
       case 8: m4_item<GATEUP, false, 256, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
       case 6: m4_item<GATEUP, false, 192, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
       case 4: m4_item<GATEUP, false, 128, kM4WRows, 2>(ai, t, n0, 1, ring, ring_lds); break;
       case 2: m4_item<GATEUP, false, 64, kM4WRows, 2>(ai, t, n0, 1, ring, ring_lds); break;
-      default:
-        if (!(t.ablk & kTileStream))
-          m4_item<GATEUP, false, 32, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
-        else if (t.nrows > 16)
+      default: {
+        const int n1 = min(n0 + FS, ai.N);
+        const int nb = (n1 - n0) * 2 / FS;
+        if (m4_direct_fits(t, ai.K))
+          m4_direct<GATEUP>(ai, t, n0, n1, ring);
+        else if (t.ablk & kTileStream)
           m4_item<GATEUP, true, 32, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
-        else if (t.nrows > 8)
-          m4_item<GATEUP, true, 16, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
         else
-          m4_item<GATEUP, true, 8, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
+          m4_item<GATEUP, false, 32, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
         break;
+      }
     }
     // the ring (and the item in it) is rewritten only after every wave has
     // passed this barrier
@@ -433,8 +659,13 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
 }
 
 hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream) {
+  // the queue heads of the two projections, in the free words of the schedule
+  static_assert(sizeof(L.sch->pad) >= 2 * kM4Queues * 8, "room for the heads");
+  unsigned long long *heads = reinterpret_cast<unsigned long long *>(L.sch + 1) - 2 * kM4Queues;
   if (stages & kStagePlan) {
-    const hipError_t err = launch_grouped_schedule(L.offsets, L.E, L.sch, L.tiles, stream);
+    hipError_t err = launch_grouped_schedule(L.offsets, L.E, L.sch, L.tiles, stream);
+    if (err == hipSuccess)
+      err = launch_zero_u32(reinterpret_cast<uint32_t *>(heads), 4 * kM4Queues, stream);
     if (err != hipSuccess) return err;
   }
   Mx4Args g{};
@@ -442,7 +673,6 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
   g.tiles = L.tiles;
   g.ntiles = &L.sch->n_tiles;
   g.n_small = &L.sch->n_small;
-  g.n_multi = &L.sch->n_multi;
   if (stages & kStageGateUp) {
     g.act = L.x;
     g.sorted_routes = L.sorted_routes;
@@ -453,8 +683,7 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
     g.out = L.h;
     g.N = L.f;
     g.K = L.d;
-    g.counter = &L.sch->counter[0];
-    g.counter_s = &L.sch->counter_s[0];
+    g.heads = heads;
     hipLaunchKernelGGL(grouped_gemm_mx4_kernel<true>, dim3(L.num_cus), dim3(kM4Threads), 0, stream,
                        g);
   }
@@ -468,8 +697,7 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
     g.out = L.y;
     g.N = L.d;
     g.K = L.f;
-    g.counter = &L.sch->counter[1];
-    g.counter_s = &L.sch->counter_s[1];
+    g.heads = heads + kM4Queues;
     hipLaunchKernelGGL(grouped_gemm_mx4_kernel<false>, dim3(L.num_cus), dim3(kM4Threads), 0,
                        stream, g);
   }
