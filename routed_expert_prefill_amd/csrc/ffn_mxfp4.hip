@@ -22,6 +22,23 @@
 
 namespace moe {
 
+constexpr int kM4Queues = 8;
+
+// Heads of a projection's work queues, and the workgroups that have left.
+struct M4Heads {
+  unsigned long long head[kM4Queues];
+  int left, pad;
+};
+
+// What the plan leaves at the start of the workspace.
+struct M4Schedule {
+  int n_tiles;  // entries of the tile list, tallest capacity first
+  int n_small;  // 32-row tiles, the last n_small entries
+  int pad[2];
+  M4Heads heads[2];  // gate/up, down
+};
+static_assert(sizeof(M4Schedule) <= sizeof(Schedule), "has the schedule's place");
+
 struct Mx4Args {
   const uint16_t *act;           // gate/up: x [T, K]; down: h [R, K]
   const int32_t *sorted_routes;  // gate/up: token of sorted row i is sorted_routes[i] / k
@@ -33,10 +50,9 @@ struct Mx4Args {
   const Tile *tiles;
   const int *ntiles;
   const int *n_small;  // 32-row tiles at the end of the tile list
-  unsigned long long *heads;  // of the work queues (M4Queues), zeroed by the plan
+  M4Heads *heads;      // of the work queues (M4Queues), zeroed by the plan
 };
 
-constexpr int kM4Queues = 8;
 constexpr int kM4Threads = 512;
 constexpr int kM4Waves = kM4Threads / kWave;
 constexpr int kM4Ring = 160 * 1024;  // the whole LDS of a workgroup
@@ -115,8 +131,8 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   constexpr int NA = KB * AR / 8;      // activation loads: 8 rows of 128 bytes
   constexpr int NW = WR * KB / 32;     // code loads: 1 KB
   // load i of a kind goes to wave i % 8
-  static_assert((NA % kM4Waves == 0 || NA < kM4Waves) && NW % kM4Waves == 0, "shares");
-  constexpr int JA = (NA + kM4Waves - 1) / kM4Waves, JW = NW / kM4Waves;
+  static_assert(NA % kM4Waves == 0 && NW % kM4Waves == 0, "even shares");
+  constexpr int JA = NA / kM4Waves, JW = NW / kM4Waves;
   constexpr int NS = G::kDepth;
   static_assert(NS >= 2 && (JA + JW) * (NS - 2) <= 32, "wait_vm counts to 32");
   const int nb = MB ? nb_arg : 1;
@@ -125,10 +141,9 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   const int K = a.K;
   const int nst = (K / 64 + KB - 1) / KB;
   const bool half = KB == 4 && (K & 128) != 0;  // the last stage has two blocks only
-  const bool has_act = NA % kM4Waves == 0 || wv < NA;
   // loads of this wave per stage, scales left out: where they are in flight
   // the wait below ends a load later than it has to
-  const int cnt = JW + (has_act ? JA : 0);
+  const int cnt = JA + JW;
 
   auto wrow = [&](int wr, const uint8_t *p0, const uint8_t *p1, int row_bytes) {
     const uint8_t *w = p0;
@@ -193,13 +208,11 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     const bool cut = half && s == nst - 1;
     const uint32_t act_off = (uint32_t)s * (128 * KB);
     const uint32_t code_off = (uint32_t)s * (32 * KB) + (MB ? (uint32_t)(b * FEAT) * (K / 2) : 0);
-    if (has_act) {
 #pragma unroll
-      for (int j = 0; j < JA; ++j) {
-        const uint8_t *p = act[j] + act_off;
-        if (KB == 4 && cut && (wv + kM4Waves * j) / (AR / 8) >= 2) p -= 256;
-        dma16(p, base + (uint32_t)j * (kM4Waves * 1024u));
-      }
+    for (int j = 0; j < JA; ++j) {
+      const uint8_t *p = act[j] + act_off;
+      if (KB == 4 && cut && (wv + kM4Waves * j) / (AR / 8) >= 2) p -= 256;
+      dma16(p, base + (uint32_t)j * (kM4Waves * 1024u));
     }
 #pragma unroll
     for (int j = 0; j < JW; ++j) {
@@ -247,7 +260,7 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     auto load_act = [&](int q, int j, bf16x8 (&fa)[TT]) {
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
-        const int r = (L::atile(wv, tt) * 32 + rr) & (AR < 32 ? AR - 1 : -1);
+        const int r = L::atile(wv, tt) * 32 + rr;
         fa[tt] = *reinterpret_cast<const bf16x8 *>(buf + (kb0 + q) * (AR * 128) + r * 128 +
                                                    ring_slot(r, 4 * rh + j) * 16);
       }
@@ -345,8 +358,7 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   };
 
   zero_acc();
-  wait_vm(0);
-  ring_barrier();  // every wave is done with the ring contents of the previous item
+  ring_barrier();  // every wave has read its item, which lies in the ring
   const int total = MB ? nb * nst : nst;
   int is = 0, ib = 0;  // stage and block of the next stage to load
   auto issue_next = [&](int slot) {
@@ -533,64 +545,153 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
 
 // ------------------------------------------------------------------ kernel
 
-// A pointer to global memory through two words of LDS.
-__device__ __forceinline__ void m4_put(int *to, const void *p) {
-  const uint64_t v = (uint64_t)(uintptr_t)p;
-  to[0] = (int)(uint32_t)v;
-  to[1] = (int)(uint32_t)(v >> 32);
-}
-__device__ __forceinline__ void *m4_get(const int *from) {
-  typedef __attribute__((address_space(1))) void global_t;  // or its accesses would be flat ones
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane(from[0]);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane(from[1]);
-  return (void *)(global_t *)(uintptr_t)(((uint64_t)hi << 32) | lo);
+// The tile list, one thread per expert: its full 256-row tiles, then one
+// remainder tile of the smallest capacity of 32, 64, 128, 192 and 256 rows
+// that holds it (Tile); all tiles of a class together, tallest class first,
+// experts in order.
+constexpr int kM4ScheduleThreads = 256;  // the most experts
+__global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
+    const int32_t *__restrict__ offsets, int E, M4Schedule *__restrict__ sch,
+    Tile *__restrict__ tiles) {
+  constexpr int NC = 5;  // capacities 256, 192, 128, 64, 32
+  constexpr int NW = kM4ScheduleThreads / kWave;
+  __shared__ int waves[NC][NW];
+  const int e = threadIdx.x, lane = lane_id(), wave = threadIdx.x / kWave;
+  int row0 = 0, n = 0;
+  if (e < E) {
+    row0 = offsets[e];
+    n = offsets[e + 1] - row0;
+  }
+  const int full = n / kTileRows, rem = n % kTileRows;
+  const int cls = rem == 0 ? NC : rem > 192 ? 0 : rem > 128 ? 1 : rem > 64 ? 2 : rem > 32 ? 3 : 4;
+  int at[NC];  // where this expert's tiles of a class begin
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int mine = (c == 0 ? full : 0) + (c == cls ? 1 : 0);
+    int v = mine;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int x = __shfl_up(v, off);
+      if (lane >= off) v += x;
+    }
+    if (lane == kWave - 1) waves[c][wave] = v;
+    at[c] = v - mine;
+  }
+  __syncthreads();
+  int total = 0, last = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    at[c] += total;
+    last = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (w < wave) at[c] += waves[c][w];
+      last += waves[c][w];
+    }
+    total += last;
+  }
+  const int only = n <= kTileRows ? kTileStream : 0;
+  for (int i = 0; i < full; ++i) tiles[at[0] + i] = Tile{e, row0 + i * kTileRows, kTileRows, 8 | only};
+  if (cls < NC) {
+    constexpr int kAblk[NC] = {8, 6, 4, 2, 1};
+    const int i = cls == 0 ? at[0] + full : cls == 1 ? at[1] : cls == 2 ? at[2] : cls == 3 ? at[3] : at[4];
+    tiles[i] = Tile{e, row0 + full * kTileRows, rem, (cls == 0 ? kAblk[0] : cls == 1 ? kAblk[1] : cls == 2 ? kAblk[2] : cls == 3 ? kAblk[3] : kAblk[4]) | only};
+  }
+  if (e < 2 * kM4Queues) sch->heads[e / kM4Queues].head[e % kM4Queues] = 0;
+  if (e < 2) sch->heads[e].left = 0;
+  if (e == 0) {
+    sch->n_tiles = total;
+    sch->n_small = last;
+  }
 }
 
-// Weight rows per item: 256; for 32-row tiles 128, in two blocks.
+// Weight rows per item: 256; for 32-row tiles 128, in four blocks.
 constexpr int kM4WRows = 256;
 constexpr int kM4WRowsSmall = 128;
 
 // Work dispatch.  Tile i of the list (tallest first) belongs to queue i % 8,
-// and workgroup b starts on queue b % 8: workgroups go round the eight XCDs
-// in that order, so the items of one tile, which share its activation rows,
-// run on one XCD and read them through one L2.  A queue is drawn from both
-// ends, by every other workgroup of an XCD from the back: where a list holds
-// tall tiles (bound by the matrix unit) and short ones (weight streams), some
-// compute units run the one kind beside the other.  A workgroup whose queue
-// is dry goes on to the next one.
+// and workgroup b to queue b % 8: workgroups go round the eight XCDs in that
+// order, so the items of one tile, which share its activation rows, run on
+// one XCD and read them through one L2.  A queue is taken from both ends, by
+// every other workgroup of an XCD from the back: where a list holds tall
+// tiles (bound by the matrix unit) and short ones (weight streams), some
+// compute units run the one kind beside the other.
 //
-// A head counts draws from the front (low word) and from the back (high
-// word) of its queue.  Every workgroup draws exactly once past the end of
-// every queue, so the draw that makes the count items + grid is the head's
-// last of the launch and sets it back to zero, as the plan left it.
+// The first item of a workgroup is fixed; more are drawn from the head of
+// its queue, which counts draws from the front (low word) and from the back
+// (high word), one item ahead so that the draw's latency passes under the
+// work.  When its own queue is dry a workgroup looks at all heads at once and
+// goes on with a queue that has items left.  The last workgroup to leave
+// sets the heads back to zero, as the plan left them: every draw of another
+// has returned before that one counts itself out.
 struct M4Queues {
-  unsigned long long *heads;
+  M4Heads *h;
   int nbig, nsmall, ptb, pts;
-  int q, left;
-  __device__ __forceinline__ M4Queues(unsigned long long *heads_, int nbig_, int nsmall_, int ptb_,
-                                      int pts_)
-      : heads(heads_), nbig(nbig_), nsmall(nsmall_), ptb(ptb_), pts(pts_) {
-    q = vreg((int)blockIdx.x) & (kM4Queues - 1);
-    left = kM4Queues;
+  int q, G;
+  bool back;
+  __device__ __forceinline__ M4Queues(M4Heads *h_, int nbig_, int nsmall_, int ptb_, int pts_)
+      : h(h_), nbig(nbig_), nsmall(nsmall_), ptb(ptb_), pts(pts_) {
+    const int b = vreg((int)blockIdx.x);
+    G = vreg((int)gridDim.x);
+    q = b % kM4Queues;
+    back = (b / kM4Queues) & 1;
   }
-  // the next item: tile and which of its items; false if none is left
-  __device__ __forceinline__ bool next(int *tile, int *part) {
-    const bool back = (vreg((int)blockIdx.x) / kM4Queues) & 1;
-    for (; left > 0; --left, q = (q + 1) & (kM4Queues - 1)) {
-      const int tall = (nbig - q + kM4Queues - 1) / kM4Queues;  // tall tiles of this queue
-      const int all = (nbig + nsmall - q + kM4Queues - 1) / kM4Queues;
-      const int n = tall * ptb + (all - tall) * pts;
-      const unsigned long long v = atomicAdd(heads + q, back ? 1ull << 32 : 1ull);
-      const int f = (int)(uint32_t)v, b = (int)(v >> 32);
-      if (f + b < n) {
-        const int i = back ? n - 1 - b : f;
-        const int j = i < tall * ptb ? i / ptb : tall + (i - tall * ptb) / pts;
-        *part = i < tall * ptb ? i - j * ptb : i - tall * ptb - (j - tall) * pts;
-        *tile = q + j * kM4Queues;
-        return true;
+  __device__ __forceinline__ int tall(int p) const { return (nbig - p + kM4Queues - 1) / kM4Queues; }
+  __device__ __forceinline__ int items(int p) const {
+    const int all = (nbig + nsmall - p + kM4Queues - 1) / kM4Queues, t = tall(p);
+    return t * ptb + (all - t) * pts;
+  }
+  // items of queue p left after v; fixed first items count as drawn
+  __device__ __forceinline__ int rest(int p, unsigned long long v) const {
+    const int owners = (G - p + kM4Queues - 1) / kM4Queues;
+    return items(p) - owners - (int)(uint32_t)v - (int)(v >> 32);
+  }
+  __device__ __forceinline__ bool item(int i, int *tile, int *part) const {
+    const int t = tall(q);
+    const int j = i < t * ptb ? i / ptb : t + (i - t * ptb) / pts;
+    *part = i < t * ptb ? i - j * ptb : i - t * ptb - (j - t) * pts;
+    *tile = q + j * kM4Queues;
+    return true;
+  }
+  __device__ __forceinline__ bool first(int *tile, int *part) const {
+    const int rank = vreg((int)blockIdx.x) / kM4Queues / 2, n = items(q);
+    if (rank >= (back ? n / 2 : (n + 1) / 2)) return false;
+    return item(back ? n - 1 - rank : rank, tile, part);
+  }
+  __device__ __forceinline__ unsigned long long draw() const {
+    return atomicAdd(&h->head[q], back ? 1ull << 32 : 1ull);
+  }
+  // The item that draw() gave, or one of another queue; false if none is left.
+  __device__ __forceinline__ bool take(unsigned long long v, int *tile, int *part) {
+    for (;;) {
+      if (rest(q, v) > 0) {
+        const int owners = (G - q + kM4Queues - 1) / kM4Queues;
+        const int i = back ? items(q) - 1 - owners / 2 - (int)(v >> 32)
+                           : (owners + 1) / 2 + (int)(uint32_t)v;
+        return item(i, tile, part);
       }
-      if (f + b == n + (int)gridDim.x - 1)
-        __hip_atomic_store(heads + q, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      unsigned long long heads[kM4Queues];
+#pragma unroll
+      for (int p = 0; p < kM4Queues; ++p)
+        heads[p] = __hip_atomic_load(&h->head[p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      int most = 0, to = 0;
+#pragma unroll
+      for (int p = 0; p < kM4Queues; ++p) {
+        const int n = rest(p, heads[p]);
+        if (n > most) {
+          most = n;
+          to = p;
+        }
+      }
+      if (most == 0) break;
+      q = to;
+      v = draw();
+    }
+    if (atomicAdd(&h->left, 1) == G - 1) {
+#pragma unroll
+      for (int p = 0; p < kM4Queues; ++p)
+        __hip_atomic_store(&h->head[p], 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&h->left, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     return false;
   }
@@ -605,36 +706,35 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
   const uint32_t ring_lds = lds_addr(ring);
   constexpr int kHalf = GATEUP ? 2 : 1;  // gate and up rows of one feature
   constexpr int FB = kM4WRows / kHalf;           // features per item of the taller tiles
-  constexpr int FS = 2 * kM4WRowsSmall / kHalf;  // and of the 32-row tiles
+  constexpr int FS = 4 * kM4WRowsSmall / kHalf;  // and of the 32-row tiles
   const int N = vreg(a.N);
   const int nsmall = vreg(*a.n_small), nbig = vreg(*a.ntiles) - nsmall;
   const int ptb = (N + FB - 1) / FB, pts = (N + FS - 1) / FS;  // items per tile
   M4Queues queues(a.heads, nbig, nsmall, ptb, pts);
+  unsigned long long drawn = 0;
+  bool begin = true;
   for (;;) {
     if (threadIdx.x == 0) {
-      int ti, part;
-      const bool some = queues.next(&ti, &part);
+      int ti = -1, part = 0;
+      bool some = begin && queues.first(&ti, &part);
+      if (begin && !some) drawn = queues.draw();
+      if (!some) some = queues.take(drawn, &ti, &part);
+      begin = false;
       next_item[0] = some ? ti : -1;
       next_item[1] = some ? part * (ti < nbig ? FB : FS) : 0;
       next_item[2] = a.K;
-      m4_put(next_item + 4, a.s0);
-      m4_put(next_item + 6, a.s1);
-      m4_put(next_item + 8, a.out);
     }
     __syncthreads();
     // read before the item's first barrier (its loads overwrite it); the
-    // reduction length and some of the pointers come through LDS so that
-    // they, and what derives from them, are not held in scalar registers
-    // across the loop (they do not fit)
+    // reduction length comes through LDS so that nothing derived from it is
+    // hoisted out of the loop into the scalar registers
     const int ti = __builtin_amdgcn_readfirstlane(next_item[0]);
     if (ti < 0) break;
     const int n0 = __builtin_amdgcn_readfirstlane(next_item[1]);
     Mx4Args ai = a;
     ai.K = __builtin_amdgcn_readfirstlane(next_item[2]);
-    ai.s0 = static_cast<const uint8_t *>(m4_get(next_item + 4));
-    ai.s1 = static_cast<const uint8_t *>(m4_get(next_item + 6));
-    ai.out = m4_get(next_item + 8);
     const Tile t = a.tiles[ti];
+    if (threadIdx.x == 0) drawn = queues.draw();  // for the item after this one
     switch (tile_class(t)) {
       case 8: m4_item<GATEUP, false, 256, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
       case 6: m4_item<GATEUP, false, 192, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
@@ -642,7 +742,7 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
       case 2: m4_item<GATEUP, false, 64, kM4WRows, 2>(ai, t, n0, 1, ring, ring_lds); break;
       default: {
         const int n1 = min(n0 + FS, ai.N);
-        const int nb = (n1 - n0) * 2 / FS;
+        const int nb = (n1 - n0) * 4 / FS;
         if (m4_direct_fits(t, ai.K))
           m4_direct<GATEUP>(ai, t, n0, n1, ring);
         else if (t.ablk & kTileStream)
@@ -659,20 +759,15 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
 }
 
 hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream) {
-  // the queue heads of the two projections, in the free words of the schedule
-  static_assert(sizeof(L.sch->pad) >= 2 * kM4Queues * 8, "room for the heads");
-  unsigned long long *heads = reinterpret_cast<unsigned long long *>(L.sch + 1) - 2 * kM4Queues;
-  if (stages & kStagePlan) {
-    hipError_t err = launch_grouped_schedule(L.offsets, L.E, L.sch, L.tiles, stream);
-    if (err == hipSuccess)
-      err = launch_zero_u32(reinterpret_cast<uint32_t *>(heads), 4 * kM4Queues, stream);
-    if (err != hipSuccess) return err;
-  }
+  M4Schedule *sch = reinterpret_cast<M4Schedule *>(L.sch);
+  if (stages & kStagePlan)
+    hipLaunchKernelGGL(mx4_schedule_kernel, dim3(1), dim3(kM4ScheduleThreads), 0, stream, L.offsets,
+                       L.E, sch, L.tiles);
   Mx4Args g{};
   g.k = L.k;
   g.tiles = L.tiles;
-  g.ntiles = &L.sch->n_tiles;
-  g.n_small = &L.sch->n_small;
+  g.ntiles = &sch->n_tiles;
+  g.n_small = &sch->n_small;
   if (stages & kStageGateUp) {
     g.act = L.x;
     g.sorted_routes = L.sorted_routes;
@@ -683,7 +778,7 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
     g.out = L.h;
     g.N = L.f;
     g.K = L.d;
-    g.heads = heads;
+    g.heads = &sch->heads[0];
     hipLaunchKernelGGL(grouped_gemm_mx4_kernel<true>, dim3(L.num_cus), dim3(kM4Threads), 0, stream,
                        g);
   }
@@ -697,7 +792,7 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
     g.out = L.y;
     g.N = L.d;
     g.K = L.f;
-    g.heads = heads + kM4Queues;
+    g.heads = &sch->heads[1];
     hipLaunchKernelGGL(grouped_gemm_mx4_kernel<false>, dim3(L.num_cus), dim3(kM4Threads), 0,
                        stream, g);
   }
