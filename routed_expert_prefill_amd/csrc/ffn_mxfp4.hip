@@ -10,12 +10,6 @@
 // The order of the reduction inside a stage follows from that: lane half h
 // of a 64-column step holds group h of it, and MFMA j of the step multiplies
 // columns 8 j .. 8 j + 7 of both groups.
-//
-// A stage is KB blocks of 64 columns: the activation rows' 128-byte lines of
-// each block, 32 KB bytes of codes per weight row, and the groups' scales.
-// KB = 4 makes the codes of a row whole 128-byte lines, which HBM streams at
-// full rate; tall tiles, bound by the matrix unit and re-reading weights
-// through the caches, take KB = 1 so that three stages fit in LDS.
 #include "kernels.h"
 #include "mx4.h"
 #include "ring.h"
@@ -33,7 +27,7 @@ struct M4Heads {
 // What the plan leaves at the start of the workspace.
 struct M4Schedule {
   int n_tiles;  // entries of the tile list, tallest capacity first
-  int n_small;  // 32-row tiles, the last n_small entries
+  int n_small;  // tiles of at most kM4DirectRows rows, the last n_small entries
   int pad[2];
   M4Heads heads[2];  // gate/up, down
 };
@@ -49,46 +43,61 @@ struct Mx4Args {
   int N, K;
   const Tile *tiles;
   const int *ntiles;
-  const int *n_small;  // 32-row tiles at the end of the tile list
+  const int *n_small;  // tiles of at most kM4DirectRows rows at the end of the tile list
   M4Heads *heads;      // of the work queues (M4Queues), zeroed by the plan
 };
 
 constexpr int kM4Threads = 512;
 constexpr int kM4Waves = kM4Threads / kWave;
-constexpr int kM4Ring = 160 * 1024;  // the whole LDS of a workgroup
+constexpr int kM4Lds = 160 * 1024;  // the whole LDS of a workgroup
+constexpr int kM4Ring = kM4Lds - 64;  // what the items use of it
+constexpr int kM4WRows = 256;        // weight rows per item of the ring
 
-// Geometry of an item with AR activation rows, WR weight rows and KB
-// 64-column blocks per stage.
-template <int AR, int WR, int KB>
-struct M4Ring {
+// How an item of 256 weight rows and AR activation rows is laid out.
+//
+// Activations come in stages of KB 64-column blocks (a 128-byte line of each
+// row per block), NS slots; codes in groups of GB blocks (16 GB bytes of each
+// weight row), NB buffers.  Whole 128-byte lines of codes (GB = 4) matter:
+// with 32-byte pieces in step with 64-column stages the requests of the codes
+// alone, one per row and piece, were more than those of the activations
+// (MI355X, 8192 tokens: gate/up without its products 1.10 ms).  Scales: 16 bytes per row for 8 blocks, two buffers.
+//
+// Split: tiles of up to 64 rows.  Wave w takes weight tiles 2 (w % 4) and
+// 2 (w % 4) + 1, every activation tile, and block w / 4 of each stage's two;
+// the two halves of the sums meet in LDS at the end.  Each weight is decoded
+// once and each activation tile read serves two products.  Taller tiles:
+// wave w takes the same weight tiles and half w / 4 of the activation tiles.
+template <int AR>
+struct M4Layout {
+  static constexpr bool kSplit = AR <= 64;
+  static constexpr int KB = kSplit ? 2 : 1;
+  static constexpr int GB = AR == 256 ? 2 : 4;
+  static constexpr int NB = kSplit || AR == 256 ? 3 : 2;
+  static constexpr int S = GB / KB;  // stages per group of codes
+  static constexpr int TT = kSplit ? AR / 32 : AR / 64;
+  static constexpr int TW = 2;
   static constexpr int kAct = AR * 128 * KB;
-  static constexpr int kCodes = WR * 32 * KB;
-  static constexpr int kSlot = kAct + kCodes;
-  // Scales come in groups of 16 bytes per weight row, for kGroup stages.  A
-  // group is loaded with its first stage and read until its last, so two
-  // buffers do if a group is at least as long as the ring (less one stage);
-  // items of several blocks, whose groups end with each block, have one
-  // buffer per slot.
-  static constexpr int kGroup = 8 / KB;
-  static constexpr int kScales = WR * 16;
-  static constexpr bool kSmall = AR <= 32;
-  // small tiles: waves 4-7 hand their sums to waves 0-3 behind the ring
-  static constexpr int kSums = kSmall ? 4 * 4096 : 0;
-  static constexpr int kFit = kSmall ? (kM4Ring - kSums) / (kSlot + kScales)
-                                     : (kM4Ring - 2 * kScales) / kSlot;
-  static constexpr int kDepth = kFit < 8 ? kFit : 8;
-  static constexpr int kBuffers = kSmall ? kDepth : 2;
-  static_assert(kSmall || kGroup >= kDepth - 1, "two buffers of scales");
-  static constexpr int kScaleBase = kDepth * kSlot;
-  static_assert(kScaleBase + kBuffers * kScales + kSums <= kM4Ring, "fits");
+  static constexpr int kCodes = kM4WRows * 16 * 2 * GB;
+  static constexpr int kScales = kM4WRows * 16;
+  static constexpr int kFit = (kM4Ring - NB * kCodes - 2 * kScales) / kAct;
+  // a group of codes is loaded ahead of the stage that follows its first one,
+  // so that only the activations decide what a stage waits for
+  static constexpr int kMost = (NB - 1) * S + 1;
+  static constexpr int NS = kFit < kMost ? kFit : kMost;
+  static constexpr int kCodeBase = NS * kAct;
+  static constexpr int kScaleBase = kCodeBase + NB * kCodes;
+  static_assert(NS >= 2 && kScaleBase + 2 * kScales <= kM4Ring, "fits");
+  static_assert(!kSplit || 4 * TW * TT * 4096 <= kM4Ring, "the sums fit");
+  __device__ static int atile(int wv, int tt) { return kSplit ? tt : (wv >> 2) * TT + tt; }
+  __device__ static int wtile(int wv, int tw) { return (wv & 3) * 2 + tw; }
 };
 
 // 16-byte chunk c of the codes of weight row r is stored at this slot of the
-// row's 2 KB: 16 lanes reading one chunk of 16 consecutive rows then touch
+// row's 2 GB: 16 lanes reading one chunk of 16 consecutive rows then touch
 // 16 distinct 16-byte slots of a 256-byte window.
-template <int KB>
+template <int GB>
 __device__ __forceinline__ int m4_slot(int r, int c) {
-  return c ^ ((r / (8 / KB)) & (2 * KB - 1));
+  return c ^ ((r / (8 / GB)) & (2 * GB - 1));
 }
 
 // Direct global->LDS load of 4 bytes per lane to LDS byte address
@@ -100,65 +109,73 @@ __device__ __forceinline__ void dma4(const void *src, uint32_t lds_byte_addr) {
                : "memory");
 }
 
-// Wave wv multiplies TT activation tiles by TW weight tiles of 32 rows.  With
-// at most 32 activation rows (and 128 weight rows) four waves would do, so
-// the other four take the second half of each stage's columns.
-template <int AR>
-struct M4Layout {
-  static constexpr bool kSplit = AR <= 32;
-  static constexpr int TT = kSplit ? 1 : AR / 64;
-  static constexpr int TW = kSplit ? 1 : 2;
-  __device__ static int atile(int wv, int tt) { return kSplit ? 0 : (wv >> 2) * TT + tt; }
-  __device__ static int wtile(int wv, int tw) { return kSplit ? (wv & 3) : (wv & 3) * 2 + tw; }
-};
+// The loads of ring.h from a uniform base plus a 32-bit offset per lane.
+__device__ __forceinline__ void m4_dma16(const void *base, uint32_t off, uint32_t lds_byte_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds_byte_addr)
+               : "memory");
+}
+__device__ __forceinline__ void m4_dma16_nt(const void *base, uint32_t off, uint32_t lds_byte_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+               :
+               : "v"(off), "s"(base), "s"(lds_byte_addr)
+               : "memory");
+}
 
 __device__ __forceinline__ f32x4 m4_quad(const f32x16 &v, int g) {
   return f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
 }
 
-// nb feature blocks of one tile, streamed through one ring fill.
-// NT: codes through non-temporal loads (whole lines only: KB == 4).
-template <bool GATEUP, bool NT, int AR, int WR, int KB>
-__device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0, int nb_arg,
-                                        uint8_t *ring, uint32_t ring_lds) {
-  static_assert(!NT || KB == 4, "half lines must not bypass the caches");
+// How many of the n stages before stage i of a group of S are first in theirs.
+__host__ __device__ constexpr int m4_firsts(int i, int n, int S) {
+  int c = 0;
+  for (int u = 1; u <= n; ++u) c += (i - u + 64 * S) % S == 0 ? 1 : 0;
+  return c;
+}
+
+// The steady wait of stage i of a group (below); i is a constant once unrolled.
+template <int JA, int JW, int NS, int S>
+__device__ __forceinline__ void m4_wait(int i) {
+  const int firsts = m4_firsts(i, NS - 1, S);
+  if (firsts == 0)
+    wait_vm_imm<JA *(NS - 2)>();
+  else if (firsts == 1)
+    wait_vm_imm<JA *(NS - 2) + JW>();
+  else
+    wait_vm_imm<JA *(NS - 2) + 2 * JW>();
+}
+
+// 256 weight rows (features from n0) of a tile of up to AR rows.
+template <bool GATEUP, int AR>
+__device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0, uint8_t *ring,
+                                        uint32_t ring_lds) {
   using L = M4Layout<AR>;
-  using G = M4Ring<AR, WR, KB>;
-  static_assert(L::kSplit ? WR == 128 && KB == 4 : WR == 256 && AR % 64 == 0, "wave layout");
-  constexpr bool MB = L::kSplit;  // several blocks only where items are short
-  constexpr int FEAT = GATEUP ? WR / 2 : WR;  // output features per block
+  constexpr int KB = L::KB, GB = L::GB, NB = L::NB, S = L::S, NS = L::NS;
   constexpr int TT = L::TT, TW = L::TW;
-  constexpr int NA = KB * AR / 8;      // activation loads: 8 rows of 128 bytes
-  constexpr int NW = WR * KB / 32;     // code loads: 1 KB
-  // load i of a kind goes to wave i % 8
-  static_assert(NA % kM4Waves == 0 && NW % kM4Waves == 0, "even shares");
-  constexpr int JA = NA / kM4Waves, JW = NW / kM4Waves;
-  constexpr int NS = G::kDepth;
-  static_assert(NS >= 2 && (JA + JW) * (NS - 2) <= 32, "wait_vm counts to 32");
-  const int nb = MB ? nb_arg : 1;
+  constexpr int JA = KB * AR / 8 / kM4Waves;       // activation loads (8 rows) of a wave per stage
+  constexpr int JW = kM4WRows * GB / 32 / kM4Waves;  // code loads (1 KB) of a wave per group
   const int lane = lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int K = a.K;
-  const int nst = (K / 64 + KB - 1) / KB;
-  const bool half = KB == 4 && (K & 128) != 0;  // the last stage has two blocks only
-  // loads of this wave per stage, scales left out: where they are in flight
-  // the wait below ends a load later than it has to
-  const int cnt = JA + JW;
+  const int nst = K / (64 * KB);
+  const int ngr = (K / 64 + GB - 1) / GB;
+  const bool half = GB == 4 && (K & 128) != 0;  // the last group has two blocks only
+  // the codes of an expert's only tile are read once: past the caches, in whole lines
+  const bool nt = L::kSplit && (t.ablk & kTileStream);
 
-  auto wrow = [&](int wr, const uint8_t *p0, const uint8_t *p1, int row_bytes) {
-    const uint8_t *w = p0;
-    int n;
-    if (GATEUP) {  // 16-row groups alternate gate and up
-      if ((wr >> 4) & 1) w = p1;
-      n = n0 + (wr >> 5) * 16 + (wr & 15);
-    } else {
-      n = min(n0 + wr, a.N - 1);
-    }
-    return w + ((size_t)t.e * a.N + n) * row_bytes;
+  // Weight row wr of the item: a row of the first or second matrix (gate/up:
+  // 16-row groups alternate), counted from feature n0.
+  auto wmat = [&](int wr) { return GATEUP ? (wr >> 4) & 1 : 0; };
+  auto wrow = [&](int wr) {
+    return GATEUP ? (wr >> 5) * 16 + (wr & 15) : min(wr, a.N - 1 - n0);
   };
-  // this lane's source of each of its loads at stage 0.  In a half stage the
-  // sources of the missing second half move back to the first (loaded, not used).
-  const uint8_t *act[JA], *codes[JW];
+  const size_t first = (size_t)t.e * a.N + n0;
+  const uint8_t *const w0 = a.w0 + first * (K / 2), *const w1 = GATEUP ? a.w1 + first * (K / 2) : w0;
+  const uint8_t *const s0 = a.s0 + first * (K / 32), *const s1 = GATEUP ? a.s1 + first * (K / 32) : s0;
+  // this lane's source of each of its loads in the first stage and group
+  const uint8_t *act[JA];
+  uint32_t codes[JW];
 #pragma unroll
   for (int j = 0; j < JA; ++j) {
     const int i = wv + kM4Waves * j;
@@ -169,227 +186,243 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     act[j] = reinterpret_cast<const uint8_t *>(a.act + s * K) + kb * 128 +
              ring_slot(r, lane & 7) * 16;
   }
-  constexpr int LPR = 2 * KB;  // lanes per row of codes
-  int code_back = 0;
+  constexpr int LPR = 2 * GB;  // lanes per row of codes; the rows of a load are of one matrix
+  constexpr int RPL = 64 / LPR;
+  int second = 0;  // bit j: load j brings columns of the group's second half
 #pragma unroll
   for (int j = 0; j < JW; ++j) {
-    const int r = (wv + kM4Waves * j) * (64 / LPR) + lane / LPR;
-    const int c = m4_slot<KB>(r, lane % LPR);
-    codes[j] = wrow(r, a.w0, a.w1, K / 2) + c * 16;
-    code_back |= (c >= 4 ? 1 : 0) << j;
+    const int r = (wv + kM4Waves * j) * RPL + lane / LPR;
+    const int c = m4_slot<GB>(r, lane % LPR);
+    codes[j] = (uint32_t)wrow(r) * (K / 2) + c * 16;
+    second |= (c >= 4 ? 1 : 0) << j;
   }
-  // Scales of a group: where rows start on 16-byte borders, one load of 16
-  // bytes per lane and 64 rows by each of the last WR / 64 waves; elsewhere
-  // loads of 4 bytes per lane and 16 rows.  Both leave 16 bytes per row in LDS.
-  constexpr int SW = WR / 64;
-  const bool wide = (K & 511) == 0;
-  const int swv = wv - (kM4Waves - SW);
-  const int srow = wide ? max(swv, 0) * 64 + lane : wv * (WR / 8) + (lane >> 2);
-  const uint8_t *scales = wrow(srow, a.s0, a.s1, K / 32);
-  int group = 0;  // groups loaded so far
-  auto issue_scales = [&](int s, int b) {
-    const uint32_t to = ring_lds + (uint32_t)G::kScaleBase +
-                        (unsigned)group % (unsigned)G::kBuffers * G::kScales;
-    ++group;
-    uint32_t off = (uint32_t)s * (2 * KB) + (MB ? (uint32_t)(b * FEAT) * (K / 32) : 0);
-    if (wide) {
-      if (swv >= 0) dma16(scales + off, to + (uint32_t)swv * 1024u);
+  // Scales: where rows start on 16-byte borders, one load of 16 bytes per
+  // lane and 64 rows by waves 4-7 (32 rows of each matrix for gate/up);
+  // elsewhere loads of 4 bytes per lane and 16 rows.  Both leave 16 bytes per
+  // row in LDS.
+  const int aligned = vreg((K & 511) == 0);  // in a vector register, for want of a scalar one
+  const bool wide = __builtin_amdgcn_readfirstlane(aligned);
+  const int srow = wide ? max(wv - 4, 0) * 64 + lane : wv * 32 + (lane >> 2);
+  const uint8_t *scales = (wmat(srow) ? s1 : s0) + (size_t)wrow(srow) * (K / 32);
+  const uint8_t *scales16 = (wmat(srow + 16) ? s1 : s0) + (size_t)wrow(srow + 16) * (K / 32);
+
+  auto issue_code = [&](int j, int g, int buf) {
+    const int i = wv + kM4Waves * j;
+    const uint8_t *base = (wmat(i * RPL) ? w1 : w0) + (uint32_t)g * (32 * GB);
+    uint32_t off = codes[j];
+    // half a group: its first half twice (loaded, not used)
+    if (GB == 4 && half && g == ngr - 1) off -= ((second >> j) & 1) * 64;
+    const uint32_t to = ring_lds + (uint32_t)(L::kCodeBase + buf * L::kCodes + i * 1024);
+    if (nt)
+      m4_dma16_nt(base, off, to);
+    else
+      m4_dma16(base, off, to);
+  };
+  auto issue_scales = [&](int g) {
+    if (g % (8 / GB) != 0) return;
+    const uint32_t to = ring_lds + (uint32_t)L::kScaleBase + (uint32_t)(g / (8 / GB) & 1) * L::kScales;
+    uint32_t off = (uint32_t)g * (2 * GB);
+    if (__builtin_amdgcn_readfirstlane(aligned)) {
+      if (wv >= 4) dma16(scales + off, to + (uint32_t)(wv - 4) * 1024u);
     } else {
       // words past the row's end are not there: the group's first instead
-      off += (s * KB + (lane & 3) * 2) * 64 < K ? (lane & 3) * 4 : 0;
-      dma4(scales + off, to + (uint32_t)wv * (WR * 2u));
-      if (WR == 256)
-        dma4(wrow(srow + 16, a.s0, a.s1, K / 32) + off, to + (uint32_t)wv * (WR * 2u) + 256u);
+      off += (g * GB + (lane & 3) * 2) * 64 < K ? (lane & 3) * 4 : 0;
+      dma4(scales + off, to + (uint32_t)wv * 512u);
+      dma4(scales16 + off, to + (uint32_t)wv * 512u + 256u);
     }
   };
-  // loads of stage s of block b
-  auto issue = [&](int s, int b, int slot) {
-    const uint32_t base = ring_lds + (uint32_t)(slot * G::kSlot) + (uint32_t)wv * 1024u;
-    const bool cut = half && s == nst - 1;
-    const uint32_t act_off = (uint32_t)s * (128 * KB);
-    const uint32_t code_off = (uint32_t)s * (32 * KB) + (MB ? (uint32_t)(b * FEAT) * (K / 2) : 0);
-#pragma unroll
-    for (int j = 0; j < JA; ++j) {
-      const uint8_t *p = act[j] + act_off;
-      if (KB == 4 && cut && (wv + kM4Waves * j) / (AR / 8) >= 2) p -= 256;
-      dma16(p, base + (uint32_t)j * (kM4Waves * 1024u));
-    }
-#pragma unroll
-    for (int j = 0; j < JW; ++j) {
-      const uint8_t *p = codes[j] + code_off;
-      if (KB == 4 && cut) p -= ((code_back >> j) & 1) * 64;
-      const uint32_t to = base + (uint32_t)G::kAct + (uint32_t)j * (kM4Waves * 1024u);
-      if (NT)
-        dma16_nt(p, to);
-      else
-        dma16(p, to);
-    }
-    if (s % G::kGroup == 0) issue_scales(s, b);
+  auto issue_act = [&](int j, int s, int slot) {
+    dma16(act[j] + (uint32_t)s * (128 * KB),
+          ring_lds + (uint32_t)(slot * L::kAct + (wv + kM4Waves * j) * 1024));
   };
 
   const int rr = lane & 31, rh = lane >> 5;
   f32x16 acc[TW][TT];
-  auto zero_acc = [&]() {
+#pragma unroll
+  for (int tw = 0; tw < TW; ++tw)
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[tw][tt][j] = 0.f;
+
+  // this wave's MFMAs of stage i of group g: activations in `slot`, codes in `buf`
+  // with between(j) after the MFMAs of step j
+  auto mma_stage = [&](int g, int i, int slot, int buf, auto between) {
+    const int q = L::kSplit ? wv >> 2 : 0;  // this wave's block of the stage
+    const uint8_t *ap = ring + slot * L::kAct + q * (AR * 128);
+    const uint8_t *cp = ring + L::kCodeBase + buf * L::kCodes;
+    // the scales' two bytes of block b = g GB + i KB + q of the row's
+    const uint8_t *sp = ring + L::kScaleBase + (g / (8 / GB) & 1) * L::kScales +
+                        (g * (GB / 2) & 3) * 4 + (i * KB + q) / 2 * 4;
+    const int shift = 8 * rh + 16 * ((i * KB + q) & 1);
+    // Activations of step j + 1 are read ahead of the products of step j
+    // (8192 tokens: gate/up 1.66 -> 1.59 ms), for which the registers of
+    // 256-row tiles do not suffice.
+    constexpr bool AHEAD = AR < 256;
+    bf16x8 fa[AHEAD ? 2 : 1][TT];
+    auto read_act = [&](int j) {
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+        fa[AHEAD ? j & 1 : 0][tt] = *reinterpret_cast<const bf16x8 *>(
+            ap + (L::atile(wv, tt) * 32 + rr) * 128 + ring_slot(rr, 4 * rh + j) * 16);
+    };
+    i32x4 raw[TW];
+    uint32_t word[TW];
+#pragma unroll
+    for (int tw = 0; tw < TW; ++tw) {
+      const int r = L::wtile(wv, tw) * 32 + rr;
+      raw[tw] = *reinterpret_cast<const i32x4 *>(cp + r * (32 * GB) +
+                                                 m4_slot<GB>(r, 2 * (i * KB + q) + rh) * 16);
+      word[tw] = *reinterpret_cast<const uint32_t *>(sp + r * 16);
+    }
+    read_act(0);
+    float scale[TW];
+#pragma unroll
+    for (int tw = 0; tw < TW; ++tw) scale[tw] = mx4_scale((word[tw] >> shift) & 0xffu);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (AHEAD) {
+        if (j < 3) read_act(j + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      } else if (j > 0) {
+        read_act(j);
+      }
+#pragma unroll
+      for (int tw = 0; tw < TW; ++tw) {
+        const bf16x8 fw = mx4_decode8((uint32_t)raw[tw][j], scale[tw]);
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) acc[tw][tt] = mfma32_bf16(fw, fa[AHEAD ? j & 1 : 0][tt], acc[tw][tt]);
+      }
+      between(j);
+    }
+  };
+
+  ring_barrier();  // every wave has read its item, which lies in the ring
+  auto issue_group = [&](int g) {
+#pragma unroll
+    for (int j = 0; j < JW; ++j) issue_code(j, g, g);
+    issue_scales(g);
+  };
+  issue_group(0);
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) {
+    if (s < nst) {
+#pragma unroll
+      for (int j = 0; j < JA; ++j) issue_act(j, s, s);
+    }
+  }
+#pragma unroll
+  for (int g = 1; g < NB - 1; ++g)
+    if (g < ngr) issue_group(g);
+  int slot = 0, buf = 0;  // of the stage being multiplied
+  static_assert(NS - 1 <= S, "the first group's stages are loaded ahead of the loop");
+#pragma unroll 1
+  for (int g = 0; g < ngr; ++g) {
+    // What may stay in flight at the start of stage s: the activations of the
+    // NS - 2 stages after it, and the codes that went out since its own
+    // activations did (with the first stage of a group, after that stage's
+    // activations).  Between the first group and the last NB that is a
+    // constant.  Scales are not counted: the wait is then one load longer.
+    const bool steady = g > 0 && g + NB < ngr;
+    const bool codes_too = g + NB - 1 < ngr;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const int s = g * S + i;
+      if (GB == 4 && i >= S / 2 && s >= nst) break;  // half a group
+      if (steady) {
+        m4_wait<JA, JW, NS, S>(i);
+      } else {
+        int n = JA * min(NS - 2, nst - 1 - s);
+        if (s <= NS - 2) n += JW * min(NB - 2, ngr - 1);  // issued ahead of the loop
+#pragma unroll
+        for (int x = 1; x < NS; ++x) {
+          const int h = g - (x - i + S - 1) / S;  // the group of stage s - x if that is its first
+          if (x >= i && (x - i) % S == 0 && h >= 0 && h + NB - 1 < ngr) n += JW;
+        }
+        wait_vm(n);
+      }
+      ring_barrier();  // the stage is in LDS for everyone; stage s - 1 is consumed
+      // the next loads go out between the products: all at once, ahead of
+      // them, they kept the waves from starting
+      const bool more = s + NS - 1 < nst;
+      mma_stage(g, i, slot, buf, [&](int j) {
+        constexpr int N = JA + JW;
+        const int to_slot = slot == 0 ? NS - 1 : slot - 1, to_buf = buf == 0 ? NB - 1 : buf - 1;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+          if (x * 4 / N != j) continue;
+          if (x < JA) {
+            if (more) issue_act(x, s + NS - 1, to_slot);
+          } else if (i == 0 && codes_too) {
+            issue_code(x - JA, g + NB - 1, to_buf);
+            if (x == N - 1) issue_scales(g + NB - 1);
+          }
+        }
+      });
+      slot = slot == NS - 1 ? 0 : slot + 1;
+    }
+    buf = buf == NB - 1 ? 0 : buf + 1;
+  }
+
+  if constexpr (L::kSplit) {
+    f32x4 *sums = reinterpret_cast<f32x4 *>(ring) + (wv & 3) * (TW * TT * 256) + lane;
+    ring_barrier();  // the ring makes room for the sums of waves 4-7
+    if (wv >= 4) {
+#pragma unroll
+      for (int tw = 0; tw < TW; ++tw)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            sums[((tw * TT + tt) * 4 + g) * kWave] = m4_quad(acc[tw][tt], g);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    ring_barrier();
+    if (wv >= 4) return;
 #pragma unroll
     for (int tw = 0; tw < TW; ++tw)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[tw][tt][j] = 0.f;
-  };
-
-  // the MFMAs of one ring stage; sbuf: the buffer with its group of scales
-  auto mma_stage = [&](const uint8_t *buf, const uint8_t *sbuf, int s) {
-    if (L::kSplit && wv >= 4 && half && s == nst - 1) return;  // no second half there
-    constexpr int KW = L::kSplit ? KB / 2 : KB;  // blocks of this wave
-    const int kb0 = L::kSplit ? (wv >> 2) * 2 : 0;
-    // two scales per block and four to a word: the word of this wave's blocks
-    const int word = L::kSplit ? (s & 1) * 2 + (wv >> 2) : KB == 2 ? s & 3 : (s >> 1) & 3;
-    uint32_t sc[TW];
-    i32x4 raw[KW][TW];
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 v = sums[((tw * TT + tt) * 4 + g) * kWave];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[tw][tt][4 * g + i] += v[i];
+        }
+  }
+  // register j of a 32x32 tile holds weight row 8*(j/4) + 4*rh + j%4, activation row rr
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt) {
+    const int r = L::atile(wv, tt) * 32 + rr;
+    if (r >= t.nrows) continue;
+    const size_t row = (size_t)(t.row0 + r);
 #pragma unroll
     for (int tw = 0; tw < TW; ++tw) {
-      const int r = L::wtile(wv, tw) * 32 + rr;
-      sc[tw] = *reinterpret_cast<const uint32_t *>(sbuf + r * 16 + word * 4) >>
-               (8 * rh + (KB == 1 ? 16 * (s & 1) : 0));
+      const int wt = L::wtile(wv, tw);
+      if (GATEUP) {
+        // rows 0-15 of the tile are gate features 16 wt + [0,16), rows 16-31 the same up features
 #pragma unroll
-      for (int q = 0; q < KW; ++q)
-        raw[q][tw] = *reinterpret_cast<const i32x4 *>(
-            buf + G::kAct + r * (32 * KB) + m4_slot<KB>(r, 2 * (kb0 + q) + rh) * 16);
-    }
-    auto load_act = [&](int q, int j, bf16x8 (&fa)[TT]) {
+        for (int g = 0; g < 2; ++g) {
+          const f32x4 gv = m4_quad(acc[tw][tt], g), uv = m4_quad(acc[tw][tt], g + 2);
+          const int n = n0 + wt * 16 + g * 8 + rh * 4;
+          uint2 v;
+          v.x = (uint32_t)f32_to_bf16_bits(swiglu(gv[0], uv[0])) |
+                ((uint32_t)f32_to_bf16_bits(swiglu(gv[1], uv[1])) << 16);
+          v.y = (uint32_t)f32_to_bf16_bits(swiglu(gv[2], uv[2])) |
+                ((uint32_t)f32_to_bf16_bits(swiglu(gv[3], uv[3])) << 16);
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.N + n) = v;
+        }
+      } else {
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        const int r = L::atile(wv, tt) * 32 + rr;
-        fa[tt] = *reinterpret_cast<const bf16x8 *>(buf + (kb0 + q) * (AR * 128) + r * 128 +
-                                                   ring_slot(r, 4 * rh + j) * 16);
-      }
-    };
-    if constexpr (L::kSplit) {
-      // everything the stage needs is read ahead: with one tile pair per wave
-      // a read in front of each MFMA left the wave waiting for LDS most of
-      // the time
-      bf16x8 fa[KW][4][TT];
-#pragma unroll
-      for (int q = 0; q < KW; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load_act(q, j, fa[q][j]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int q = 0; q < KW; ++q) {
-        const float scale = mx4_scale((sc[0] >> (16 * q)) & 0xffu);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[0][0] = mfma32_bf16(mx4_decode8((uint32_t)raw[q][0][j], scale), fa[q][j][0], acc[0][0]);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < KW; ++q) {
-        float scale[TW];
-#pragma unroll
-        for (int tw = 0; tw < TW; ++tw) scale[tw] = mx4_scale((sc[tw] >> (16 * q)) & 0xffu);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bf16x8 fa[TT];
-          load_act(q, j, fa);
-#pragma unroll
-          for (int tw = 0; tw < TW; ++tw) {
-            const bf16x8 fw = mx4_decode8((uint32_t)raw[q][tw][j], scale[tw]);
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt) acc[tw][tt] = mfma32_bf16(fw, fa[tt], acc[tw][tt]);
-          }
+        for (int g = 0; g < 4; ++g) {
+          const int n = n0 + wt * 32 + g * 8 + rh * 4;
+          if (n < a.N)
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + row * a.N + n) =
+                m4_quad(acc[tw][tt], g);
         }
       }
-    }
-  };
-
-  // results of the block at feature nb0
-  auto epilogue = [&](int nb0) {
-    if constexpr (L::kSplit) {
-      f32x4 *sums = reinterpret_cast<f32x4 *>(ring + kM4Ring - G::kSums) + (wv & 3) * 256 + lane;
-      if (wv >= 4) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) sums[g * 64] = m4_quad(acc[0][0], g);
-      }
-      // the sums are written; the next ones are a barrier of every stage away
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      ring_barrier();
-      if (wv >= 4) return;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 v = sums[g * 64];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][0][4 * g + i] += v[i];
-      }
-    }
-    // register j of a 32x32 tile holds weight row 8*(j/4) + 4*rh + j%4, activation row rr
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      const int r = L::atile(wv, tt) * 32 + rr;
-      if (r >= t.nrows) continue;
-      const size_t row = (size_t)(t.row0 + r);
-#pragma unroll
-      for (int tw = 0; tw < TW; ++tw) {
-        const int wt = L::wtile(wv, tw);
-        if (GATEUP) {
-          // rows 0-15 of the tile are gate features 16 wt + [0,16), rows 16-31 the same up features
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const f32x4 gv = m4_quad(acc[tw][tt], g), uv = m4_quad(acc[tw][tt], g + 2);
-            const int n = nb0 + wt * 16 + g * 8 + rh * 4;
-            uint2 v;
-            v.x = (uint32_t)f32_to_bf16_bits(swiglu(gv[0], uv[0])) |
-                  ((uint32_t)f32_to_bf16_bits(swiglu(gv[1], uv[1])) << 16);
-            v.y = (uint32_t)f32_to_bf16_bits(swiglu(gv[2], uv[2])) |
-                  ((uint32_t)f32_to_bf16_bits(swiglu(gv[3], uv[3])) << 16);
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.N + n) = v;
-          }
-        } else {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int n = nb0 + wt * 32 + g * 8 + rh * 4;
-            if (n < a.N)
-              *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + row * a.N + n) =
-                  m4_quad(acc[tw][tt], g);
-          }
-        }
-      }
-    }
-  };
-
-  zero_acc();
-  ring_barrier();  // every wave has read its item, which lies in the ring
-  const int total = MB ? nb * nst : nst;
-  int is = 0, ib = 0;  // stage and block of the next stage to load
-  auto issue_next = [&](int slot) {
-    issue(is, ib, slot);
-    if (++is == nst && MB) {
-      is = 0;
-      ++ib;
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < NS - 1; ++s)
-    if (s < total) issue_next(s);
-  int slot = 0, cs = 0, cb = 0;  // stage and block being multiplied
-  int cg = 0;                    // buffer of its group of scales
-  for (int s = 0; s < total; ++s) {
-    // this wave's loads of stage s are done; later stages may stay in flight
-    // (stores of an earlier block, counted too, only make the wait longer)
-    wait_vm(cnt * min(NS - 2, total - 1 - s));
-    ring_barrier();  // stage s is in LDS for everyone; stage s - 1 is consumed
-    if (s + NS - 1 < total) issue_next(slot == 0 ? NS - 1 : slot - 1);
-    mma_stage(ring + slot * G::kSlot, ring + G::kScaleBase + cg * G::kScales, cs);
-    slot = slot == NS - 1 ? 0 : slot + 1;
-    ++cs;
-    if (cs % G::kGroup == 0 || (MB && cs == nst)) cg = cg == G::kBuffers - 1 ? 0 : cg + 1;
-    if (MB && cs == nst) {
-      epilogue(n0 + cb * FEAT);
-      cs = 0;
-      if (++cb < nb) zero_acc();
     }
   }
-  if (!MB) epilogue(n0);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -414,8 +447,8 @@ constexpr int kM4DirectAct = kM4Ring - kM4Waves * kM4ScaleWave;  // LDS for acti
 // Row stride of the activation rows in LDS, padded: consecutive rows start
 // in different banks.
 __device__ __forceinline__ int m4_direct_stride(int K) { return 2 * K + 16; }
-__device__ __forceinline__ bool m4_direct_fits(const Tile &t, int K) {
-  return t.nrows <= kM4DirectRows && t.nrows * m4_direct_stride(K) <= kM4DirectAct;
+__device__ __forceinline__ bool m4_direct_fits(int K) {
+  return kM4DirectRows * m4_direct_stride(K) <= kM4DirectAct;  // K <= 4,608
 }
 
 // One chunk of a wave's two weight tiles of 16 rows.
@@ -546,14 +579,15 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
 // ------------------------------------------------------------------ kernel
 
 // The tile list, one thread per expert: its full 256-row tiles, then one
-// remainder tile of the smallest capacity of 32, 64, 128, 192 and 256 rows
-// that holds it (Tile); all tiles of a class together, tallest class first,
-// experts in order.
+// remainder tile of the smallest capacity of 16, 64, 128, 192 and 256 rows
+// that holds it (Tile::ablk in 32 rows, 1 for 16); all tiles of a class
+// together, tallest class first, experts in order.  (A class of 32 rows saved
+// nothing: up to 64 rows the weight stream is the bound.)
 constexpr int kM4ScheduleThreads = 256;  // the most experts
 __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     const int32_t *__restrict__ offsets, int E, M4Schedule *__restrict__ sch,
     Tile *__restrict__ tiles) {
-  constexpr int NC = 5;  // capacities 256, 192, 128, 64, 32
+  constexpr int NC = 5;  // capacities 256, 192, 128, 64, 16
   constexpr int NW = kM4ScheduleThreads / kWave;
   __shared__ int waves[NC][NW];
   const int e = threadIdx.x, lane = lane_id(), wave = threadIdx.x / kWave;
@@ -563,7 +597,7 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     n = offsets[e + 1] - row0;
   }
   const int full = n / kTileRows, rem = n % kTileRows;
-  const int cls = rem == 0 ? NC : rem > 192 ? 0 : rem > 128 ? 1 : rem > 64 ? 2 : rem > 32 ? 3 : 4;
+  const int cls = rem == 0 ? NC : rem > 192 ? 0 : rem > 128 ? 1 : rem > 64 ? 2 : rem > kM4DirectRows ? 3 : 4;
   int at[NC];  // where this expert's tiles of a class begin
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -605,10 +639,6 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
   }
 }
 
-// Weight rows per item: 256; for 32-row tiles 128, in four blocks.
-constexpr int kM4WRows = 256;
-constexpr int kM4WRowsSmall = 128;
-
 // Work dispatch.  Tile i of the list (tallest first) belongs to queue i % 8,
 // and workgroup b to queue b % 8: workgroups go round the eight XCDs in that
 // order, so the items of one tile, which share its activation rows, run on
@@ -629,12 +659,12 @@ struct M4Queues {
   int nbig, nsmall, ptb, pts;
   int q, G;
   bool back;
-  __device__ __forceinline__ M4Queues(M4Heads *h_, int nbig_, int nsmall_, int ptb_, int pts_)
-      : h(h_), nbig(nbig_), nsmall(nsmall_), ptb(ptb_), pts(pts_) {
-    const int b = vreg((int)blockIdx.x);
+  // The state lies in LDS while a workgroup multiplies: the registers are
+  // all taken.
+  __device__ __forceinline__ M4Queues(M4Heads *h_, const int *state)
+      : h(h_), nbig(state[0]), nsmall(state[1]), ptb(state[2]), pts(state[3]), q(state[4]) {
     G = vreg((int)gridDim.x);
-    q = b % kM4Queues;
-    back = (b / kM4Queues) & 1;
+    back = (vreg((int)blockIdx.x) / kM4Queues) & 1;
   }
   __device__ __forceinline__ int tall(int p) const { return (nbig - p + kM4Queues - 1) / kM4Queues; }
   __device__ __forceinline__ int items(int p) const {
@@ -699,58 +729,62 @@ struct M4Queues {
 
 template <bool GATEUP>
 __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[kM4Ring];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kM4Lds];
   // the next item (tile index, first feature; tile -1 = none left) is passed
   // from thread 0 through the idle ring between items
   int *next_item = reinterpret_cast<int *>(ring);
+  int *state = reinterpret_cast<int *>(ring + kM4Ring);  // of the dispatch, thread 0's
   const uint32_t ring_lds = lds_addr(ring);
   constexpr int kHalf = GATEUP ? 2 : 1;  // gate and up rows of one feature
-  constexpr int FB = kM4WRows / kHalf;           // features per item of the taller tiles
-  constexpr int FS = 4 * kM4WRowsSmall / kHalf;  // and of the 32-row tiles
-  const int N = vreg(a.N);
-  const int nsmall = vreg(*a.n_small), nbig = vreg(*a.ntiles) - nsmall;
-  const int ptb = (N + FB - 1) / FB, pts = (N + FS - 1) / FS;  // items per tile
-  M4Queues queues(a.heads, nbig, nsmall, ptb, pts);
+  constexpr int FB = kM4WRows / kHalf;  // features per item of the ring
+  if (threadIdx.x == 0) {
+    const int FS = m4_direct_fits(a.K) ? 2 * FB : FB;  // and of tiles of few rows
+    state[0] = *a.ntiles - *a.n_small;
+    state[1] = *a.n_small;
+    state[2] = (a.N + FB - 1) / FB;  // items per tile
+    state[3] = (a.N + FS - 1) / FS;
+    state[4] = (int)blockIdx.x % kM4Queues;
+  }
   unsigned long long drawn = 0;
   bool begin = true;
   for (;;) {
     if (threadIdx.x == 0) {
+      M4Queues queues(a.heads, state);
       int ti = -1, part = 0;
       bool some = begin && queues.first(&ti, &part);
       if (begin && !some) drawn = queues.draw();
       if (!some) some = queues.take(drawn, &ti, &part);
       begin = false;
+      state[4] = queues.q;
+      const int FS = m4_direct_fits(a.K) ? 2 * FB : FB, nbig = queues.nbig;
       next_item[0] = some ? ti : -1;
       next_item[1] = some ? part * (ti < nbig ? FB : FS) : 0;
       next_item[2] = a.K;
+      next_item[3] = a.N;
     }
     __syncthreads();
     // read before the item's first barrier (its loads overwrite it); the
-    // reduction length comes through LDS so that nothing derived from it is
-    // hoisted out of the loop into the scalar registers
+    // sizes come through LDS so that nothing derived from them is hoisted
+    // out of the loop into the scalar registers
     const int ti = __builtin_amdgcn_readfirstlane(next_item[0]);
     if (ti < 0) break;
     const int n0 = __builtin_amdgcn_readfirstlane(next_item[1]);
     Mx4Args ai = a;
     ai.K = __builtin_amdgcn_readfirstlane(next_item[2]);
+    ai.N = __builtin_amdgcn_readfirstlane(next_item[3]);
     const Tile t = a.tiles[ti];
-    if (threadIdx.x == 0) drawn = queues.draw();  // for the item after this one
+    if (threadIdx.x == 0) drawn = M4Queues(a.heads, state).draw();  // for the item after this one
     switch (tile_class(t)) {
-      case 8: m4_item<GATEUP, false, 256, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
-      case 6: m4_item<GATEUP, false, 192, kM4WRows, 1>(ai, t, n0, 1, ring, ring_lds); break;
-      case 4: m4_item<GATEUP, false, 128, kM4WRows, 2>(ai, t, n0, 1, ring, ring_lds); break;
-      case 2: m4_item<GATEUP, false, 64, kM4WRows, 2>(ai, t, n0, 1, ring, ring_lds); break;
-      default: {
-        const int n1 = min(n0 + FS, ai.N);
-        const int nb = (n1 - n0) * 4 / FS;
-        if (m4_direct_fits(t, ai.K))
-          m4_direct<GATEUP>(ai, t, n0, n1, ring);
-        else if (t.ablk & kTileStream)
-          m4_item<GATEUP, true, 32, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
+      case 8: m4_item<GATEUP, 256>(ai, t, n0, ring, ring_lds); break;
+      case 6: m4_item<GATEUP, 192>(ai, t, n0, ring, ring_lds); break;
+      case 4: m4_item<GATEUP, 128>(ai, t, n0, ring, ring_lds); break;
+      case 2: m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds); break;
+      default:
+        if (m4_direct_fits(ai.K))
+          m4_direct<GATEUP>(ai, t, n0, min(n0 + 2 * FB, ai.N), ring);
         else
-          m4_item<GATEUP, false, 32, kM4WRowsSmall, 4>(ai, t, n0, nb, ring, ring_lds);
+          m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds);
         break;
-      }
     }
     // the ring (and the item in it) is rewritten only after every wave has
     // passed this barrier
