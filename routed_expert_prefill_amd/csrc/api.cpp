@@ -92,8 +92,10 @@ FfnLayout ffn_layout(const moe_ffn_desc *d) {
   size_t off = 0;
   L.sched = off;
   off += align_up(sizeof(moe::Schedule));
-  L.tiles = off;  // at most R / 256 full tiles plus one remainder per expert
-  off += align_up(sizeof(moe::Tile) * (R / moe::kTileRows + (size_t)d->E));
+  // at most R / 256 full tiles plus one remainder per expert (MXFP4: R / 64)
+  const size_t full = d->weight_dtype == MOE_W_MXFP4 ? 64 : moe::kTileRows;
+  L.tiles = off;
+  off += align_up(sizeof(moe::Tile) * (R / full + (size_t)d->E));
   L.h = off;
   off += align_up(R * (size_t)d->f * 2);
   if (fp8) {

@@ -578,14 +578,19 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
 
 // ------------------------------------------------------------------ kernel
 
-// The tile list, one thread per expert: its full 256-row tiles, then one
+// The tile list, one thread per expert: its full tiles of `cap` rows, then one
 // remainder tile of the smallest capacity of 16, 64, 128, 192 and 256 rows
 // that holds it (Tile::ablk in 32 rows, 1 for 16); all tiles of a class
 // together, tallest class first, experts in order.  (A class of 32 rows saved
 // nothing: up to 64 rows the weight stream is the bound.)
+//
+// cap is 256 rows, which reads an expert's weights least often, unless the
+// tiles then make fewer items than there are workgroups: 128 or 64 rows give
+// more of them, each with less to multiply (777 tokens, three routes each
+// over 24 experts, d 1152, f 640: gate/up 32.5 -> 18.7 us, down 23.9 -> 13.4 us).
 constexpr int kM4ScheduleThreads = 256;  // the most experts
 __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
-    const int32_t *__restrict__ offsets, int E, M4Schedule *__restrict__ sch,
+    const int32_t *__restrict__ offsets, int E, int blocks, int grid, M4Schedule *__restrict__ sch,
     Tile *__restrict__ tiles) {
   constexpr int NC = 5;  // capacities 256, 192, 128, 64, 16
   constexpr int NW = kM4ScheduleThreads / kWave;
@@ -596,12 +601,26 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     row0 = offsets[e];
     n = offsets[e + 1] - row0;
   }
-  const int full = n / kTileRows, rem = n % kTileRows;
+  int cap = kTileRows;
+  for (; cap > 64; cap /= 2) {
+    int v = (n + cap - 1) / cap;
+#pragma unroll
+    for (int m = kWave / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+    if (lane == 0) waves[0][wave] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += waves[0][w];
+    __syncthreads();
+    if ((long long)v * blocks >= grid) break;
+  }
+  const int full = n / cap, rem = n % cap;
+  const int fc = cap == 256 ? 0 : cap == 128 ? 2 : 3;  // class of the full tiles
   const int cls = rem == 0 ? NC : rem > 192 ? 0 : rem > 128 ? 1 : rem > 64 ? 2 : rem > kM4DirectRows ? 3 : 4;
   int at[NC];  // where this expert's tiles of a class begin
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int mine = (c == 0 ? full : 0) + (c == cls ? 1 : 0);
+    const int mine = (c == fc ? full : 0) + (c == cls ? 1 : 0);
     int v = mine;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
@@ -624,12 +643,14 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     }
     total += last;
   }
-  const int only = n <= kTileRows ? kTileStream : 0;
-  for (int i = 0; i < full; ++i) tiles[at[0] + i] = Tile{e, row0 + i * kTileRows, kTileRows, 8 | only};
-  if (cls < NC) {
+  const int only = n <= cap ? kTileStream : 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
     constexpr int kAblk[NC] = {8, 6, 4, 2, 1};
-    const int i = cls == 0 ? at[0] + full : cls == 1 ? at[1] : cls == 2 ? at[2] : cls == 3 ? at[3] : at[4];
-    tiles[i] = Tile{e, row0 + full * kTileRows, rem, (cls == 0 ? kAblk[0] : cls == 1 ? kAblk[1] : cls == 2 ? kAblk[2] : cls == 3 ? kAblk[3] : kAblk[4]) | only};
+    if (c == fc)
+      for (int i = 0; i < full; ++i) tiles[at[c] + i] = Tile{e, row0 + i * cap, cap, kAblk[c] | only};
+    if (c == cls)
+      tiles[at[c] + (c == fc ? full : 0)] = Tile{e, row0 + full * cap, rem, kAblk[c] | only};
   }
   if (e < 2 * kM4Queues) sch->heads[e / kM4Queues].head[e % kM4Queues] = 0;
   if (e < 2) sch->heads[e].left = 0;
@@ -688,6 +709,12 @@ struct M4Queues {
     if (rank >= (back ? n / 2 : (n + 1) / 2)) return false;
     return item(back ? n - 1 - rank : rank, tile, part);
   }
+  // Whether the fixed first items are all there are: nothing is drawn then.
+  __device__ __forceinline__ bool fixed() const {
+    for (int p = 0; p < kM4Queues; ++p)
+      if (rest(p, 0) > 0) return false;
+    return true;
+  }
   __device__ __forceinline__ unsigned long long draw() const {
     return atomicAdd(&h->head[q], back ? 1ull << 32 : 1ull);
   }
@@ -744,6 +771,7 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     state[2] = (a.N + FB - 1) / FB;  // items per tile
     state[3] = (a.N + FS - 1) / FS;
     state[4] = (int)blockIdx.x % kM4Queues;
+    state[5] = M4Queues(a.heads, state).fixed();
   }
   unsigned long long drawn = 0;
   bool begin = true;
@@ -752,10 +780,12 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
       M4Queues queues(a.heads, state);
       int ti = -1, part = 0;
       bool some = begin && queues.first(&ti, &part);
-      if (begin && !some) drawn = queues.draw();
-      if (!some) some = queues.take(drawn, &ti, &part);
+      if (!state[5]) {
+        if (begin && !some) drawn = queues.draw();
+        if (!some) some = queues.take(drawn, &ti, &part);
+        state[4] = queues.q;
+      }
       begin = false;
-      state[4] = queues.q;
       const int FS = m4_direct_fits(a.K) ? 2 * FB : FB, nbig = queues.nbig;
       next_item[0] = some ? ti : -1;
       next_item[1] = some ? part * (ti < nbig ? FB : FS) : 0;
@@ -773,7 +803,8 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     ai.K = __builtin_amdgcn_readfirstlane(next_item[2]);
     ai.N = __builtin_amdgcn_readfirstlane(next_item[3]);
     const Tile t = a.tiles[ti];
-    if (threadIdx.x == 0) drawn = M4Queues(a.heads, state).draw();  // for the item after this one
+    if (threadIdx.x == 0 && !state[5])
+      drawn = M4Queues(a.heads, state).draw();  // for the item after this one
     switch (tile_class(t)) {
       case 8: m4_item<GATEUP, 256>(ai, t, n0, ring, ring_lds); break;
       case 6: m4_item<GATEUP, 192>(ai, t, n0, ring, ring_lds); break;
@@ -796,7 +827,8 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
   M4Schedule *sch = reinterpret_cast<M4Schedule *>(L.sch);
   if (stages & kStagePlan)
     hipLaunchKernelGGL(mx4_schedule_kernel, dim3(1), dim3(kM4ScheduleThreads), 0, stream, L.offsets,
-                       L.E, sch, L.tiles);
+                       L.E, min(L.f / (kM4WRows / 2), (L.d + kM4WRows - 1) / kM4WRows), L.num_cus,
+                       sch, L.tiles);
   Mx4Args g{};
   g.k = L.k;
   g.tiles = L.tiles;
