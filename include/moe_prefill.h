@@ -194,6 +194,21 @@ int moe_grouped_ffn(const moe_ffn_desc *desc /* host */, const void *x, const in
                     const void *s_down, float *y, void *workspace, size_t workspace_bytes,
                     moe_stream_t stream);
 
+/* ------------------------------------------------------------ grouped FFN on codes
+ * moe_grouped_ffn in fp8 mode for a caller that holds x quantised already
+ * (moe_add_rmsnorm, moe_quant_rows_fp8): the same kernels and, for the codes
+ * and scales that moe_quant_rows_fp8 gives, the same y bit for bit.
+ *
+ * xq  uint8 [T,d] E4M3 codes;  xs fp32 [T];  other arguments, workspace and
+ * errors as for moe_grouped_ffn; desc's weight_dtype must be
+ * MOE_W_FP8_E4M3_B128 (MOE_EUNSUPPORTED otherwise).
+ */
+int moe_grouped_ffn_codes(const moe_ffn_desc *desc /* host */, const uint8_t *xq, const float *xs,
+                          const int32_t *offsets, const int32_t *sorted_routes,
+                          const void *w_gate, const void *w_up, const void *w_down,
+                          const void *s_gate, const void *s_up, const void *s_down, float *y,
+                          void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------------ FFN stages
  * moe_grouped_ffn is exactly these three calls, in this order, on one stream
  * with one workspace.  They are exposed for callers that time or overlap the

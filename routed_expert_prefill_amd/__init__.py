@@ -16,7 +16,7 @@ from ._lib import (MOE_ACT_BF16, MOE_ACT_FP8_E4M3_ROW, MOE_W_BF16, MOE_W_FP8_E4M
                    MOE_W_MXFP4, LibraryNotBuilt, MoeFfnDesc)
 
 __all__ = [
-    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "decode_ffn", "MoEPrefill", "RouteTable",
+    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "grouped_ffn_codes", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "decode_ffn", "MoEPrefill", "RouteTable",
     "ffn_desc", "ffn_plan", "ffn_gate_up", "ffn_down", "LibraryNotBuilt", "load_library",
 ]
 
@@ -32,10 +32,18 @@ class RouteTable(NamedTuple):
     route_rows: "torch.Tensor"  # int32 [T*k]
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    # imported with the first call, and kept: the import statement alone is
+    # 0.3 us, several times a call
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -50,6 +58,12 @@ def _stream() -> int:
 
 
 def _need(t, name, dtype, ndim=None):
+    try:
+        if (t.is_cuda and t.dtype == (dtype or t.dtype) and (ndim is None or t.dim() == ndim)
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -103,8 +117,8 @@ def route_build(topk_ids, route_mask, E: int, out: Optional[RouteTable] = None,
             sorted_routes=torch.empty(T * k, dtype=torch.int32, device=dev),
             route_rows=torch.empty(T * k, dtype=torch.int32, device=dev),
         )
-    wsb = lib.moe_route_build_workspace(T, k, E)
     if workspace is None:
+        wsb = lib.moe_route_build_workspace(T, k, E)
         workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=dev)
     rc = lib.moe_route_build(_ptr(topk_ids), _ptr(route_mask), T, k, E, _ptr(out.counts),
                              _ptr(out.offsets), _ptr(out.sorted_routes), _ptr(out.route_rows),
@@ -201,13 +215,51 @@ def grouped_ffn(x, offsets, sorted_routes, w_gate, w_up, w_down, k: int, s_gate=
     if y is None:
         y = torch.empty(T * k, d, dtype=torch.float32, device=x.device)
     _need(y, "y", torch.float32, 2)
-    wsb = lib.moe_grouped_ffn_workspace(ctypes.byref(desc))
     if workspace is None:
-        workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=x.device)
+        workspace = _ffn_ws(desc, x.device, None)
     rc = lib.moe_grouped_ffn(ctypes.byref(desc), _ptr(x), _ptr(offsets), _ptr(sorted_routes),
                              _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(s_gate), _ptr(s_up),
                              _ptr(s_down), _ptr(y), _ptr(workspace), workspace.numel(), _stream())
     _lib.check(rc, "moe_grouped_ffn")
+    return y
+
+
+def grouped_ffn_codes(xq, xs, offsets, sorted_routes, w_gate, w_up, w_down, k: int, s_gate, s_up,
+                      s_down, y=None, workspace=None):
+    """moe_grouped_ffn_codes: the fp8 grouped_ffn on rows that are quantised
+    already -- E4M3 codes xq (uint8) [T, d] and scales xs [T], as add_rmsnorm
+    and quant_rows_fp8 give them."""
+    torch = _torch()
+    lib = _lib.load()
+    _need(xq, "xq", torch.uint8, 2)
+    _need(xs, "xs", torch.float32, 1)
+    for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
+        _need(w, name, torch.uint8, 3)
+    for name, s in (("s_gate", s_gate), ("s_up", s_up), ("s_down", s_down)):
+        _need(s, name, torch.float32, 3)
+    _need(offsets, "offsets", torch.int32, 1)
+    _need(sorted_routes, "sorted_routes", torch.int32, 1)
+    T, d = xq.shape
+    E, f, _ = w_gate.shape
+    for name, t, shape in (("xs", xs, (T,)), ("w_gate", w_gate, (E, f, d)),
+                           ("w_up", w_up, (E, f, d)), ("w_down", w_down, (E, d, f)),
+                           ("s_gate", s_gate, (E, f // 128, d // 128)),
+                           ("s_up", s_up, (E, f // 128, d // 128)),
+                           ("s_down", s_down, (E, d // 128, f // 128)),
+                           ("offsets", offsets, (E + 2,)), ("sorted_routes", sorted_routes, (T * k,))):
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    desc = ffn_desc(T, k, E, d, f, weights="fp8")
+    if y is None:
+        y = torch.empty(T * k, d, dtype=torch.float32, device=xq.device)
+    _need(y, "y", torch.float32, 2)
+    if workspace is None:
+        workspace = _ffn_ws(desc, xq.device, None)
+    rc = lib.moe_grouped_ffn_codes(ctypes.byref(desc), _ptr(xq), _ptr(xs), _ptr(offsets),
+                                   _ptr(sorted_routes), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                   _ptr(s_gate), _ptr(s_up), _ptr(s_down), _ptr(y),
+                                   _ptr(workspace), workspace.numel(), _stream())
+    _lib.check(rc, "moe_grouped_ffn_codes")
     return y
 
 
@@ -390,13 +442,13 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, 
                    ((x if residual is None else residual).dtype,), dev)
     if y is None:
         if want_bf16:
-            y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            y = torch.empty_like(x, dtype=torch.bfloat16)
     else:
         _need_rows(y, "y", shape, (torch.bfloat16,), dev)
     if q is not None:
         _need_rows(q, "q", shape, (torch.uint8,), dev)
     elif want_fp8 or s is not None:
-        q = torch.empty(shape, dtype=torch.uint8, device=dev)
+        q = torch.empty_like(x, dtype=torch.uint8)
     if s is not None:
         _need_rows(s, "s", shape[:1], (torch.float32,), dev)
     elif q is not None:
@@ -506,12 +558,21 @@ class MoEPrefill:
 
     def __call__(self, x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate=None,
                  s_up=None, s_down=None, stage_events=None, shared=None):
-        """One pass of the path.  shared: fp32 rows [T, d] of the shared
-        expert, added to the routed sum.  stage_events: optional torch events
-        recorded on the current stream: 2 events around the gate/up stage, or
-        6 -- before the route build and after each of route build, FFN plan,
-        gate/up, down and combine."""
+        """One pass of the path.  x: bf16 rows [T, d], or with fp8 weights the
+        pair of their E4M3 codes and scales (add_rmsnorm, quant_rows_fp8).
+        shared: fp32 rows [T, d] of the shared expert, added to the routed
+        sum.  stage_events: optional torch events recorded on the current
+        stream: 2 events around the gate/up stage, or 6 -- before the route
+        build and after each of route build, FFN plan, gate/up, down and
+        combine."""
         ev = stage_events
+        if isinstance(x, tuple):
+            if not self.fp8 or ev is not None:
+                raise ValueError("codes and scales need fp8 weights, and no stage events")
+            rt = route_build(topk_ids, route_mask, self.E, out=self.rt, workspace=self.rb_ws)
+            grouped_ffn_codes(*x, rt.offsets, rt.sorted_routes, w_gate, w_up, w_down, self.k,
+                              s_gate, s_up, s_down, y=self.y, workspace=self.ffn_ws)
+            return self._combine(rt, topk_w, route_mask, shared)
         if self.decode and ev is None:
             return decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_up,
                               s_down, shared=shared, out=self.out, workspace=self.ffn_ws)

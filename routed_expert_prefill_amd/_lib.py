@@ -34,7 +34,7 @@ EXPORTED = [
     "moe_ffn_plan", "moe_ffn_gate_up", "moe_ffn_down",
     "moe_combine", "moe_quant_rows_fp8", "moe_route_topk", "moe_combine_shared",
     "moe_route_build_noalloc", "moe_add_rmsnorm",
-    "moe_decode_ffn_workspace", "moe_decode_ffn",
+    "moe_decode_ffn_workspace", "moe_decode_ffn", "moe_grouped_ffn_codes",
 ]
 
 
@@ -99,6 +99,8 @@ def load() -> ctypes.CDLL:
     lib.moe_decode_ffn_workspace.argtypes = [dp]
     lib.moe_decode_ffn.restype = i32
     lib.moe_decode_ffn.argtypes = [dp] + [vp] * 14 + [sz, vp]
+    lib.moe_grouped_ffn_codes.restype = i32
+    lib.moe_grouped_ffn_codes.argtypes = [dp] + [vp] * 12 + [sz, vp]
     _lib = lib
     return lib
 

@@ -184,6 +184,43 @@ size_t moe_grouped_ffn_workspace(const moe_ffn_desc *desc) {
 
 namespace {
 
+// The fp8 launch of a call whose arguments are checked, x quantised into the
+// workspace.
+moe::FfnLaunchFp8 fp8_launch(const moe_ffn_desc *desc, const void *x, const int32_t *offsets,
+                             const int32_t *sorted_routes, const void *w_gate, const void *w_up,
+                             const void *w_down, const void *s_gate, const void *s_up,
+                             const void *s_down, float *y, char *ws) {
+  const FfnLayout lay = ffn_layout(desc);
+  moe::FfnLaunchFp8 L{};
+  L.x = static_cast<const uint16_t *>(x);
+  L.qx = reinterpret_cast<uint8_t *>(ws + lay.qx);
+  L.sx = reinterpret_cast<float *>(ws + lay.sx);
+  L.offsets = offsets;
+  L.sorted_routes = sorted_routes;
+  L.wg = static_cast<const uint8_t *>(w_gate);
+  L.wu = static_cast<const uint8_t *>(w_up);
+  L.wd = static_cast<const uint8_t *>(w_down);
+  L.sg = static_cast<const float *>(s_gate);
+  L.su = static_cast<const float *>(s_up);
+  L.sd = static_cast<const float *>(s_down);
+  L.y = y;
+  L.h = reinterpret_cast<uint16_t *>(ws + lay.h);
+  L.qh = reinterpret_cast<uint8_t *>(ws + lay.qh);
+  L.sh = reinterpret_cast<float *>(ws + lay.sh);
+  L.hmax = reinterpret_cast<uint32_t *>(ws + lay.hmax);
+  L.sch = reinterpret_cast<moe::Schedule *>(ws + lay.sched);
+  L.tiles = reinterpret_cast<moe::Tile *>(ws + lay.tiles);
+  L.num_cus = num_cus_current_device();
+  L.T = desc->T;
+  L.k = desc->k;
+  L.E = desc->E;
+  L.d = desc->d;
+  L.f = desc->f;
+  L.R = desc->T * desc->k;
+  L.grid_cap = grid_cap_for_current_device();
+  return L;
+}
+
 // Shared body of moe_grouped_ffn and its stage calls.
 int ffn_call(const moe_ffn_desc *desc, int stages, const void *x, const int32_t *offsets,
              const int32_t *sorted_routes, const void *w_gate, const void *w_up,
@@ -256,34 +293,9 @@ int ffn_call(const moe_ffn_desc *desc, int stages, const void *x, const int32_t 
     L.R = R;
     return status_from(moe::launch_grouped_ffn_bf16(L, stages, s));
   }
-  moe::FfnLaunchFp8 L{};
-  L.x = static_cast<const uint16_t *>(x);
-  L.qx = reinterpret_cast<uint8_t *>(ws + lay.qx);
-  L.sx = reinterpret_cast<float *>(ws + lay.sx);
-  L.offsets = offsets;
-  L.sorted_routes = sorted_routes;
-  L.wg = static_cast<const uint8_t *>(w_gate);
-  L.wu = static_cast<const uint8_t *>(w_up);
-  L.wd = static_cast<const uint8_t *>(w_down);
-  L.sg = static_cast<const float *>(s_gate);
-  L.su = static_cast<const float *>(s_up);
-  L.sd = static_cast<const float *>(s_down);
-  L.y = y;
-  L.h = reinterpret_cast<uint16_t *>(ws + lay.h);
-  L.qh = reinterpret_cast<uint8_t *>(ws + lay.qh);
-  L.sh = reinterpret_cast<float *>(ws + lay.sh);
-  L.hmax = reinterpret_cast<uint32_t *>(ws + lay.hmax);
-  L.sch = reinterpret_cast<moe::Schedule *>(ws + lay.sched);
-  L.tiles = reinterpret_cast<moe::Tile *>(ws + lay.tiles);
-  L.num_cus = num_cus_current_device();
-  L.T = desc->T;
-  L.k = desc->k;
-  L.E = desc->E;
-  L.d = desc->d;
-  L.f = desc->f;
-  L.R = R;
-  L.grid_cap = grid_cap_for_current_device();
-  return status_from(moe::launch_ffn_fp8(L, stages, s));
+  return status_from(moe::launch_ffn_fp8(
+      fp8_launch(desc, x, offsets, sorted_routes, w_gate, w_up, w_down, s_gate, s_up, s_down, y, ws),
+      stages, s));
 }
 
 }  // namespace
@@ -297,6 +309,35 @@ int moe_grouped_ffn(const moe_ffn_desc *desc, const void *x, const int32_t *offs
                     moe_stream_t stream) {
   return ffn_call(desc, moe::kStageAll, x, offsets, sorted_routes, w_gate, w_up, w_down, s_gate,
                   s_up, s_down, y, workspace, workspace_bytes, stream);
+}
+
+int moe_grouped_ffn_codes(const moe_ffn_desc *desc, const uint8_t *xq, const float *xs,
+                          const int32_t *offsets, const int32_t *sorted_routes,
+                          const void *w_gate, const void *w_up, const void *w_down,
+                          const void *s_gate, const void *s_up, const void *s_down, float *y,
+                          void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+  int st;
+  if (!ffn_desc_status(desc, &st)) return st;
+  if (desc->weight_dtype != MOE_W_FP8_E4M3_B128) return MOE_EUNSUPPORTED;
+  const void *ptrs[] = {xq,     xs,     offsets, sorted_routes, w_gate, w_up,
+                        w_down, s_gate, s_up,    s_down,        y};
+  for (const void *p : ptrs)
+    if (!p) return MOE_EINVAL;
+  for (const void *p : ptrs)
+    if (misaligned(p)) return MOE_EALIGN;
+  if (workspace && misaligned(workspace)) return MOE_EALIGN;
+  if (!workspace || workspace_bytes < ffn_layout(desc).total) return MOE_EWORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  moe::FfnLaunchFp8 L = fp8_launch(desc, nullptr, offsets, sorted_routes, w_gate, w_up, w_down,
+                                   s_gate, s_up, s_down, y, static_cast<char *>(workspace));
+  // read only: without the plan stage nothing writes the rows' codes
+  L.qx = const_cast<uint8_t *>(xq);
+  L.sx = const_cast<float *>(xs);
+  // the plan without its quantisation
+  hipError_t err = moe::launch_grouped_schedule(L.offsets, L.E, L.sch, L.tiles, s);
+  if (err == hipSuccess) err = moe::launch_zero_u32(L.hmax, L.R, s);
+  if (err == hipSuccess) err = moe::launch_ffn_fp8(L, moe::kStageGateUp | moe::kStageDown, s);
+  return status_from(err);
 }
 
 int moe_ffn_plan(const moe_ffn_desc *desc, const void *x, const int32_t *offsets,

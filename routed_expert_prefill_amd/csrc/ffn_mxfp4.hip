@@ -315,15 +315,14 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   for (int g = 1; g < NB - 1; ++g)
     if (g < ngr) issue_group(g);
   int slot = 0, buf = 0;  // of the stage being multiplied
-  static_assert(NS - 1 <= S, "the first group's stages are loaded ahead of the loop");
 #pragma unroll 1
   for (int g = 0; g < ngr; ++g) {
     // What may stay in flight at the start of stage s: the activations of the
     // NS - 2 stages after it, and the codes that went out since its own
     // activations did (with the first stage of a group, after that stage's
-    // activations).  Between the first group and the last NB that is a
+    // activations).  Between the first groups and the last NB that is a
     // constant.  Scales are not counted: the wait is then one load longer.
-    const bool steady = g > 0 && g + NB < ngr;
+    const bool steady = g * S >= NS - 1 && g + NB < ngr;
     const bool codes_too = g + NB - 1 < ngr;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -535,8 +534,11 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
     acc[1] = f32x4{};
   };
 
-  M4Chunk qa, qb;
-  if (total > 0) load(qa, 0);
+  M4Chunk qa, qb, qc;
+  if (total > 0) {
+    load(qa, 0);
+    load(qb, min(1, total - 1));
+  }
   ring_barrier();  // every wave has read its item, which lies where the rows go
   // wave w brings rows w and w + 8
   for (int r = wv; r < t.nrows; r += kM4Waves) {
@@ -561,19 +563,21 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
   if (total == 0) return;
   int i = 0;
 #pragma unroll 1
-  for (; i + 2 < total; i += 2) {
-    load(qb, i + 1);
+  for (; i + 4 < total; i += 3) {
+    load(qc, i + 2);
     multiply(qa, i);
-    load(qa, i + 2);
+    load(qa, i + 3);
     multiply(qb, i + 1);
+    load(qb, i + 4);
+    multiply(qc, i + 2);
   }
-  if (i + 1 < total) {
-    load(qb, i + 1);
-    multiply(qa, i);
-    multiply(qb, i + 1);
-  } else {
-    multiply(qa, i);
-  }
+  const int rest = total - i;  // one to four
+  if (rest > 2) load(qc, i + 2);
+  multiply(qa, i);
+  if (rest > 3) load(qa, i + 3);
+  if (rest > 1) multiply(qb, i + 1);
+  if (rest > 2) multiply(qc, i + 2);
+  if (rest > 3) multiply(qa, i + 3);
 }
 
 // ------------------------------------------------------------------ kernel

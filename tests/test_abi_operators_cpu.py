@@ -93,3 +93,22 @@ def test_decode_errors(lib):
     assert f(desc=_desc(T=0)) == _lib.MOE_EINVAL
     assert f(ws=0) == _lib.MOE_EWORKSPACE and f(wsb=1024) == _lib.MOE_EWORKSPACE
     assert lib.moe_decode_ffn(None, *[A] * 14, 1 << 30, None) == _lib.MOE_EINVAL
+
+
+def test_grouped_ffn_codes_errors(lib):
+    names = ("xq", "xs", "offs", "sr", "wg", "wu", "wd", "sg", "su", "sd", "y")
+
+    def f(desc=None, ws=A, wsb=1 << 40, **kw):
+        p = {**dict.fromkeys(names, A), **kw}
+        d = desc or _desc(w=_lib.MOE_W_FP8_E4M3_B128, a=_lib.MOE_ACT_FP8_E4M3_ROW)
+        return lib.moe_grouped_ffn_codes(ctypes.byref(d), *[p[n] or None for n in names],
+                                         ws or None, wsb, None)
+
+    for n in names:
+        assert f(**{n: 0}) == _lib.MOE_EINVAL, n
+        assert f(**{n: A + 8}) == _lib.MOE_EALIGN, n
+    assert f(desc=_desc()) == _lib.MOE_EUNSUPPORTED  # MXFP4
+    assert f(desc=_desc(w=0, a=0)) == _lib.MOE_EUNSUPPORTED
+    assert f(desc=_desc(T=0, w=1, a=1)) == _lib.MOE_EINVAL
+    assert f(ws=0) == _lib.MOE_EWORKSPACE and f(wsb=4096) == _lib.MOE_EWORKSPACE
+    assert f(ws=A + 8) == _lib.MOE_EALIGN
