@@ -453,11 +453,21 @@ __device__ __forceinline__ bool m4_direct_fits(int K) {
 // One chunk of a wave's two weight tiles of 16 rows.
 struct M4Chunk {
   i32x4 raw[kM4Steps][2];
-  uint32_t sc[2];  // lane group c: the scales of step c
+  uint32_t sc[2];  // without WIDE: in lane group c the scales of step c
+};
+
+// The scales of a wave's two weight tiles for a whole row of up to eight
+// chunks, in whole lines: lane l holds chunk l % 8 of rows l / 8 and l / 8 + 8.
+struct M4Scales {
+  i32x4 v[2][2];
 };
 
 // Output features [n0, n1) of a tile.
-template <bool GATEUP>
+// WIDE (K a multiple of 1024): the scales come in whole lines, a chunk's 16
+// bytes per row passing through LDS to the lanes that multiply; fetched with
+// each chunk instead, 16 bytes of a line at a time, they cost twice their
+// share of the bytes (MI355X, 401 tokens: gate/up 440 us, 390 without scales).
+template <bool GATEUP, bool WIDE>
 __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n0, int n1,
                                           uint8_t *lds) {
   constexpr int FG = GATEUP ? 16 : 32;  // features of a wave's two weight tiles
@@ -469,7 +479,8 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
   const int chunks = (nk + kM4Steps - 1) / kM4Steps;
   const int groups = max(((n1 - n0) / FG - wv + kM4Waves - 1) / kM4Waves, 0);
   const int total = groups * chunks;
-  uint8_t *sc_lds = lds + kM4DirectAct + wv * kM4ScaleWave + row * kM4ScaleRow;
+  uint8_t *sc_lds0 = lds + kM4DirectAct + wv * kM4ScaleWave;
+  uint8_t *sc_lds = sc_lds0 + row * kM4ScaleRow;
 
   auto load = [&](M4Chunk &q, int i) {
     const int g = i / chunks, s = (i - g * chunks) * kM4Steps;
@@ -480,21 +491,43 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
       const uint8_t *codes = (GATEUP && w ? a.w1 : a.w0) + r * (K / 2) + c * 16;
       const uint8_t *scales = (GATEUP && w ? a.s1 : a.s0) + r * (K / 32);
       // steps past the end load the last one again
-      q.sc[w] = *reinterpret_cast<const uint32_t *>(scales + min(s + c, nk - 1) * 4);
+      if (!WIDE) q.sc[w] = *reinterpret_cast<const uint32_t *>(scales + min(s + c, nk - 1) * 4);
 #pragma unroll
       for (int u = 0; u < kM4Steps; ++u)
         q.raw[u][w] = *reinterpret_cast<const i32x4 *>(codes + min(s + u, nk - 1) * 64);
     }
     asm volatile("" ::: "memory");  // issued here, not where they are used
   };
+  auto load_scales = [&](M4Scales &q, int g) {
+    const int n = n0 + (wv + kM4Waves * g) * FG;
+    const int at = min(lane & 7, chunks - 1) * 16;
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const size_t r = (size_t)t.e * a.N + n + (lane >> 3) + 8 * h + (GATEUP ? 0 : 16 * w);
+        q.v[w][h] = *reinterpret_cast<const i32x4 *>((GATEUP && w ? a.s1 : a.s0) + r * (K / 32) + at);
+      }
+    asm volatile("" ::: "memory");
+  };
   f32x4 acc[2] = {};
   const uint8_t *mine = lds + min(row, t.nrows - 1) * stride + c * 64;
+  M4Scales sa, sb;  // WIDE: of the group being multiplied, and of the next
   auto multiply = [&](const M4Chunk &q, int i) {
     const int g = i / chunks, ci = i - g * chunks, s = ci * kM4Steps;
     i32x4 ss[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      *reinterpret_cast<uint32_t *>(sc_lds + w * 16 * kM4ScaleRow + c * 4) = q.sc[w];
+      if (WIDE) {
+        if ((lane & 7) == ci) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<i32x4 *>(sc_lds0 + (w * 16 + (lane >> 3) + 8 * h) * kM4ScaleRow) =
+                sa.v[w][h];
+        }
+      } else {
+        *reinterpret_cast<uint32_t *>(sc_lds + w * 16 * kM4ScaleRow + c * 4) = q.sc[w];
+      }
       ss[w] = *reinterpret_cast<const i32x4 *>(sc_lds + w * 16 * kM4ScaleRow);
     }
     const int steps = min(kM4Steps, nk - s);
@@ -534,10 +567,10 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
     acc[1] = f32x4{};
   };
 
-  M4Chunk qa, qb, qc;
+  M4Chunk qa, qb;
   if (total > 0) {
+    if (WIDE) load_scales(sa, 0);
     load(qa, 0);
-    load(qb, min(1, total - 1));
   }
   ring_barrier();  // every wave has read its item, which lies where the rows go
   // wave w brings rows w and w + 8
@@ -558,26 +591,39 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   ring_barrier();
-  // no load in the loop is conditional: where a path without it joined, the
+  // no load in the loops is conditional: where a path without it joined, the
   // compiler would have to wait for all of them
   if (total == 0) return;
   int i = 0;
+  if (WIDE) {  // an even number of chunks per row
 #pragma unroll 1
-  for (; i + 4 < total; i += 3) {
-    load(qc, i + 2);
-    multiply(qa, i);
-    load(qa, i + 3);
-    multiply(qb, i + 1);
-    load(qb, i + 4);
-    multiply(qc, i + 2);
+    for (int g = 0; g < groups; ++g) {
+      load_scales(sb, min(g + 1, groups - 1));
+#pragma unroll 1
+      for (int ci = 0; ci < chunks; ci += 2, i += 2) {
+        load(qb, i + 1);
+        multiply(qa, i);
+        load(qa, min(i + 2, total - 1));
+        multiply(qb, i + 1);
+      }
+      sa = sb;
+    }
+  } else {
+#pragma unroll 1
+    for (; i + 2 < total; i += 2) {
+      load(qb, i + 1);
+      multiply(qa, i);
+      load(qa, i + 2);
+      multiply(qb, i + 1);
+    }
+    if (i + 1 < total) {
+      load(qb, i + 1);
+      multiply(qa, i);
+      multiply(qb, i + 1);
+    } else {
+      multiply(qa, i);
+    }
   }
-  const int rest = total - i;  // one to four
-  if (rest > 2) load(qc, i + 2);
-  multiply(qa, i);
-  if (rest > 3) load(qa, i + 3);
-  if (rest > 1) multiply(qb, i + 1);
-  if (rest > 2) multiply(qc, i + 2);
-  if (rest > 3) multiply(qa, i + 3);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -815,8 +861,10 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
       case 4: m4_item<GATEUP, 128>(ai, t, n0, ring, ring_lds); break;
       case 2: m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds); break;
       default:
-        if (m4_direct_fits(ai.K))
-          m4_direct<GATEUP>(ai, t, n0, min(n0 + 2 * FB, ai.N), ring);
+        if (m4_direct_fits(ai.K) && ai.K % 1024 == 0)
+          m4_direct<GATEUP, true>(ai, t, n0, min(n0 + 2 * FB, ai.N), ring);
+        else if (m4_direct_fits(ai.K))
+          m4_direct<GATEUP, false>(ai, t, n0, min(n0 + 2 * FB, ai.N), ring);
         else
           m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds);
         break;
