@@ -80,9 +80,10 @@ struct M4Layout {
   static constexpr int kCodes = kM4WRows * 16 * 2 * GB;
   static constexpr int kScales = kM4WRows * 16;
   static constexpr int kFit = (kM4Ring - NB * kCodes - 2 * kScales) / kAct;
-  // a group of codes is loaded ahead of the stage that follows its first one,
-  // so that only the activations decide what a stage waits for
-  static constexpr int kMost = (NB - 1) * S + 1;
+  // A group's codes go out NB - 1 groups ahead, after the activations of that
+  // stage; with no more slots than this they are older than the activations
+  // of the group's first stage, which alone then decide what a stage waits for.
+  static constexpr int kMost = (NB - 1) * S;
   static constexpr int NS = kFit < kMost ? kFit : kMost;
   static constexpr int kCodeBase = NS * kAct;
   static constexpr int kScaleBase = kCodeBase + NB * kCodes;

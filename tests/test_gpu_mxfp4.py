@@ -86,6 +86,29 @@ def test_full_width():
     _close(out, omoe.moe_ref_blocked(x, ids, w, mask, bf16_source(W), E)[0])
 
 
+@pytest.mark.parametrize("rows", [13, 60, 100, 128, 180, 256])
+def test_many_tiles_of_one_height(rows):
+    """Enough items of one tile height, at a reduction of 4096 columns, to keep
+    every workgroup at it for several rounds: a stage that started ahead of
+    its loads would show here."""
+    E, d, f = 40, 4096, 1024
+    p = _problem([rows - e % 3 for e in range(E)], 4, d, f, seed=rows)
+    _, ids, w, mask, x, W = p
+    _, out = _run(p)
+    sub = [0, 1, 7, 20, 39]  # the reference of every expert would take minutes: these experts' share
+    only = np.where(np.isin(ids, sub), mask, 0).astype(np.uint8)
+    _, part = _run((E, ids, w, only, x, W))
+    _close(part, omoe.moe_ref_blocked(x, ids, w, only, bf16_source(W), E)[0])
+    # and the whole as the sum of eight shares, each run by itself.  A share has
+    # fewer items, so its tiles may be shorter and their sums in another order:
+    # the tolerance above
+    total = np.zeros_like(out)
+    for g in range(8):
+        share = np.where(ids % 8 == g, mask, 0).astype(np.uint8)
+        total += _run((E, ids, w, share, x, W))[1]
+    _close(out, total)
+
+
 def test_masked_and_out_of_range_routes_add_exact_zeros():
     p = _problem([5, 0, 40, 3], 3, 256, 128, seed=5, masked=20, invalid=6)
     E, ids, w, mask, x, W = p
