@@ -171,16 +171,25 @@ _WEIGHTS = {"bf16": (MOE_W_BF16, MOE_ACT_BF16),
             "mxfp4": (MOE_W_MXFP4, MOE_ACT_BF16)}
 
 
-def _need_mx4(E, d, f, w_gate, w_up, w_down, s_gate, s_up, s_down):
-    """Codes and scales of MXFP4 weights: [E, rows, cols/2] and [E, rows, cols/32]."""
-    torch = _torch()
+def _need_mx4(x, offsets, sorted_routes, E, f, w_gate, w_up, w_down, s_gate, s_up, s_down):
+    """Codes and scales of MXFP4 weights: [E, rows, cols/2] and [E, rows, cols/32];
+    everything on the device of x, the current one."""
+    u8, d = (_torch().uint8,), x.shape[1]
+    dev = _on_current(x, "x")
     for name, w, s, rows, cols in (("gate", w_gate, s_gate, f, d), ("up", w_up, s_up, f, d),
                                    ("down", w_down, s_down, d, f)):
-        _need(w, "w_" + name, torch.uint8, 3)
-        _need(s, "s_" + name, torch.uint8, 3)
-        if w.shape != (E, rows, cols // 2) or s.shape != (E, rows, cols // 32):
-            raise ValueError(f"w_{name} must have shape {(E, rows, cols // 2)} and s_{name} "
-                             f"{(E, rows, cols // 32)}, got {tuple(w.shape)} and {tuple(s.shape)}")
+        _need_rows(w, "w_" + name, (E, rows, cols // 2), u8, dev)
+        _need_rows(s, "s_" + name, (E, rows, cols // 32), u8, dev)
+    for name, t in (("offsets", offsets), ("sorted_routes", sorted_routes)):
+        _need_rows(t, name, t.shape, (t.dtype,), dev)
+
+
+def _need_y(y, R, d, workspace, device):
+    """y for R sorted rows, or more, and the workspace beside it."""
+    torch = _torch()
+    _need(y, "y", torch.float32, 2)
+    _need_rows(y, "y", (max(R, y.shape[0]), d), (torch.float32,), device)
+    _need_rows(workspace, "workspace", workspace.shape, (torch.uint8,), device)
 
 
 def grouped_ffn(x, offsets, sorted_routes, w_gate, w_up, w_down, k: int, s_gate=None,
@@ -206,7 +215,7 @@ def grouped_ffn(x, offsets, sorted_routes, w_gate, w_up, w_down, k: int, s_gate=
     T, d = x.shape
     E, f, d2 = w_gate.shape
     if mx4:
-        _need_mx4(E, d, f, w_gate, w_up, w_down, s_gate, s_up, s_down)
+        _need_mx4(x, offsets, sorted_routes, E, f, w_gate, w_up, w_down, s_gate, s_up, s_down)
     elif d2 != d or tuple(w_up.shape) != (E, f, d) or tuple(w_down.shape) != (E, d, f):
         raise ValueError("weight shapes must be w_gate/w_up [E,f,d] and w_down [E,d,f]")
     if offsets.numel() != E + 2 or sorted_routes.numel() != T * k:
@@ -217,6 +226,8 @@ def grouped_ffn(x, offsets, sorted_routes, w_gate, w_up, w_down, k: int, s_gate=
     _need(y, "y", torch.float32, 2)
     if workspace is None:
         workspace = _ffn_ws(desc, x.device, None)
+    if mx4:
+        _need_y(y, T * k, d, workspace, x.device)
     rc = lib.moe_grouped_ffn(ctypes.byref(desc), _ptr(x), _ptr(offsets), _ptr(sorted_routes),
                              _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(s_gate), _ptr(s_up),
                              _ptr(s_down), _ptr(y), _ptr(workspace), workspace.numel(), _stream())
@@ -231,30 +242,25 @@ def grouped_ffn_codes(xq, xs, offsets, sorted_routes, w_gate, w_up, w_down, k: i
     and quant_rows_fp8 give them."""
     torch = _torch()
     lib = _lib.load()
+    dev = _on_current(xq, "xq")
     _need(xq, "xq", torch.uint8, 2)
-    _need(xs, "xs", torch.float32, 1)
-    for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
-        _need(w, name, torch.uint8, 3)
-    for name, s in (("s_gate", s_gate), ("s_up", s_up), ("s_down", s_down)):
-        _need(s, name, torch.float32, 3)
-    _need(offsets, "offsets", torch.int32, 1)
-    _need(sorted_routes, "sorted_routes", torch.int32, 1)
+    _need(w_gate, "w_gate", torch.uint8, 3)
     T, d = xq.shape
     E, f, _ = w_gate.shape
-    for name, t, shape in (("xs", xs, (T,)), ("w_gate", w_gate, (E, f, d)),
-                           ("w_up", w_up, (E, f, d)), ("w_down", w_down, (E, d, f)),
-                           ("s_gate", s_gate, (E, f // 128, d // 128)),
-                           ("s_up", s_up, (E, f // 128, d // 128)),
-                           ("s_down", s_down, (E, d // 128, f // 128)),
-                           ("offsets", offsets, (E + 2,)), ("sorted_routes", sorted_routes, (T * k,))):
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    u8, f32, i32 = (torch.uint8,), (torch.float32,), (torch.int32,)
+    for name, t, shape, dtypes in (
+            ("xs", xs, (T,), f32), ("w_gate", w_gate, (E, f, d), u8), ("w_up", w_up, (E, f, d), u8),
+            ("w_down", w_down, (E, d, f), u8), ("s_gate", s_gate, (E, f // 128, d // 128), f32),
+            ("s_up", s_up, (E, f // 128, d // 128), f32),
+            ("s_down", s_down, (E, d // 128, f // 128), f32), ("offsets", offsets, (E + 2,), i32),
+            ("sorted_routes", sorted_routes, (T * k,), i32)):
+        _need_rows(t, name, shape, dtypes, dev)
     desc = ffn_desc(T, k, E, d, f, weights="fp8")
     if y is None:
-        y = torch.empty(T * k, d, dtype=torch.float32, device=xq.device)
-    _need(y, "y", torch.float32, 2)
+        y = torch.empty(T * k, d, dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = _ffn_ws(desc, xq.device, None)
+        workspace = _ffn_ws(desc, dev, None)
+    _need_y(y, T * k, d, workspace, dev)
     rc = lib.moe_grouped_ffn_codes(ctypes.byref(desc), _ptr(xq), _ptr(xs), _ptr(offsets),
                                    _ptr(sorted_routes), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                                    _ptr(s_gate), _ptr(s_up), _ptr(s_down), _ptr(y),
@@ -503,6 +509,7 @@ def decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_
     if workspace is None:
         workspace = torch.empty(max(lib.moe_decode_ffn_workspace(desc), 256), dtype=torch.uint8,
                                 device=dev)
+    _need_rows(workspace, "workspace", workspace.shape, (torch.uint8,), dev)
     f32 = out.dtype == torch.float32
     rc = lib.moe_decode_ffn(desc, x.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
                             _ptr(route_mask), w_gate.data_ptr(), w_up.data_ptr(),

@@ -158,6 +158,33 @@ def test_graph_replays():
         args[1].copy_(np_dev(ids))
 
 
+def test_two_streams_and_the_workspaces_end():
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    lib = rep.load_library()
+    runs = []
+    for seed in (17, 18):
+        p = _problem(5, 4, 12, 640, 384, seed=seed, mask_p=0.2)
+        ids, w, mask, x, W = p
+        n = lib.moe_decode_ffn_workspace(rep.ffn_desc(5, 4, 12, 640, 384, weights="mxfp4"))
+        ws = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        out = torch.full((7, 640), 7.0, device="cuda")
+        runs.append(((bf16_dev(x), np_dev(ids), np_dev(w), np_dev(mask), *_dev(W)), n, ws, out,
+                     _decode(p)))
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (args, _, ws, out, _) in zip(streams, runs):
+            with torch.cuda.stream(s):
+                rep.decode_ffn(*args, out=out[:5], workspace=ws)
+    torch.cuda.synchronize()
+    for _, n, ws, out, want in runs:
+        assert torch.equal(out[:5].view(torch.int32), want.view(torch.int32))
+        assert (out[5:] == 7).all() and (ws[n:] == 0xA5).all()
+
+
 def test_refusals():
     import torch
 
@@ -175,7 +202,9 @@ def test_refusals():
                 dict(s_down=good["s_gate"]), dict(w_up=good["w_up"].cpu()),
                 dict(shared=torch.zeros(3, 128, device="cuda")),
                 dict(out=torch.zeros(3, 256, device="cuda", dtype=torch.float16)),
-                dict(w_down=good["w_down"].transpose(0, 1))):
+                dict(w_down=good["w_down"].transpose(0, 1)),
+                dict(workspace=torch.empty(4096, dtype=torch.uint8)),
+                dict(out=torch.zeros(2, 256, device="cuda"))):
         with pytest.raises((TypeError, ValueError)):
             rep.decode_ffn(**{**good, **bad})
     with pytest.raises(RuntimeError, match="MOE_EWORKSPACE"):

@@ -95,8 +95,23 @@ def test_fp8_on_given_codes_is_the_fp8_path():
         layer((q, s), *args, stage_events=[None] * 6)
     with pytest.raises(ValueError):
         rep.MoEPrefill(T, k, E, d, f)((q, s), *args)
+    # on a stream of its own, and replayed
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = layer((q, s), *args)
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int32), want.view(torch.int32))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer((q, s), *args)
+    for _ in range(3):
+        layer.out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.out.view(torch.int32), want.view(torch.int32))
+        assert torch.equal(layer(x, *args).view(torch.int32), want.view(torch.int32))
     rt = layer.rt
-    for bad in (dict(xq=q[:, :256].contiguous()), dict(xs=s[:5]), dict(xq=x), dict(xs=s.cpu()),
+    for bad in (dict(y=layer.y[1:]), dict(y=layer.y[:, :256].contiguous()),
+                dict(workspace=layer.ffn_ws.cpu()), dict(xq=q[:, :256].contiguous()), dict(xs=s[:5]), dict(xq=x), dict(xs=s.cpu()),
                 dict(w_down=Wd["wg"]), dict(s_up=Wd["sd"]), dict(offsets=rt.counts)):
         a = dict(xq=q, xs=s, offsets=rt.offsets, sorted_routes=rt.sorted_routes, k=k,
                  **dict(zip(("w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down"), weights)))

@@ -204,6 +204,70 @@ def test_runs_again_bit_for_bit_and_in_graph_replays():
         assert torch.equal(run(*args).view(torch.int32), eager.view(torch.int32))
 
 
+@pytest.mark.parametrize("d,f", [(4864, 256), (128, 4736)])
+def test_few_rows_of_a_long_reduction(d, f):
+    """Rows too long for LDS: tiles of at most 16 rows then go through the
+    ring, here with a last group of codes that is half there."""
+    p = _problem([1, 16, 5, 17, 0, 9], 2, d, f, seed=d)
+    E, ids, w, mask, x, W = p
+    _, out = _run(p)
+    _close(out, omoe.moe_ref_blocked(x, ids, w, mask, bf16_source(W), E)[0])
+
+
+def test_not_a_number_stays_in_its_token():
+    """Tiles of every height with a NaN and an infinity in one row each."""
+    p = _problem(CLASS_COUNTS, 6, 384, 256, seed=12)
+    E, ids, w, mask, x, W = p
+    _, clean = _run(p)
+    x = x.copy()
+    x[3, 7], x[50, 300] = 0x7FC0, 0x7F80
+    _, out = _run((E, ids, w, mask, x, W))
+    read = (mask != 0).any(1)
+    assert read[3] and read[50] and np.isnan(out[3]).all()
+    rest = np.delete(np.arange(ids.shape[0]), [3, 50])
+    assert np.array_equal(out[rest], clean[rest])
+
+
+def test_an_expert_named_twice_by_a_token():
+    p = _problem([20, 3, 0, 0], 4, 256, 128, seed=13, masked=0)
+    E, ids, w, mask, x, W = p
+    ids[:] = np.array([0, 1, 0, 0], np.int32)
+    _, out = _run(p)
+    _close(out, omoe.moe_ref_blocked(x, ids, w, mask, bf16_source(W), E)[0])
+
+
+def test_two_streams_and_the_workspaces_end():
+    """Two layers at once, each on a stream and in a workspace of its own, that
+    write nothing behind the bytes they asked for."""
+    import ctypes
+
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    lib = rep.load_library()
+    runs = []
+    for seed in (14, 15):
+        p = _problem([70, 0, 300, 9, 130], 3, 512, 256, seed=seed)
+        E, ids, w, mask, x, W = p
+        layer = rep.MoEPrefill(*ids.shape, E, 512, 256, weights="mxfp4")
+        layer.decode = False
+        n = lib.moe_grouped_ffn_workspace(ctypes.byref(layer.desc))
+        layer.ffn_ws = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        runs.append((layer, n, (bf16_dev(x), np_dev(ids), np_dev(w), np_dev(mask), *_dev(W)),
+                     _run(p)[1]))
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (layer, _, args, _) in zip(streams, runs):
+            with torch.cuda.stream(s):
+                layer(*args)
+    torch.cuda.synchronize()
+    for layer, n, _, want in runs:
+        assert np.array_equal(layer.out.cpu().numpy().astype(np.float64), want)
+        assert (layer.ffn_ws[n:] == 0xA5).all()
+
+
 def test_refusals():
     import torch
 
@@ -227,6 +291,14 @@ def test_refusals():
                 dict(w_up=good["w_up"].transpose(1, 2)), dict(s_up=good["s_up"].cpu())):
         with pytest.raises((TypeError, ValueError)):
             call(**bad)
+    base = (bf16_dev(x), rt.offsets, rt.sorted_routes, *(good[n] for n in names[:3]), 1,
+            *(good[n] for n in names[3:]))
+    for bad in (dict(y=torch.empty(6, 256, device="cuda")), dict(y=torch.empty(7, 128, device="cuda")),
+                dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            rep.grouped_ffn(*base, **bad)
+    with pytest.raises(RuntimeError, match="MOE_EWORKSPACE"):
+        rep.grouped_ffn(*base, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         rep.MoEPrefill(7, 1, 2, 256, 128, weights="int4")
     with pytest.raises(ValueError):
