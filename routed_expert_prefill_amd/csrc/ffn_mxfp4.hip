@@ -28,7 +28,8 @@ struct M4Heads {
 struct M4Schedule {
   int n_tiles;  // entries of the tile list, tallest capacity first
   int n_small;  // tiles of at most kM4DirectRows rows, the last n_small entries
-  int pad[2];
+  int n_stream;  // tiles for m4_stream ahead of them
+  int pad;
   M4Heads heads[2];  // gate/up, down
 };
 static_assert(sizeof(M4Schedule) <= sizeof(Schedule), "has the schedule's place");
@@ -43,7 +44,8 @@ struct Mx4Args {
   int N, K;
   const Tile *tiles;
   const int *ntiles;
-  const int *n_small;  // tiles of at most kM4DirectRows rows at the end of the tile list
+  const int *n_small;  // tiles of at most kM4DirectRows rows at the end of the tile list,
+                       // and in the next word the number of those for m4_stream ahead of them
   M4Heads *heads;      // of the work queues (M4Queues), zeroed by the plan
 };
 
@@ -156,7 +158,7 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   constexpr int TT = L::TT, TW = L::TW;
   constexpr int JA = KB * AR / 8 / kM4Waves;       // activation loads (8 rows) of a wave per stage
   constexpr int JW = kM4WRows * GB / 32 / kM4Waves;  // code loads (1 KB) of a wave per group
-  const int lane = lane_id();
+  const int lane = vreg(lane_id());
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int K = a.K;
   const int nst = K / (64 * KB);
@@ -463,16 +465,16 @@ struct M4Scales {
   i32x4 v[2][2];
 };
 
-// Output features [n0, n1) of a tile.
+// 512 weight rows (features from n0) of a tile.
 // WIDE (K a multiple of 1024): the scales come in whole lines, a chunk's 16
 // bytes per row passing through LDS to the lanes that multiply; fetched with
 // each chunk instead, 16 bytes of a line at a time, they cost twice their
 // share of the bytes (MI355X, 401 tokens: gate/up 440 us, 390 without scales).
 template <bool GATEUP, bool WIDE>
-__device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n0, int n1,
-                                          uint8_t *lds) {
+__device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n0, uint8_t *lds) {
   constexpr int FG = GATEUP ? 16 : 32;  // features of a wave's two weight tiles
-  const int lane = lane_id();
+  const int n1 = min(n0 + 2 * kM4Waves * FG, a.N);
+  const int lane = vreg(lane_id());
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane >> 4, row = lane & 15;
   const int K = a.K, nk = K / 128;
@@ -627,6 +629,172 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
   }
 }
 
+// ------------------------------------------------------------------ up to 64 rows
+
+// Tiles of 17 to 64 rows over a reduction of whole slices of 512 columns.
+// Weights go straight into registers as in m4_direct, chunk by chunk of 256
+// columns; of the activations two slices of 64 rows are in LDS, the next one
+// on its way while one is multiplied, and the waves meet once per slice.
+// Wave w takes weight rows [64 w, 64 w + 64) of the item's 512.
+//
+// Row r of a slice takes 1 KB of LDS, one load of a wave; its 16-byte chunk
+// p lies at p ^ (r % 8), so that eight lanes reading one chunk of consecutive
+// rows touch all banks once.
+constexpr int kM4SliceCols = 512;
+constexpr int kM4StreamRows = 64;
+constexpr int kM4Slice = kM4StreamRows * kM4SliceCols * 2;
+static_assert(2 * kM4Slice <= kM4Ring, "two slices fit");
+
+__device__ __forceinline__ bool m4_stream_takes(int K) { return K % kM4SliceCols == 0; }
+
+// One chunk of a wave's four weight tiles of 16 rows: two steps of 128 columns.
+struct M4Chunk2 {
+  i32x4 raw[2][4];
+};
+
+// 512 weight rows (features from n0) of a tile of up to 16 TM rows.
+template <bool GATEUP, int TM>
+__device__ __forceinline__ void m4_stream(const Mx4Args &a, const Tile &t, int n0, uint8_t *lds,
+                                          uint32_t lds_base) {
+  constexpr int FG = GATEUP ? 32 : 64;  // features of a wave's four weight tiles
+  const int lane = vreg(lane_id());
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane >> 4, row = lane & 15;
+  const int K = a.K, slices = K / kM4SliceCols;
+  const int nw = n0 + wv * FG;
+  // waves past the last feature keep the others company on its rows
+  const size_t first = (size_t)t.e * a.N + min(nw, a.N - FG);
+  const uint8_t *const w0 = a.w0 + first * (K / 2), *const w1 = GATEUP ? a.w1 + first * (K / 2) : w0;
+  // tile w of a wave: gate/up: gate and up rows of 16 features, then of the next 16
+  auto tile_row = [](int w) { return GATEUP ? (w >> 1) * 16 : w * 16; };
+  constexpr int NO = GATEUP ? 2 : 4;
+  uint32_t code_off[NO];
+#pragma unroll
+  for (int i = 0; i < NO; ++i) code_off[i] = (uint32_t)vreg(i * 16 + row) * (K / 2) + c * 16;
+
+  auto load = [&](M4Chunk2 &q, int ch) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint8_t *base = (GATEUP && (w & 1) ? w1 : w0) + (uint32_t)ch * 128;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        q.raw[u][w] = *reinterpret_cast<const i32x4 *>(base + code_off[GATEUP ? w >> 1 : w] + u * 64);
+    }
+    asm volatile("" ::: "memory");  // issued here, not where they are used
+  };
+  // The scales of four slices: lane group c holds those of slice c, 16 bytes a row.
+  auto load_scales = [&](i32x4 (&q)[4], int s) {
+    const size_t at = (size_t)(w0 - a.w0) / 16;  // a byte of scales to 16 of codes
+    const uint32_t off = (uint32_t)row * (K / 32) + (uint32_t)min(s + c, slices - 1) * 16;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      q[w] = *reinterpret_cast<const i32x4 *>((GATEUP && (w & 1) ? a.s1 : a.s0) + at +
+                                            tile_row(w) * (K / 32) + off);
+    asm volatile("" ::: "memory");
+  };
+  // source row of tile row wv + 8 l in lane l; rows past the last repeat it
+  const int tile_at = t.row0 + min(wv + kM4Waves * (lane & 7), t.nrows - 1);
+  const int src = GATEUP ? a.sorted_routes[tile_at] / a.k : tile_at;
+  const uint32_t act_off = (uint32_t)((lane ^ wv) * 16);
+  // this wave's rows of slice s: wv, wv + 8, ..
+  auto issue = [&](int s) {
+    const uint32_t to = lds_base + (uint32_t)((s & 1) * kM4Slice + wv * 1024);
+#pragma unroll
+    for (int i = 0; i < 16 * TM / kM4Waves; ++i) {
+      const size_t from = (size_t)__builtin_amdgcn_readlane(src, i) * K + (size_t)s * kM4SliceCols;
+      m4_dma16(a.act + from, act_off, to + (uint32_t)(i * kM4Waves * 1024));
+    }
+  };
+
+  f32x4 acc[4][TM] = {};
+  i32x4 sa[4];  // scales of the four slices being multiplied
+  const int sel = row * 4;
+  // half of slice s, with between() behind its first products
+  auto multiply = [&](const M4Chunk2 &q, int s, int half, auto between) {
+    const uint8_t *ap = lds + (s & 1) * kM4Slice + row * 1024 + half * 512;
+    bf16x8 fa[2][TM];
+    auto read = [&](int x) {
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+        fa[x & 1][m] = *reinterpret_cast<const bf16x8 *>(
+            ap + m * 16384 + (x >> 2) * 256 + (((c * 4 + (x & 3)) ^ (lane & 7)) * 16));
+    };
+    read(0);
+    float scale[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute(
+            sel + (s & 3) * 64, half == 0 ? sa[w][u] : sa[w][2 + u]);
+        scale[u][w] = mx4_scale((v >> (8 * c)) & 0xffu);
+      }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (x < 7) read(x + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const bf16x8 fw = mx4_decode8((uint32_t)q.raw[x >> 2][w][x & 3], scale[x >> 2][w]);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[w][m] = mfma_bf16(fw, fa[x & 1][m], acc[w][m]);
+      }
+      if (x == 0) between();
+    }
+  };
+
+  M4Chunk2 qa, qb;
+  load_scales(sa, 0);
+  load(qa, 0);
+  ring_barrier();  // every wave has read its item, which lies where the rows go
+  issue(0);
+  wait_vm_imm<0>();
+  ring_barrier();
+#pragma unroll 1
+  for (int s4 = 0; s4 < slices; s4 += 4) {
+    const int end = min(s4 + 4, slices);
+#pragma unroll 1
+    for (int s = s4; s < end; ++s) {
+      load(qb, 2 * s + 1);
+      // The other slice's place is free since the last barrier.  These loads
+      // are older than the chunk that is loaded next and younger than this one,
+      // so no wait for codes is longer for them.
+      multiply(qa, s, 0, [&] {
+        if (s + 1 < slices) issue(s + 1);
+      });
+      load(qa, min(2 * s + 2, 2 * slices - 1));
+      multiply(qb, s, 1, [] {});
+      wait_vm_imm<8>();  // all but the chunk's: slice s + 1 is here
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      ring_barrier();
+    }
+    load_scales(sa, s4 + 4);
+  }
+  if (nw >= a.N) return;
+  // register r of lane l: weight row 4 (l / 16) + r, activation row l % 16
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    if (m * 16 + row >= t.nrows) continue;
+    const size_t o = (size_t)(t.row0 + m * 16 + row) * a.N + nw + 4 * c;
+    if (GATEUP) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 g = acc[2 * h][m], u = acc[2 * h + 1][m];
+        uint2 v;
+        v.x = (uint32_t)f32_to_bf16_bits(swiglu(g[0], u[0])) |
+              ((uint32_t)f32_to_bf16_bits(swiglu(g[1], u[1])) << 16);
+        v.y = (uint32_t)f32_to_bf16_bits(swiglu(g[2], u[2])) |
+              ((uint32_t)f32_to_bf16_bits(swiglu(g[3], u[3])) << 16);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + o + 16 * h) = v;
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + o + 16 * w) = acc[w][m];
+    }
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 
 // The tile list, one thread per expert: its full tiles of `cap` rows, then one
@@ -653,6 +821,7 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     n = offsets[e + 1] - row0;
   }
   int cap = kTileRows;
+  bool many = false;
   for (; cap > 64; cap /= 2) {
     int v = (n + cap - 1) / cap;
 #pragma unroll
@@ -663,6 +832,7 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += waves[0][w];
     __syncthreads();
+    many = cap == kTileRows && (long long)v * blocks >= 2 * grid;
     if ((long long)v * blocks >= grid) break;
   }
   const int full = n / cap, rem = n % cap;
@@ -682,10 +852,11 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     at[c] = v - mine;
   }
   __syncthreads();
-  int total = 0, last = 0;
+  int total = 0, last = 0, before = 0;  // all tiles; of the last class; of the one before it
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     at[c] += total;
+    before = last;
     last = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
@@ -708,6 +879,7 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
   if (e == 0) {
     sch->n_tiles = total;
     sch->n_small = last;
+    sch->n_stream = many ? before : 0;
   }
 }
 
@@ -816,12 +988,15 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
   constexpr int kHalf = GATEUP ? 2 : 1;  // gate and up rows of one feature
   constexpr int FB = kM4WRows / kHalf;  // features per item of the ring
   if (threadIdx.x == 0) {
-    const int FS = m4_direct_fits(a.K) ? 2 * FB : FB;  // and of tiles of few rows
-    state[0] = *a.ntiles - *a.n_small;
-    state[1] = *a.n_small;
+    const int streamed = m4_stream_takes(a.K) ? a.n_small[1] : 0;
+    // and of tiles of few rows
+    const int FS = m4_direct_fits(a.K) || streamed ? 2 * FB : FB;
+    state[1] = a.n_small[0] + (FS == FB ? 0 : streamed);
+    state[0] = *a.ntiles - state[1];
     state[2] = (a.N + FB - 1) / FB;  // items per tile
     state[3] = (a.N + FS - 1) / FS;
     state[4] = (int)blockIdx.x % kM4Queues;
+    state[6] = FS;
     state[5] = M4Queues(a.heads, state).fixed();
   }
   unsigned long long drawn = 0;
@@ -837,11 +1012,12 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
         state[4] = queues.q;
       }
       begin = false;
-      const int FS = m4_direct_fits(a.K) ? 2 * FB : FB, nbig = queues.nbig;
+      const bool small = ti >= queues.nbig && state[6] != FB;  // an item of twice the features
       next_item[0] = some ? ti : -1;
-      next_item[1] = some ? part * (ti < nbig ? FB : FS) : 0;
+      next_item[1] = some ? part * (small ? 2 * FB : FB) : 0;
       next_item[2] = a.K;
       next_item[3] = a.N;
+      next_item[4] = small;
     }
     __syncthreads();
     // read before the item's first barrier (its loads overwrite it); the
@@ -853,6 +1029,7 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     Mx4Args ai = a;
     ai.K = __builtin_amdgcn_readfirstlane(next_item[2]);
     ai.N = __builtin_amdgcn_readfirstlane(next_item[3]);
+    const bool small = __builtin_amdgcn_readfirstlane(next_item[4]);
     const Tile t = a.tiles[ti];
     if (threadIdx.x == 0 && !state[5])
       drawn = M4Queues(a.heads, state).draw();  // for the item after this one
@@ -860,14 +1037,19 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
       case 8: m4_item<GATEUP, 256>(ai, t, n0, ring, ring_lds); break;
       case 6: m4_item<GATEUP, 192>(ai, t, n0, ring, ring_lds); break;
       case 4: m4_item<GATEUP, 128>(ai, t, n0, ring, ring_lds); break;
-      case 2: m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds); break;
       default:
-        if (m4_direct_fits(ai.K) && ai.K % 1024 == 0)
-          m4_direct<GATEUP, true>(ai, t, n0, min(n0 + 2 * FB, ai.N), ring);
-        else if (m4_direct_fits(ai.K))
-          m4_direct<GATEUP, false>(ai, t, n0, min(n0 + 2 * FB, ai.N), ring);
-        else
+        if (!small)
           m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds);
+        else if (t.nrows > kM4DirectRows || !m4_direct_fits(ai.K))
+          switch ((t.nrows + 15) / 16) {
+            case 4: m4_stream<GATEUP, 4>(ai, t, n0, ring, ring_lds); break;
+            case 3: m4_stream<GATEUP, 3>(ai, t, n0, ring, ring_lds); break;
+            default: m4_stream<GATEUP, 2>(ai, t, n0, ring, ring_lds); break;
+          }
+        else if (ai.K % 1024 == 0)
+          m4_direct<GATEUP, true>(ai, t, n0, ring);
+        else
+          m4_direct<GATEUP, false>(ai, t, n0, ring);
         break;
     }
     // the ring (and the item in it) is rewritten only after every wave has

@@ -109,6 +109,35 @@ def test_many_tiles_of_one_height(rows):
     _close(out, total)
 
 
+@pytest.mark.parametrize("E,d,f", [
+    (96, 1536, 1536),  # both projections by slices of 512 columns
+    (160, 1024, 640),  # gate/up only, its last item half full
+    (200, 640, 1024),  # down only, the same
+    (130, 5120, 512),  # rows too long for LDS: the smallest tiles too
+])
+def test_tiles_of_up_to_64_rows(E, d, f):
+    """Enough items that tiles of up to 64 rows stream their weights: every
+    number of 16-row tiles, beside shorter and taller tiles."""
+    sizes = [17, 24, 32, 33, 40, 48, 49, 60, 64, 9, 16, 70, 0, 1]
+    p = _problem([sizes[e % len(sizes)] for e in range(E)], 4, d, f, seed=E)
+    _, ids, w, mask, x, W = p
+    run, out = _run(p)
+    rt = route_table(ids, mask, E)
+    n = int(rt.offsets[E])
+    y = run.y.cpu().numpy()
+    assert np.isnan(y[n:]).all() and not np.isnan(y[:n]).any()
+    sample = [int(rt.sorted_routes[i]) for i in range(0, n, 41)]
+    _close(y[rt.route_rows[sample]], omoe.route_outputs_ref(x, ids, bf16_source(W), sample))
+    # every row, by another path: a call of few experts' routes takes other tiles
+    for g in range(0, 24, 8):
+        some = np.where((ids >= g) & (ids < g + 8), mask, 0).astype(np.uint8)
+        part, _ = _run((E, ids, w, some, x, W))
+        rows = [r for r in range(ids.size) if some.flat[r]]
+        there = route_table(ids, some, E).route_rows[rows]
+        _close(y[rt.route_rows[rows]].astype(np.float64),
+               part.y.cpu().numpy()[there].astype(np.float64))
+
+
 def test_masked_and_out_of_range_routes_add_exact_zeros():
     p = _problem([5, 0, 40, 3], 3, 256, 128, seed=5, masked=20, invalid=6)
     E, ids, w, mask, x, W = p
