@@ -149,6 +149,11 @@ __device__ __forceinline__ void m4_wait(int i) {
     wait_vm_imm<JA *(NS - 2) + 2 * JW>();
 }
 
+template <int N>
+struct M4Tiles {
+  static constexpr int n = N;
+};
+
 // 256 weight rows (features from n0) of a tile of up to AR rows.
 template <bool GATEUP, int AR>
 __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0, uint8_t *ring,
@@ -174,7 +179,6 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     return GATEUP ? (wr >> 5) * 16 + (wr & 15) : min(wr, a.N - 1 - n0);
   };
   const size_t first = (size_t)t.e * a.N + n0;
-  const uint8_t *const w0 = a.w0 + first * (K / 2), *const w1 = GATEUP ? a.w1 + first * (K / 2) : w0;
   const uint8_t *const s0 = a.s0 + first * (K / 32), *const s1 = GATEUP ? a.s1 + first * (K / 32) : s0;
   // this lane's source of each of its loads in the first stage and group
   const uint8_t *act[JA];
@@ -185,12 +189,15 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     const int kb = i / (AR / 8);
     const int r = (i - kb * (AR / 8)) * 8 + (lane >> 3);
     const int row = t.row0 + min(r, t.nrows - 1);
-    const size_t s = GATEUP ? (size_t)(a.sorted_routes[row] / a.k) : (size_t)row;
+    const size_t s = GATEUP ? (size_t)(a.sorted_routes[row] / vreg(a.k)) : (size_t)row;
     act[j] = reinterpret_cast<const uint8_t *>(a.act + s * K) + kb * 128 +
              ring_slot(r, lane & 7) * 16;
   }
   constexpr int LPR = 2 * GB;  // lanes per row of codes; the rows of a load are of one matrix
   constexpr int RPL = 64 / LPR;
+  // all code loads of a wave are of the same matrix (they are 8 RPL rows apart)
+  static_assert(kM4Waves * RPL % 32 == 0, "of the same matrix");
+  const uint8_t *const w = (wmat(wv * RPL) ? a.w1 : a.w0) + first * (K / 2);
   int second = 0;  // bit j: load j brings columns of the group's second half
 #pragma unroll
   for (int j = 0; j < JW; ++j) {
@@ -211,7 +218,7 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
 
   auto issue_code = [&](int j, int g, int buf) {
     const int i = wv + kM4Waves * j;
-    const uint8_t *base = (wmat(i * RPL) ? w1 : w0) + (uint32_t)g * (32 * GB);
+    const uint8_t *base = w + (uint32_t)g * (32 * GB);
     uint32_t off = codes[j];
     // half a group: its first half twice (loaded, not used)
     if (GB == 4 && half && g == ngr - 1) off -= ((second >> j) & 1) * 64;
@@ -240,6 +247,8 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
   };
 
   const int rr = lane & 31, rh = lane >> 5;
+  // whether the tile has rows in this wave's last activation tile
+  const bool last = __builtin_amdgcn_readfirstlane(L::atile(wv, TT - 1) * 32 < t.nrows);
   f32x16 acc[TW][TT];
 #pragma unroll
   for (int tw = 0; tw < TW; ++tw)
@@ -250,7 +259,8 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
 
   // this wave's MFMAs of stage i of group g: activations in `slot`, codes in `buf`
   // with between(j) after the MFMAs of step j
-  auto mma_stage = [&](int g, int i, int slot, int buf, auto between) {
+  auto mma_stage = [&](auto tiles, int g, int i, int slot, int buf, auto between) {
+    constexpr int N = decltype(tiles)::n;
     const int q = L::kSplit ? wv >> 2 : 0;  // this wave's block of the stage
     const uint8_t *ap = ring + slot * L::kAct + q * (AR * 128);
     const uint8_t *cp = ring + L::kCodeBase + buf * L::kCodes;
@@ -262,10 +272,10 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
     // (8192 tokens: gate/up 1.66 -> 1.59 ms), for which the registers of
     // 256-row tiles do not suffice.
     constexpr bool AHEAD = AR < 256;
-    bf16x8 fa[AHEAD ? 2 : 1][TT];
+    bf16x8 fa[AHEAD ? 2 : 1][N];
     auto read_act = [&](int j) {
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt)
+      for (int tt = 0; tt < N; ++tt)
         fa[AHEAD ? j & 1 : 0][tt] = *reinterpret_cast<const bf16x8 *>(
             ap + (L::atile(wv, tt) * 32 + rr) * 128 + ring_slot(rr, 4 * rh + j) * 16);
     };
@@ -294,7 +304,8 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
       for (int tw = 0; tw < TW; ++tw) {
         const bf16x8 fw = mx4_decode8((uint32_t)raw[tw][j], scale[tw]);
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) acc[tw][tt] = mfma32_bf16(fw, fa[AHEAD ? j & 1 : 0][tt], acc[tw][tt]);
+        for (int tt = 0; tt < N; ++tt)
+          acc[tw][tt] = mfma32_bf16(fw, fa[AHEAD ? j & 1 : 0][tt], acc[tw][tt]);
       }
       between(j);
     }
@@ -317,54 +328,61 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
 #pragma unroll
   for (int g = 1; g < NB - 1; ++g)
     if (g < ngr) issue_group(g);
-  int slot = 0, buf = 0;  // of the stage being multiplied
+  auto stages = [&](auto tiles) {
+    int slot = 0, buf = 0;  // of the stage being multiplied
 #pragma unroll 1
-  for (int g = 0; g < ngr; ++g) {
-    // What may stay in flight at the start of stage s: the activations of the
-    // NS - 2 stages after it, and the codes that went out since its own
-    // activations did (with the first stage of a group, after that stage's
-    // activations).  Between the first groups and the last NB that is a
-    // constant.  Scales are not counted: the wait is then one load longer.
-    const bool steady = g * S >= NS - 1 && g + NB < ngr;
-    const bool codes_too = g + NB - 1 < ngr;
+    for (int g = 0; g < ngr; ++g) {
+      // What may stay in flight at the start of stage s: the activations of the
+      // NS - 2 stages after it, and the codes that went out since its own
+      // activations did (with the first stage of a group, after that stage's
+      // activations).  Between the first groups and the last NB that is a
+      // constant.  Scales are not counted: the wait is then one load longer.
+      const bool steady = g * S >= NS - 1 && g + NB < ngr;
+      const bool codes_too = g + NB - 1 < ngr;
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int s = g * S + i;
-      if (GB == 4 && i >= S / 2 && s >= nst) break;  // half a group
-      if (steady) {
-        m4_wait<JA, JW, NS, S>(i);
-      } else {
-        int n = JA * min(NS - 2, nst - 1 - s);
-        if (s <= NS - 2) n += JW * min(NB - 2, ngr - 1);  // issued ahead of the loop
+      for (int i = 0; i < S; ++i) {
+        const int s = g * S + i;
+        if (GB == 4 && i >= S / 2 && s >= nst) break;  // half a group
+        if (steady) {
+          m4_wait<JA, JW, NS, S>(i);
+        } else {
+          int n = JA * min(NS - 2, nst - 1 - s);
+          if (s <= NS - 2) n += JW * min(NB - 2, ngr - 1);  // issued ahead of the loop
 #pragma unroll
-        for (int x = 1; x < NS; ++x) {
-          const int h = g - (x - i + S - 1) / S;  // the group of stage s - x if that is its first
-          if (x >= i && (x - i) % S == 0 && h >= 0 && h + NB - 1 < ngr) n += JW;
-        }
-        wait_vm(n);
-      }
-      ring_barrier();  // the stage is in LDS for everyone; stage s - 1 is consumed
-      // the next loads go out between the products: all at once, ahead of
-      // them, they kept the waves from starting
-      const bool more = s + NS - 1 < nst;
-      mma_stage(g, i, slot, buf, [&](int j) {
-        constexpr int N = JA + JW;
-        const int to_slot = slot == 0 ? NS - 1 : slot - 1, to_buf = buf == 0 ? NB - 1 : buf - 1;
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-          if (x * 4 / N != j) continue;
-          if (x < JA) {
-            if (more) issue_act(x, s + NS - 1, to_slot);
-          } else if (i == 0 && codes_too) {
-            issue_code(x - JA, g + NB - 1, to_buf);
-            if (x == N - 1) issue_scales(g + NB - 1);
+          for (int x = 1; x < NS; ++x) {
+            const int h = g - (x - i + S - 1) / S;  // the group of stage s - x if that is its first
+            if (x >= i && (x - i) % S == 0 && h >= 0 && h + NB - 1 < ngr) n += JW;
           }
+          wait_vm(n);
         }
-      });
-      slot = slot == NS - 1 ? 0 : slot + 1;
+        ring_barrier();  // the stage is in LDS for everyone; stage s - 1 is consumed
+        // the next loads go out between the products: all at once, ahead of
+        // them, they kept the waves from starting
+        const bool more = s + NS - 1 < nst;
+        const auto between = [&](int j) {
+          constexpr int N = JA + JW;
+          const int to_slot = slot == 0 ? NS - 1 : slot - 1, to_buf = buf == 0 ? NB - 1 : buf - 1;
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            if (x * 4 / N != j) continue;
+            if (x < JA) {
+              if (more) issue_act(x, s + NS - 1, to_slot);
+            } else if (i == 0 && codes_too) {
+              issue_code(x - JA, g + NB - 1, to_buf);
+              if (x == N - 1) issue_scales(g + NB - 1);
+            }
+          }
+        };
+        mma_stage(tiles, g, i, slot, buf, between);
+        slot = slot == NS - 1 ? 0 : slot + 1;
+      }
+      buf = buf == NB - 1 ? 0 : buf + 1;
     }
-    buf = buf == NB - 1 ? 0 : buf + 1;
-  }
+  };
+  if (L::kSplit || last)
+    stages(M4Tiles<TT>{});
+  else
+    stages(M4Tiles<L::kSplit ? TT : TT - 1>{});
 
   if constexpr (L::kSplit) {
     f32x4 *sums = reinterpret_cast<f32x4 *>(ring) + (wv & 3) * (TW * TT * 256) + lane;
@@ -579,7 +597,7 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
   // wave w brings rows w and w + 8
   for (int r = wv; r < t.nrows; r += kM4Waves) {
     const int i = t.row0 + r;
-    const size_t s = GATEUP ? (size_t)(a.sorted_routes[i] / a.k) : (size_t)i;
+    const size_t s = GATEUP ? (size_t)(a.sorted_routes[i] / vreg(a.k)) : (size_t)i;
     for (int p0 = 0; p0 < K / 8; p0 += 8 * kWave) {
       i32x4 v[8];
 #pragma unroll
@@ -694,7 +712,7 @@ __device__ __forceinline__ void m4_stream(const Mx4Args &a, const Tile &t, int n
   };
   // source row of tile row wv + 8 l in lane l; rows past the last repeat it
   const int tile_at = t.row0 + min(wv + kM4Waves * (lane & 7), t.nrows - 1);
-  const int src = GATEUP ? a.sorted_routes[tile_at] / a.k : tile_at;
+  const int src = GATEUP ? a.sorted_routes[tile_at] / vreg(a.k) : tile_at;
   const uint32_t act_off = (uint32_t)((lane ^ wv) * 16);
   // this wave's rows of slice s: wv, wv + 8, ..
   auto issue = [&](int s) {
@@ -991,19 +1009,29 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     const int streamed = m4_stream_takes(a.K) ? a.n_small[1] : 0;
     // and of tiles of few rows
     const int FS = m4_direct_fits(a.K) || streamed ? 2 * FB : FB;
-    state[1] = a.n_small[0] + (FS == FB ? 0 : streamed);
+    state[1] = a.n_small[0] + streamed;
     state[0] = *a.ntiles - state[1];
     state[2] = (a.N + FB - 1) / FB;  // items per tile
     state[3] = (a.N + FS - 1) / FS;
     state[4] = (int)blockIdx.x % kM4Queues;
     state[6] = FS;
+    state[7] = a.K;
+    state[8] = a.N;
     state[5] = M4Queues(a.heads, state).fixed();
   }
   unsigned long long drawn = 0;
   bool begin = true;
+  // the heads from the tile list, at a distance that takes no scalar register
+  // (both lie in the workspace, which one int spans between them)
+  const int heads_at = vreg((int)(reinterpret_cast<const char *>(a.heads) -
+                                  reinterpret_cast<const char *>(a.tiles)));
+  const auto heads = [&] {
+    return reinterpret_cast<M4Heads *>(reinterpret_cast<char *>(const_cast<Tile *>(a.tiles)) +
+                                       heads_at);
+  };
   for (;;) {
     if (threadIdx.x == 0) {
-      M4Queues queues(a.heads, state);
+      M4Queues queues(heads(), state);
       int ti = -1, part = 0;
       bool some = begin && queues.first(&ti, &part);
       if (!state[5]) {
@@ -1015,9 +1043,7 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
       const bool small = ti >= queues.nbig && state[6] != FB;  // an item of twice the features
       next_item[0] = some ? ti : -1;
       next_item[1] = some ? part * (small ? 2 * FB : FB) : 0;
-      next_item[2] = a.K;
-      next_item[3] = a.N;
-      next_item[4] = small;
+      next_item[2] = small;
     }
     __syncthreads();
     // read before the item's first barrier (its loads overwrite it); the
@@ -1027,12 +1053,12 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     if (ti < 0) break;
     const int n0 = __builtin_amdgcn_readfirstlane(next_item[1]);
     Mx4Args ai = a;
-    ai.K = __builtin_amdgcn_readfirstlane(next_item[2]);
-    ai.N = __builtin_amdgcn_readfirstlane(next_item[3]);
-    const bool small = __builtin_amdgcn_readfirstlane(next_item[4]);
+    ai.K = __builtin_amdgcn_readfirstlane(state[7]);
+    ai.N = __builtin_amdgcn_readfirstlane(state[8]);
+    const bool small = __builtin_amdgcn_readfirstlane(next_item[2]);
     const Tile t = a.tiles[ti];
     if (threadIdx.x == 0 && !state[5])
-      drawn = M4Queues(a.heads, state).draw();  // for the item after this one
+      drawn = M4Queues(heads(), state).draw();  // for the item after this one
     switch (tile_class(t)) {
       case 8: m4_item<GATEUP, 256>(ai, t, n0, ring, ring_lds); break;
       case 6: m4_item<GATEUP, 192>(ai, t, n0, ring, ring_lds); break;

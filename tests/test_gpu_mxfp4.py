@@ -86,7 +86,7 @@ def test_full_width():
     _close(out, omoe.moe_ref_blocked(x, ids, w, mask, bf16_source(W), E)[0])
 
 
-@pytest.mark.parametrize("rows", [13, 60, 100, 128, 180, 256])
+@pytest.mark.parametrize("rows", [13, 60, 90, 100, 128, 150, 180, 220, 256])
 def test_many_tiles_of_one_height(rows):
     """Enough items of one tile height, at a reduction of 4096 columns, to keep
     every workgroup at it for several rounds: a stage that started ahead of
