@@ -53,8 +53,8 @@ def _ptr(t) -> Optional[int]:
 def _stream() -> int:
     # the raw handle of torch.cuda.current_stream(), without making a Stream
     # object for it (about 3 us a call)
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    C = _torch()._C
+    return C._cuda_getCurrentRawStream(C._cuda_getDevice())
 
 
 def _need(t, name, dtype, ndim=None):
@@ -415,7 +415,7 @@ def _on_current(t, name):
     dev = t.device
     if dev.type != "cuda":
         raise ValueError(f"{name} must be on a GPU device")
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():  # torch.cuda.current_device(), initialised by x
         raise ValueError(f"{name} is on {dev}, which is not the current device")
     return dev
 
