@@ -1,15 +1,28 @@
 // Persistent grouped GEMM for the routed-MoE FFN with MXFP4 weights (mx4.h)
-// and bf16 activations: one kernel per projection (gate/up with the SwiGLU
-// epilogue, then down), fp32 accumulation.
+// and bf16 activations: one kernel per projection, fp32 accumulation.
 //
-// Same tile list, two work queues and direct global->LDS stage ring as the
-// bf16 kernels (ffn_grouped.hip, ring.h).  The ring holds the weights as
-// codes, a quarter of the bf16 bytes; a wave reads 16 bytes of a weight row
-// per lane -- 32 codes, exactly one scale group -- and converts them in
-// registers in front of the MFMAs, so no pass over expanded weights exists.
-// The order of the reduction inside a stage follows from that: lane half h
-// of a 64-column step holds group h of it, and MFMA j of the step multiplies
-// columns 8 j .. 8 j + 7 of both groups.
+//   gate/up: h[i, n] = bf16(silu(g) u),  g = sum_c Wg[e, n, c] x[t, c],  u likewise with Wu
+//   down:    y[i, n] = sum_c Wd[e, n, c] h[i, c]
+//
+// for sorted row i of expert e and token t.  Weights stay codes until the
+// products: a lane reads 16 bytes of a weight row, 32 codes, exactly one scale
+// group, and converts them in registers, so no pass over expanded weights
+// exists and a weight costs 4.25 bits of memory traffic.  The order of a
+// reduction follows from that (MFMA j of a step multiplies columns
+// 8 j .. 8 j + 7 of each lane group's scale group); it is fixed for a tile
+// height, and tile heights depend on the routing alone.
+//
+// What bounds an expert's tile goes with its rows, so there are three ways
+// through it (times: 256 experts, d 4096, f 2048, gate/up; MI355X):
+//   up to 16 rows   m4_direct  the weight stream: 401 tokens of top-6, about nine rows
+//                              an expert, 413 us = 5.5 TB/s of codes and scales
+//   17 to 64 rows   m4_stream  the stream, and from about 48 rows the matrix unit as much:
+//                              24 rows an expert 520 us, 48 rows 605, 64 rows 690
+//   more, and what the  m4_item    the matrix unit: 180 rows 1.53 ms, 256 rows 1.96 ms
+//   others do not take             = 1.12 PFLOP/s, where the library's dense bf16 product
+//                                  reaches 1.1 to 1.3 on this card
+// The tile list, the queues that hand tiles out (M4Queues) and the rules for
+// tile heights (mx4_schedule_kernel) are further down.
 #include "kernels.h"
 #include "mx4.h"
 #include "ring.h"
@@ -29,7 +42,7 @@ struct M4Schedule {
   int n_tiles;  // entries of the tile list, tallest capacity first
   int n_small;  // tiles of at most kM4DirectRows rows, the last n_small entries
   int n_stream;  // tiles for m4_stream ahead of them
-  int pad;
+  int many;      // whether items of tiles of few rows have twice the weight rows
   M4Heads heads[2];  // gate/up, down
 };
 static_assert(sizeof(M4Schedule) <= sizeof(Schedule), "has the schedule's place");
@@ -43,9 +56,7 @@ struct Mx4Args {
   void *out;               // gate/up: h bf16 [R, N]; down: y fp32 [R, N]
   int N, K;
   const Tile *tiles;
-  const int *ntiles;
-  const int *n_small;  // tiles of at most kM4DirectRows rows at the end of the tile list,
-                       // and in the next word the number of those for m4_stream ahead of them
+  const M4Schedule *sch;
   M4Heads *heads;      // of the work queues (M4Queues), zeroed by the plan
 };
 
@@ -454,7 +465,7 @@ __device__ __forceinline__ void m4_item(const Mx4Args &a, const Tile &t, int n0,
 // there is no barrier per stage, so no wave waits for another's loads, and
 // LDS serves the activations only.  (Through the ring, whose stages all waves
 // read at the same time, reads of activation tiles kept LDS busy for most of
-// a stage: MI355X, 401 tokens, gate/up 4.5 TB/s.)
+// a stage: MI355X, 401 tokens, gate/up 508 us; this way 413.)
 // Products are 16x16x32 MFMAs: a step is 128 columns, lane group c = l / 16
 // holds the codes of group c of a weight row l % 16 (16 bytes), and MFMA j
 // multiplies columns 8 j .. 8 j + 7 of the four groups.
@@ -483,15 +494,15 @@ struct M4Scales {
   i32x4 v[2][2];
 };
 
-// 512 weight rows (features from n0) of a tile.
+// Output features [n0, n1) of a tile.
 // WIDE (K a multiple of 1024): the scales come in whole lines, a chunk's 16
 // bytes per row passing through LDS to the lanes that multiply; fetched with
 // each chunk instead, 16 bytes of a line at a time, they cost twice their
 // share of the bytes (MI355X, 401 tokens: gate/up 440 us, 390 without scales).
 template <bool GATEUP, bool WIDE>
-__device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n0, uint8_t *lds) {
+__device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n0, int n1,
+                                          uint8_t *lds) {
   constexpr int FG = GATEUP ? 16 : 32;  // features of a wave's two weight tiles
-  const int n1 = min(n0 + 2 * kM4Waves * FG, a.N);
   const int lane = vreg(lane_id());
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane >> 4, row = lane & 15;
@@ -651,9 +662,15 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
 
 // Tiles of 17 to 64 rows over a reduction of whole slices of 512 columns.
 // Weights go straight into registers as in m4_direct, chunk by chunk of 256
-// columns; of the activations two slices of 64 rows are in LDS, the next one
-// on its way while one is multiplied, and the waves meet once per slice.
-// Wave w takes weight rows [64 w, 64 w + 64) of the item's 512.
+// columns; of the activations two slices of up to 64 rows are in LDS, the next
+// one on its way while one is multiplied, and the waves meet once per slice.
+// Wave w takes weight rows [64 w, 64 w + 64) of the item's 512, which keeps
+// the reads of activations at half of what LDS can do beside the products, and
+// multiplies with as many 16-row tiles as hold rows (TM).  Against the ring,
+// which multiplies 64 rows always and meets every 128 columns (MI355X, 256
+// experts, d 4096, f 2048, gate/up): 24 rows an expert 670 -> 510 us, 48 rows
+// 735 -> 605, 64 rows 720 -> 690.  At 48 rows the loads alone take 460 us and
+// the products alone 590.
 //
 // Row r of a slice takes 1 KB of LDS, one load of a wave; its 16-byte chunk
 // p lies at p ^ (r % 8), so that eight lanes reading one chunk of consecutive
@@ -818,13 +835,20 @@ __device__ __forceinline__ void m4_stream(const Mx4Args &a, const Tile &t, int n
 // The tile list, one thread per expert: its full tiles of `cap` rows, then one
 // remainder tile of the smallest capacity of 16, 64, 128, 192 and 256 rows
 // that holds it (Tile::ablk in 32 rows, 1 for 16); all tiles of a class
-// together, tallest class first, experts in order.  (A class of 32 rows saved
-// nothing: up to 64 rows the weight stream is the bound.)
+// together, tallest class first, experts in order.  Inside a class a tile
+// pays for its rows in steps of 16 (m4_stream) or 32 (m4_item).
 //
 // cap is 256 rows, which reads an expert's weights least often, unless the
 // tiles then make fewer items than there are workgroups: 128 or 64 rows give
 // more of them, each with less to multiply (777 tokens, three routes each
 // over 24 experts, d 1152, f 640: gate/up 32.5 -> 18.7 us, down 23.9 -> 13.4 us).
+// Tiles of up to 64 rows come in items of twice the weight rows, and those of
+// 17 to 64 through m4_stream, where single items would take the workgroups
+// more than one round (the same layer with E experts of 48 rows, d 4096,
+// f 2048, gate/up: 16 experts, one round, 46 us single and 58 double; 24
+// experts 93 and 66; 32 experts 99 and 75; 64 experts 180 and 155.  Nine rows:
+// 8 experts 30 us single and 44 double, 16 experts 33 and 48, 24 experts 53
+// either way).
 constexpr int kM4ScheduleThreads = 256;  // the most experts
 __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     const int32_t *__restrict__ offsets, int E, int blocks, int grid, M4Schedule *__restrict__ sch,
@@ -850,7 +874,7 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += waves[0][w];
     __syncthreads();
-    many = cap == kTileRows && (long long)v * blocks >= 2 * grid;
+    many = cap == kTileRows && (long long)v * blocks > grid;
     if ((long long)v * blocks >= grid) break;
   }
   const int full = n / cap, rem = n % cap;
@@ -898,6 +922,7 @@ __global__ __launch_bounds__(kM4ScheduleThreads) void mx4_schedule_kernel(
     sch->n_tiles = total;
     sch->n_small = last;
     sch->n_stream = many ? before : 0;
+    sch->many = many;
   }
 }
 
@@ -1006,11 +1031,11 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
   constexpr int kHalf = GATEUP ? 2 : 1;  // gate and up rows of one feature
   constexpr int FB = kM4WRows / kHalf;  // features per item of the ring
   if (threadIdx.x == 0) {
-    const int streamed = m4_stream_takes(a.K) ? a.n_small[1] : 0;
+    const int streamed = m4_stream_takes(a.K) ? a.sch->n_stream : 0;
     // and of tiles of few rows
-    const int FS = m4_direct_fits(a.K) || streamed ? 2 * FB : FB;
-    state[1] = a.n_small[0] + streamed;
-    state[0] = *a.ntiles - state[1];
+    const int FS = a.sch->many && (m4_direct_fits(a.K) || streamed) ? 2 * FB : FB;
+    state[1] = a.sch->n_small + streamed;
+    state[0] = a.sch->n_tiles - state[1];
     state[2] = (a.N + FB - 1) / FB;  // items per tile
     state[3] = (a.N + FS - 1) / FS;
     state[4] = (int)blockIdx.x % kM4Queues;
@@ -1040,10 +1065,10 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
         state[4] = queues.q;
       }
       begin = false;
-      const bool small = ti >= queues.nbig && state[6] != FB;  // an item of twice the features
+      const bool wide = ti >= queues.nbig && state[6] != FB;  // an item of twice the features
       next_item[0] = some ? ti : -1;
-      next_item[1] = some ? part * (small ? 2 * FB : FB) : 0;
-      next_item[2] = small;
+      next_item[1] = some ? part * (wide ? 2 * FB : FB) : 0;
+      next_item[2] = wide;
     }
     __syncthreads();
     // read before the item's first barrier (its loads overwrite it); the
@@ -1055,7 +1080,7 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
     Mx4Args ai = a;
     ai.K = __builtin_amdgcn_readfirstlane(state[7]);
     ai.N = __builtin_amdgcn_readfirstlane(state[8]);
-    const bool small = __builtin_amdgcn_readfirstlane(next_item[2]);
+    const bool wide = __builtin_amdgcn_readfirstlane(next_item[2]);
     const Tile t = a.tiles[ti];
     if (threadIdx.x == 0 && !state[5])
       drawn = M4Queues(heads(), state).draw();  // for the item after this one
@@ -1064,18 +1089,21 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
       case 6: m4_item<GATEUP, 192>(ai, t, n0, ring, ring_lds); break;
       case 4: m4_item<GATEUP, 128>(ai, t, n0, ring, ring_lds); break;
       default:
-        if (!small)
-          m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds);
-        else if (t.nrows > kM4DirectRows || !m4_direct_fits(ai.K))
+        if (t.nrows <= kM4DirectRows && m4_direct_fits(ai.K)) {
+          const int n1 = min(n0 + (wide ? 2 * FB : FB), ai.N);
+          if (ai.K % 1024 == 0)
+            m4_direct<GATEUP, true>(ai, t, n0, n1, ring);
+          else
+            m4_direct<GATEUP, false>(ai, t, n0, n1, ring);
+        } else if (wide) {
           switch ((t.nrows + 15) / 16) {
             case 4: m4_stream<GATEUP, 4>(ai, t, n0, ring, ring_lds); break;
             case 3: m4_stream<GATEUP, 3>(ai, t, n0, ring, ring_lds); break;
             default: m4_stream<GATEUP, 2>(ai, t, n0, ring, ring_lds); break;
           }
-        else if (ai.K % 1024 == 0)
-          m4_direct<GATEUP, true>(ai, t, n0, ring);
-        else
-          m4_direct<GATEUP, false>(ai, t, n0, ring);
+        } else {
+          m4_item<GATEUP, 64>(ai, t, n0, ring, ring_lds);
+        }
         break;
     }
     // the ring (and the item in it) is rewritten only after every wave has
@@ -1093,8 +1121,7 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
   Mx4Args g{};
   g.k = L.k;
   g.tiles = L.tiles;
-  g.ntiles = &sch->n_tiles;
-  g.n_small = &sch->n_small;
+  g.sch = sch;
   if (stages & kStageGateUp) {
     g.act = L.x;
     g.sorted_routes = L.sorted_routes;
