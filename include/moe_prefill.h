@@ -369,9 +369,11 @@ int moe_decode_ffn(const moe_ffn_desc *desc /* host */, const void *x, const int
  *   y = bf16_rne(n)
  *   s[i] = max_c |n[i,c]| / 448 (1 for an all-zero row),  q = e4m3_rne_saturate(n / s)
  *
- * Each output is rounded once, from fp32: q is formed from n, not from y.
- * The mean is taken in fp64.  A row that holds a NaN or an infinity gets
- * NaN where the formulas give it; other rows are unaffected.
+ * Each output is rounded once: residual_out, y and s from fp32, and q (which is
+ * not formed from y) from the quotient v * weight * 448 / max_c |v * weight| in
+ * fp64, so that a code is the nearest one.  The mean is taken in fp64.  A row
+ * that holds a NaN or an infinity gets NaN where the formulas give it; other
+ * rows are unaffected.
  *
  * x            [rows, d], x_dtype (moe_dtype)
  * residual     [rows, d], residual_dtype, or NULL

@@ -5,17 +5,27 @@
 //   v = residual + x,  r = 1 / sqrt(mean(v^2) + eps),  n = (v * weight) * r
 //   residual_out = v,  y = bf16(n),  s = max|n| / 448,  q = e4m3(n / s)
 //
-// A row is read once and stays in registers as fp32; each output is rounded
-// once from it (n is not rounded to bf16 ahead of the quantisation, and the
-// norm takes v as it is before residual_out is rounded).  The squares are
-// summed in fp64: rows whose squares overflow fp32 keep their norm, and the
-// fp64 work (one conversion and one FMA per element) hides behind the memory
-// traffic.  max|n| needs no second pass: rounding is monotone, so
-// max|n| = fl(max|v * weight| * r), and both reductions share one exchange.
+// A row is read once and stays in registers; each output is rounded once (n
+// is not rounded to bf16 ahead of the quantisation, and the norm takes v as it
+// is before residual_out is rounded).  The squares are summed in fp64: rows
+// whose squares overflow fp32 keep their norm.
+//
+// Codes.  n / s = v weight 448 / max|v weight|: the root cancels, and the
+// codes are those of that quotient in fp64.  Nearly every element takes its
+// code from fp32: y = n (1 / s) lies within 8 x 2^-24 of the quotient (v, two
+// products, s with its product and division, its reciprocal, and the product
+// with it: one rounding each), so where no midpoint between two codes is near,
+// the code is the same; the few others are formed again from the inputs in
+// fp64.  Codes taken from fp32 alone were off by one step in about one element
+// of a million.
 //
 // Bound by memory traffic (9 bytes per element with bf16 rows, a bf16
-// residual and both outputs) from a few hundred rows on, by the latency of one row's load,
-// reduction and store below that.
+// residual and both outputs) from a few hundred rows on: 8192 rows of 4096 take
+// 61 us on MI355X, 4.95 TB/s, where a large copy reaches 4.8 (59 us with codes
+// from fp32).  Below that by the latency of one row's load, reduction and
+// store: one row of 4096 4 us, 401 rows 9.5 us.  A workgroup to a row keeps that
+// latency short; rows of up to 512 columns leave three of its waves idle, so a
+// wave takes one there.
 #include "e4m3.h"
 #include "kernels.h"
 
@@ -70,10 +80,29 @@ __device__ __forceinline__ double nm_wave_sum(double v) {
   return v;
 }
 
-__device__ __forceinline__ float nm_wave_max(float v) {
+__device__ __forceinline__ double nm_wave_max(double v) {
 #pragma unroll
-  for (int m = kWave / 2; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+  for (int m = kWave / 2; m > 0; m >>= 1) v = fmax(v, __shfl_xor(v, m));
   return v;
+}
+
+// Whether a value within 8 x 2^-24 of y may have another code than y: it is
+// near a midpoint between codes, which are the patterns with low bits 0x80000
+// in the normal range and odd multiples of 2^-10 below it, or no number.
+__device__ __forceinline__ bool nm_near_midpoint(float y) {
+  const uint32_t a = __float_as_uint(y) & 0x7fffffffu;
+  const float t = __uint_as_float(a) * 512.0f;
+  return a >= 0x3c800000u ? a > 0x7f800000u || ((a & 0xfffffu) - 0x7fff0u) < 32u
+                          : fabsf(t - floorf(t) - 0.5f) < 1e-5f;
+}
+
+// E4M3 code of a fp64 value, rounded once: fp32 rounded to odd on the way.
+__device__ __forceinline__ uint32_t nm_code(double t) {
+  uint32_t b = __float_as_uint((float)t);
+  const double f = fabs((double)__uint_as_float(b));
+  if (f > fabs(t)) --b;
+  if (f != fabs(t)) b |= 1u;
+  return f32_to_e4m3(__uint_as_float(b));
 }
 
 // 1 / sqrt(m): in fp32 where m is well inside its range, in fp64 elsewhere.
@@ -89,7 +118,7 @@ template <int NC, bool WIDE, bool XF, int RES>
 __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
   constexpr int TPR = WIDE ? kNmThreads : kWave;  // threads per row
   __shared__ double part_sum[kNmWaves];
-  __shared__ float part_max[kNmWaves];
+  __shared__ double part_max[kNmWaves];
   const int wave = threadIdx.x / kWave;
   const int tid = WIDE ? (int)threadIdx.x : lane_id();
   const int row = WIDE ? (int)blockIdx.x : (int)blockIdx.x * kNmWaves + wave;
@@ -106,9 +135,12 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
       if (RES) rr[c].load(a.residual, base + i);
     }
   }
-  float v[NC][8], n[NC][8];
-  double sum = 0.0;
-  float top = 0.0f;
+  // element e of chunk c of x + residual, unrounded
+  const auto sum_of = [&](int c, int e) {
+    return RES ? (double)xr[c].at(e) + (double)rr[c].at(e) : (double)xr[c].at(e);
+  };
+  float n[NC][8];
+  double sum = 0.0, top = 0.0;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int i = (c * TPR + tid) * 8;
@@ -125,16 +157,17 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = wr.at(e);
     }
+    float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v[c][e] = xr[c].at(e);
-      if (RES) v[c][e] += rr[c].at(e);
-      const double t = (double)v[c][e];
+      v[e] = xr[c].at(e);
+      if (RES) v[e] += rr[c].at(e);
+      const double t = (double)v[e];
       sum = __builtin_fma(t, t, sum);
-      n[c][e] = v[c][e] * w[e];
-      top = fmaxf(top, fabsf(n[c][e]));
+      n[c][e] = v[e] * w[e];
+      if (a.q) top = fmax(top, fabs(sum_of(c, e) * (double)w[e]));
     }
-    if (a.residual_out) nm_store8(a.residual_out, base + i, RES == 2 || (RES == 0 && XF), v[c]);
+    if (a.residual_out) nm_store8(a.residual_out, base + i, RES == 2 || (RES == 0 && XF), v);
   }
   sum = nm_wave_sum(sum);
   top = nm_wave_max(top);
@@ -149,15 +182,14 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int w = 1; w < kNmWaves; ++w) {
       sum += part_sum[w];
-      top = fmaxf(top, part_max[w]);
+      top = fmax(top, part_max[w]);
     }
   }
   const float r = nm_rsqrt(sum / a.d + (double)a.eps);
-  top *= r;
-  const bool zero = top == 0.0f;
-  const float sc = q_scale(top);
+  const float sc = q_scale((float)top * r);
   bool exact;
   const float rcp = quant_rcp(sc, &exact);
+  exact = exact || top < 1e-28;  // products close to the end of fp32
   if (a.s && tid == 0) a.s[row] = sc;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -166,14 +198,31 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) n[c][e] *= r;
     if (a.y) nm_store8(a.y, base + i, false, n[c]);
-    if (a.q) {
-      const float lo[4] = {n[c][0], n[c][1], n[c][2], n[c][3]};
-      const float hi[4] = {n[c][4], n[c][5], n[c][6], n[c][7]};
-      uint2 o;
-      o.x = quant_e4m3_x4(lo, sc, rcp, exact, zero);
-      o.y = quant_e4m3_x4(hi, sc, rcp, exact, zero);
-      *reinterpret_cast<uint2 *>(a.q + base + i) = o;
+    if (!a.q) continue;
+    uint2 o = {};
+    if ((float)top * r != 0.0f) {
+      bool any = exact;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[c][e] *= rcp;
+        any = any || nm_near_midpoint(n[c][e]);
+      }
+      o.x = cvt_e4m3_x2<true>(n[c][2], n[c][3], cvt_e4m3_x2<false>(n[c][0], n[c][1], 0u));
+      o.y = cvt_e4m3_x2<true>(n[c][6], n[c][7], cvt_e4m3_x2<false>(n[c][4], n[c][5], 0u));
+      if (any) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (!exact && !nm_near_midpoint(n[c][e])) continue;
+          const float w = a.w_f32 ? static_cast<const float *>(a.weight)[i + e]
+                                  : bf16_bits_to_f32(static_cast<const uint16_t *>(a.weight)[i + e]);
+          const double t = sum_of(c, e) * (double)w * 448.0 / top;
+          const uint32_t code = nm_code(sc == sc ? t : (double)sc);
+          uint32_t &part = e < 4 ? o.x : o.y;
+          part = (part & ~(0xffu << (8 * (e & 3)))) | (code << (8 * (e & 3)));
+        }
+      }
     }
+    *reinterpret_cast<uint2 *>(a.q + base + i) = o;
   }
 }
 

@@ -6,7 +6,8 @@ conversion counts half, the root and the quotient one each: 2.5 x 2^-24), so
 |n - n64| <= 6 x 2^-24 |n64|; bf16 adds half a step, at most 2^-8 of the
 value.  residual_out is one fp32 addition rounded once more, and compared bit
 for bit.  A scale adds one division.  A code is the nearest to n / s: within
-half a step of it, and 2^-18 of the value for n's own error."""
+half a step of it, and 2^-18 of the value for n's own error; and exactly the
+nearest to the quotient that 64 bits give (test_codes_are_the_nearest)."""
 import numpy as np
 import pytest
 
@@ -86,6 +87,29 @@ def test_matches_the_formulas(rows, d, xt, rt, wt):
     _, _, q3, s3 = rep.add_rmsnorm(dx, dw, eps=1e-5, residual=dr, want_bf16=False, want_fp8=True)
     assert torch.equal(y2.view(torch.int16), got[0].view(torch.int16))
     assert torch.equal(q3, got[2]) and torch.equal(s3, got[3])
+
+
+@pytest.mark.parametrize("rows,d,xt,rt,wt", [
+    (1500, 1416, "bf16", "f32", "bf16"), (401, 4096, "bf16", "bf16", "bf16"),
+    (300, 8200, "f32", "f32", "f32"), (2000, 384, "f32", None, "bf16"),
+])
+def test_codes_are_the_nearest(rows, d, xt, rt, wt):
+    """Every code is that of the quotient in 64 bits: v weight is exact there
+    but for the residual's addition, and so is its product with 448."""
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    types = {"bf16": torch.bfloat16, "f32": torch.float32, None: None}
+    x, r, w = _inputs(rows, d, types[xt], types[rt], types[wt], seed=rows)
+    if r is not None:
+        r[:, :: d // 4] *= 50  # the rest lies in the low codes, subnormal ones among them
+    dev = torch_dev()
+    _, _, q, _ = rep.add_rmsnorm(x.to(dev), w.to(dev), want_fp8=True,
+                                 residual=None if r is None else r.to(dev))
+    p = _ref(x, r, w, 1e-6)[0] * w.double().numpy()
+    t = p * 448 / np.abs(p).max(-1, keepdims=True)
+    assert np.array_equal(q.cpu().numpy(), nx.e4m3_encode(t))
 
 
 @pytest.mark.parametrize("d", [384, 4096])
