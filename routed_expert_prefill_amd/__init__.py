@@ -46,6 +46,27 @@ def _torch():
     return _torch_module
 
 
+_native_module = False
+
+
+def _native():
+    """The extension module of csrc/binding.cpp, bound to the loaded library,
+    or None where it is not built: the calls then go the way of the others."""
+    global _native_module
+    if _native_module is False:
+        lib = _lib.load()
+        _torch()  # whose libraries the module needs loaded
+        try:
+            from . import _binding
+        except ImportError:
+            _binding = None
+        else:
+            _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                            for f in (lib.moe_add_rmsnorm, lib.moe_decode_ffn)))
+        _native_module = _binding
+    return _native_module
+
+
 def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -431,6 +452,14 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, 
     residual it is written only if given (then v is x).  No rows: nothing is
     launched."""
     torch = _torch()
+    native = _native()
+    if native is not None and getattr(x, "is_cuda", False):
+        dev = torch._C._cuda_getDevice()
+        done = native.add_rmsnorm(x, weight, eps, residual, residual_out, y, q, s, want_bf16,
+                                  want_fp8, dev, torch._C._cuda_getCurrentRawStream(dev))
+        if done is not None:
+            return done
+    # refusals, no rows, and without the module every call
     lib = _lib.load()
     dev = _on_current(x, "x")
     if x.dim() != 2:
@@ -480,6 +509,15 @@ def decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_
     (torch.float32 by default).  The other arguments are those of route_build,
     grouped_ffn and combine_shared."""
     torch = _torch()
+    native = _native()
+    if (native is not None and out is not None and workspace is not None
+            and getattr(x, "is_cuda", False)):
+        dev = torch._C._cuda_getDevice()
+        if native.decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_up,
+                             s_down, shared, out, workspace, dev,
+                             torch._C._cuda_getCurrentRawStream(dev)):
+            return out
+    # outputs to be made, refusals, and without the module every call
     lib = _lib.load()
     dev = _on_current(x, "x")
     if x.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 3:

@@ -66,6 +66,28 @@ def build(verbose: bool = False, defines=(), out: str = LIB, build_dir: str = BU
     tmp = out + ".tmp"
     _run([cc, "-shared", "--offload-arch=gfx950", "-o", tmp, *objs])
     os.replace(tmp, out)
+    if out == LIB:
+        build_binding()
+    return out
+
+
+def build_binding() -> str:
+    """The extension module for the shortest Python calls (csrc/binding.cpp),
+    host code against the installed torch; returns its path."""
+    import sysconfig
+
+    import torch
+
+    top = os.path.dirname(os.path.abspath(torch.__file__))
+    out = os.path.join(PKG, "_binding.so")
+    cc = shutil.which("g++") or shutil.which("c++") or hipcc()
+    _run([cc, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-cast-function-type",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I" + os.path.join(ROOT, "include"), "-isystem", os.path.join(top, "include"),
+          "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"),
+          "-o", out + ".tmp", "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu",
+          "-lc10"])
+    os.replace(out + ".tmp", out)
     return out
 
 

@@ -9,6 +9,7 @@ from gpu_util import bf16_dev, np_dev
 from mxfp4_util import bf16_source, mx_weights
 from test_gpu_ffn import _x
 from test_gpu_mxfp4 import _close, _dev
+from test_gpu_norm import _call_both_ways
 
 pytestmark = pytest.mark.gpu
 
@@ -183,6 +184,41 @@ def test_two_streams_and_the_workspaces_end():
     for _, n, ws, out, want in runs:
         assert torch.equal(out[:5].view(torch.int32), want.view(torch.int32))
         assert (out[5:] == 7).all() and (ws[n:] == 0xA5).all()
+
+
+def test_with_and_without_the_extension(monkeypatch):
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    p = _problem(5, 4, 12, 640, 384, seed=21, mask_p=0.2)
+    ids, w, mask, x, W = p
+    shared = torch.randn(5, 640, device="cuda")
+    args = (bf16_dev(x), np_dev(ids), np_dev(w), np_dev(mask), *_dev(W))
+    for mask_too in (True, False):
+        for dtype in (torch.float32, torch.bfloat16):
+            layer = rep.MoEPrefill(5, 4, 12, 640, 384, weights="mxfp4", out_dtype=dtype)
+            call = args if mask_too else (*args[:3], None, *args[4:])
+
+            def run():
+                layer.out.fill_(float("nan"))
+                return layer(*call, shared=shared).clone()
+
+            a, b, used = _call_both_ways(monkeypatch, run)
+            assert used is True and torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # what the module leaves to the Python code
+    layer = rep.MoEPrefill(5, 4, 12, 640, 384, weights="mxfp4")
+    for i, bad in ((0, args[0][:3]), (1, args[1].long()), (2, args[2].cpu()), (3, args[3].bool()),
+                   (4, args[4].transpose(0, 1)), (6, args[4]), (9, args[9].float())):
+        call = (*args[:i], bad, *args[i + 1:])
+
+        def run():
+            with pytest.raises((TypeError, ValueError)) as e:
+                layer(*call)
+            return str(e.value)
+
+        a, b, used = _call_both_ways(monkeypatch, run)
+        assert a == b and used is None
 
 
 def test_refusals():

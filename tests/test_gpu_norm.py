@@ -223,3 +223,80 @@ def test_own_stream_and_graph_replays():
         for a, b in zip(cap, eager):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
         (x.float() * 2).sum().item()
+
+
+def _call_both_ways(monkeypatch, call):
+    """call() through the extension module and without it."""
+    import routed_expert_prefill_amd as rep
+
+    native = rep._native()
+    assert native is not None
+    used = []
+
+    class Spy:
+        def __getattr__(self, name):
+            def run(*args):
+                used.append(getattr(native, name)(*args))
+                return used[-1]
+            return run
+
+    monkeypatch.setattr(rep, "_native", lambda: Spy())
+    first = call()
+    monkeypatch.setattr(rep, "_native", lambda: None)
+    second = call()
+    monkeypatch.undo()
+    return first, second, used[0]
+
+
+@pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f32", "bf16"), ("f32", None)])
+@pytest.mark.parametrize("want", [dict(), dict(want_fp8=True), dict(want_fp8=True, want_bf16=False),
+                                  "outputs"])
+def test_with_and_without_the_extension(monkeypatch, xt, rt, want):
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    types = {"bf16": torch.bfloat16, "f32": torch.float32, None: None}
+    x, r, w = (None if t is None else t.to(torch_dev())
+               for t in _inputs(33, 640, types[xt], types[rt], torch.bfloat16, seed=2))
+
+    def call():
+        kw = want
+        if want == "outputs":
+            kw = dict(y=torch.empty_like(x, dtype=torch.bfloat16), s=torch.empty(33, device=x.device),
+                      residual_out=torch.empty_like(x if r is None else r))
+        got = rep.add_rmsnorm(x, w, residual=r, **kw)
+        if want == "outputs":
+            assert got[0] is kw["y"] and got[3] is kw["s"] and got[1] is kw["residual_out"]
+        return got
+
+    a, b, used = _call_both_ways(monkeypatch, call)
+    assert used is not None
+    for p, q in zip(a, b):
+        assert (p is None) == (q is None)
+        if p is not None:
+            assert p.dtype == q.dtype and torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
+def test_the_extension_leaves_refusals_to_python(monkeypatch):
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    x, r, w = (t.to(torch_dev()) for t in _inputs(4, 64, torch.bfloat16, torch.float32,
+                                                  torch.bfloat16, seed=3))
+    for kw in (dict(x=x.t()), dict(x=x[:, ::2]), dict(weight=w[:8]), dict(weight=w.double()),
+               dict(residual=r[:2]), dict(residual=r.cpu()), dict(y=torch.empty_like(r)),
+               dict(q=torch.empty_like(x)), dict(s=torch.empty(3, device=x.device)),
+               dict(residual_out=torch.empty_like(x)), dict(eps=-1.0), dict(want_bf16=False)):
+        args = dict(x=x, weight=w, residual=r, **{k: v for k, v in kw.items()
+                                                  if k not in ("x", "weight", "residual")})
+        args.update({k: v for k, v in kw.items() if k in ("x", "weight", "residual")})
+
+        def call():
+            with pytest.raises((TypeError, ValueError, RuntimeError)) as e:
+                rep.add_rmsnorm(**args)
+            return str(e.value)
+
+        a, b, used = _call_both_ways(monkeypatch, call)
+        assert a == b and used is None
