@@ -59,18 +59,21 @@ struct NmRaw {
   }
 };
 
+// Stores past the caches (nontemporal): nothing here reads a line again, and
+// dirty lines left in L2 are what the kernel's end waits for (8192 rows of
+// 4096: 67 -> 59.5 us, 1999 rows of 1416: 12 -> 10.4).  Loads gained nothing.
 __device__ __forceinline__ void nm_store8(void *base, size_t i, bool f32, const float (&v)[8]) {
   if (f32) {
     f32x4 *p = reinterpret_cast<f32x4 *>(static_cast<float *>(base) + i);
-    p[0] = f32x4{v[0], v[1], v[2], v[3]};
-    p[1] = f32x4{v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, p);
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, p + 1);
   } else {
     i32x4 o;
 #pragma unroll
     for (int w = 0; w < 4; ++w)
       o[w] = (int)((uint32_t)f32_to_bf16_bits(v[2 * w]) |
                    ((uint32_t)f32_to_bf16_bits(v[2 * w + 1]) << 16));
-    *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(base) + i) = o;
+    __builtin_nontemporal_store(o, reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(base) + i));
   }
 }
 
@@ -222,7 +225,7 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
         }
       }
     }
-    *reinterpret_cast<uint2 *>(a.q + base + i) = o;
+    __builtin_nontemporal_store((uint64_t)o.x | (uint64_t)o.y << 32, reinterpret_cast<uint64_t *>(a.q + base + i));
   }
 }
 
