@@ -18,13 +18,15 @@
 // lane group c = l / 16 of a step holds group c, and MFMA j multiplies
 // columns 8 j .. 8 j + 7 of all four groups.
 //
-// MI355X, d 4096, f 2048, gate/up and down: one token of top-6 12.6 + 8.8 us
-// (53.5 + 26.7 MB: 4.2 and 3.0 TB/s), four tokens, 21 experts, 40.5 + 21.4 us
+// MI355X, d 4096, f 2048, gate/up and down: one token of top-6 11.1 + 9.1 us
+// (53.5 + 26.7 MB: 4.8 and 2.9 TB/s), four tokens, 21 experts, 40.5 + 21.4 us
 // (4.6 and 4.4 TB/s).  At one token about 4 us of each launch are its start and
 // the latency of its first loads.  Gate/up splits a reduction over four waves,
 // which makes the workgroups of one token's six experts (768) fill the chip;
 // down gives each wave whole experts, so that the routes' sums meet in LDS and
-// no combine follows.
+// no combine follows.  h is rounded to bf16 between them, the matrix unit's
+// operand, as the grouped path rounds it, so that prompts and single tokens
+// agree.
 #include "kernels.h"
 #include "mx4.h"
 

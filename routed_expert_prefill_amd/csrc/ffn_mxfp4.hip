@@ -4,7 +4,9 @@
 //   gate/up: h[i, n] = bf16(silu(g) u),  g = sum_c Wg[e, n, c] x[t, c],  u likewise with Wu
 //   down:    y[i, n] = sum_c Wd[e, n, c] h[i, c]
 //
-// for sorted row i of expert e and token t.  Weights stay codes until the
+// for sorted row i of expert e and token t; h is rounded to bf16 because it is
+// the second product's operand in the matrix unit, as in the bf16 kernels, and
+// nothing else is rounded to fewer than 32 bits.  Weights stay codes until the
 // products: a lane reads 16 bytes of a weight row, 32 codes, exactly one scale
 // group, and converts them in registers, so no pass over expanded weights
 // exists and a weight costs 4.25 bits of memory traffic.  The order of a

@@ -21,11 +21,10 @@
 //
 // Bound by memory traffic (9 bytes per element with bf16 rows, a bf16
 // residual and both outputs) from a few hundred rows on: 8192 rows of 4096 take
-// 61 us on MI355X, 4.95 TB/s, where a large copy reaches 4.8 (59 us with codes
-// from fp32).  Below that by the latency of one row's load, reduction and
-// store: one row of 4096 4 us, 401 rows 9.5 us.  A workgroup to a row keeps that
-// latency short; rows of up to 512 columns leave three of its waves idle, so a
-// wave takes one there.
+// 58.5 us on MI355X, 5.2 TB/s, where a large copy reaches 4.8.  Below that by
+// the latency of one row's load, reduction and store: one row of 4096 4 us, 401
+// rows 9 us.  A workgroup to a row keeps that latency short; rows of up to 512
+// columns would leave three of its waves idle, so a wave takes one there.
 #include "e4m3.h"
 #include "kernels.h"
 
