@@ -978,10 +978,10 @@ struct M4Queues {
     return item(back ? n - 1 - rank : rank, tile, part);
   }
   // Whether the fixed first items are all there are: nothing is drawn then.
+  // Queue 0 has the most items (no fewer tall tiles and no fewer tiles than
+  // any other, and a tall tile has no fewer items), queue 7 the fewest owners.
   __device__ __forceinline__ bool fixed() const {
-    for (int p = 0; p < kM4Queues; ++p)
-      if (rest(p, 0) > 0) return false;
-    return true;
+    return items(0) <= G / kM4Queues;
   }
   __device__ __forceinline__ unsigned long long draw() const {
     return atomicAdd(&h->head[q], back ? 1ull << 32 : 1ull);
