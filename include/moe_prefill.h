@@ -185,6 +185,8 @@ int moe_route_build_noalloc(const int32_t *topk_ids, const uint8_t *route_mask, 
  *
  * MXFP4 mode (weights MXFP4, activations BF16): the formulas above with the
  * weights' exact values, which are bf16 numbers; no other rounding is added.
+ * The order of a row's sums goes with the row counts of the experts (the
+ * tiles); equal offsets give equal bits.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
  */
 size_t moe_grouped_ffn_workspace(const moe_ffn_desc *desc /* host */);

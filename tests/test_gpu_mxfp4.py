@@ -297,6 +297,38 @@ def test_two_streams_and_the_workspaces_end():
         assert (layer.ffn_ws[n:] == 0xA5).all()
 
 
+@pytest.mark.parametrize("decode", [False, True])
+def test_two_graphs_share_a_layer(decode):
+    """Two captures of one layer, one workspace and one output, on other inputs
+    each, replayed in turn between eager calls."""
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    counts = ([3, 0, 9, 8], [20, 0, 0, 0]) if decode else ([70, 0, 300, 9], [9, 200, 0, 170])
+    problems = [_problem(c, 2, 512, 256, seed=30 + i, masked=379 - sum(c) if not decode else 0)
+                for i, c in enumerate(counts)]
+    layer = rep.MoEPrefill(*problems[0][1].shape, 4, 512, 256, weights="mxfp4")
+    assert layer.decode == decode
+    runs = []
+    for E, ids, w, mask, x, W in problems:
+        assert ids.shape == problems[0][1].shape
+        args = (bf16_dev(x), np_dev(ids), np_dev(w), np_dev(mask), *_dev(W))
+        eager = layer(*args).clone()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer(*args)
+        runs.append((g, args, eager))
+    for _ in range(3):
+        for g, args, eager in runs:
+            layer.out.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(layer.out.view(torch.int32), eager.view(torch.int32))
+            assert torch.equal(layer(*args).view(torch.int32), eager.view(torch.int32))
+
+
 def test_refusals():
     import torch
 
