@@ -173,7 +173,8 @@ int moe_route_build_noalloc(const int32_t *topk_ids, const uint8_t *route_mask, 
  *               block scales, element [n,c] of expert e is multiplied by
  *               s[e, n/128, c/128].  NULL for bf16 weights.
  *               For MOE_W_MXFP4: E8M0 bytes, uint8 [E, f, d/32] and [E, d, f/32];
- *               element [n,c] is multiplied by 2^(s[e, n, c/32] - 127) (255: NaN).
+ *               element [n,c] is multiplied by 2^(s[e, n, c/32] - 127) (255: NaN;
+ *               products of 2^128 and more are infinite).
  * y             fp32 [T*k, d]
  * workspace     at least moe_grouped_ffn_workspace(desc) bytes; holds the
  *               tile schedule, h and (fp8) the quantised activations.
@@ -330,10 +331,11 @@ int moe_quant_rows_fp8(const void *x, int rows, int cols, uint8_t *q, float *s,
  * The routed experts for decoding: matrix-vector products with MXFP4
  * weights straight from the router's ids, in two launches.  The result is
  * that of moe_route_build, moe_grouped_ffn and moe_combine_shared on the
- * same inputs (with the row limit), sums of products in another order:
+ * same inputs (with the row limit), but for the order of sums and for h, which
+ * is not rounded to bf16 but kept to 16 significant bits:
  *
  *   routed[t] = sum over j ascending, route (t, j) read, of topk_w[t,j] *
- *               Wd[e] . bf16_rne(silu(Wg[e] . x[t]) * (Wu[e] . x[t])),  e = topk_ids[t,j]
+ *               Wd[e] . (silu(Wg[e] . x[t]) * (Wu[e] . x[t])),  e = topk_ids[t,j]
  *   out[t] = routed[t] + shared[t],  out_bf16[t] = bf16_rne(out[t])
  *
  * A route is read when route_mask[r] != 0 (or route_mask is NULL) and its id

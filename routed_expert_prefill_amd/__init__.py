@@ -564,16 +564,17 @@ class MoEPrefill:
     across calls (nothing is allocated per call after construction).
 
     weights: "bf16", "fp8" or "mxfp4" (default: by fp8).  out_dtype:
-    torch.float32 (default) or torch.bfloat16.  With MXFP4 weights and at most
-    DECODE_ROUTES routes a pass is decode_ffn (unless stage events are asked
-    for): self.rt and self.y are then not written."""
+    torch.float32 (default) or torch.bfloat16.  With MXFP4 weights and few
+    routes (DECODE_ROUTES) a pass is decode_ffn, unless stage events are asked
+    for or self.decode is set to False: self.rt and self.y are then not written."""
 
-    # At most this many routes go through decode_ffn, its own limit: over 256
-    # experts, d 4096, f 2048, 6 routes take 21 us (grouped: 70), 24 take 62
-    # (79) and 60 take 137 (171); 64 routes over 16 experts, d 1024, f 512, 18
-    # (34).  Only many routes of one expert are faster grouped, whose weights
-    # decode_ffn reads again for every four of them (64 routes of one expert,
-    # d 4096, f 2048: 109 us, grouped 67; 32 routes: 57 and 63).
+    # At most this many routes go through decode_ffn, its own limit, and from 33
+    # on no more than four for each expert there is.  Over 256 experts, d 4096,
+    # f 2048, 6 routes take 21 us (grouped: 48), 24 take 62 (76) and 60 take 144
+    # (172); over 16 experts, d 1024, f 512, 64 routes 20 (28).  Where experts
+    # have many routes decode_ffn reads their weights again for every two or
+    # four: 8 experts, d 4096, f 2048, 16 routes 27 us (47), 32 routes 46 (47),
+    # 64 routes 63 (48).
     DECODE_ROUTES = 64
 
     def __init__(self, T: int, k: int, E: int, d: int, f: int, fp8: bool = False, device="cuda",
@@ -597,6 +598,9 @@ class MoEPrefill:
                                  dtype=torch.uint8, device=dev)
         self.desc = ffn_desc(T, k, E, d, f, fp8, weights)
         self.ffn_ws = _ffn_ws(self.desc, dev, None)
+        more = lib.moe_decode_ffn_workspace(ctypes.byref(self.desc))  # 0: not its kind of layer
+        if more > self.ffn_ws.numel():
+            self.ffn_ws = torch.empty(more, dtype=torch.uint8, device=dev)
         self.y = torch.empty(R, d, dtype=torch.float32, device=dev)
         self.out = torch.empty(T, d, dtype=out_dtype or torch.float32, device=dev)
         # offsets[E]: rows of y the FFN writes.  The combine reads no route at
@@ -604,7 +608,7 @@ class MoEPrefill:
         # the route build sends to the trailing bin -- add exact zeros, as
         # masked ones do.
         self.row_limit = self.rt.offsets[E:E + 1]
-        self.decode = self.weights == "mxfp4" and R <= self.DECODE_ROUTES
+        self.decode = self.weights == "mxfp4" and R <= min(self.DECODE_ROUTES, max(32, 4 * E))
 
     def __call__(self, x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate=None,
                  s_up=None, s_down=None, stage_events=None, shared=None):

@@ -441,7 +441,7 @@ int moe_add_rmsnorm(const void *x, int x_dtype, const void *residual, void *resi
 
 size_t moe_decode_ffn_workspace(const moe_ffn_desc *desc) {
   if (decode_desc_status(desc) != MOE_OK) return 0;
-  return align_up((size_t)desc->T * desc->k * desc->f * 2);
+  return align_up((size_t)desc->T * desc->k * desc->f * 4);
 }
 
 int moe_decode_ffn(const moe_ffn_desc *desc, const void *x, const int32_t *topk_ids,

@@ -18,15 +18,19 @@
 // lane group c = l / 16 of a step holds group c, and MFMA j multiplies
 // columns 8 j .. 8 j + 7 of all four groups.
 //
-// MI355X, d 4096, f 2048, gate/up and down: one token of top-6 11.1 + 9.1 us
-// (53.5 + 26.7 MB: 4.8 and 2.9 TB/s), four tokens, 21 experts, 40.5 + 21.4 us
-// (4.6 and 4.4 TB/s).  At one token about 4 us of each launch are its start and
+// MI355X, d 4096, f 2048, gate/up and down: one token of top-6 11.5 + 8.9 us
+// (53.5 + 26.7 MB: 4.7 and 3.0 TB/s), four tokens, 21 experts, 40.5 + 22.6 us
+// (4.6 and 4.1 TB/s).  At one token about 4 us of each launch are its start and
 // the latency of its first loads.  Gate/up splits a reduction over four waves,
 // which makes the workgroups of one token's six experts (768) fill the chip;
 // down gives each wave whole experts, so that the routes' sums meet in LDS and
-// no combine follows.  h is rounded to bf16 between them, the matrix unit's
-// operand, as the grouped path rounds it, so that prompts and single tokens
-// agree.
+// no combine follows.
+//
+// h goes from one to the other as two bf16 numbers, the value rounded and what
+// that took, rounded: 16 significant bits.  One rounding to bf16, as the grouped
+// path has it, is as large as the output's own, and a token's few sums do not
+// average it; the second part costs nothing here, where the matrix
+// instruction's 16 columns hold one or two routes.
 #include "kernels.h"
 #include "mx4.h"
 
@@ -146,8 +150,8 @@ __device__ __forceinline__ void dec_products_n(const uint8_t *const (&codes)[TW]
                                                const uint8_t *const (&scales)[TW],
                                                const uint16_t *x, const uint32_t (&rows)[kDecRows],
                                                int s0, int s1, uint8_t *lds, f32x4 (&acc)[TW]) {
-  // several rows' activations take the registers of some of the steps
-  constexpr int U = NR == 1 ? MU : 4;
+  // many rows' activations take the registers of some of the steps
+  constexpr int U = NR <= 2 ? MU : 4;
   int s = s0;
   for (; s + U <= s1; s += U) dec_steps<TW, MU, NR, U>(codes, scales, x, rows, s, lds, acc);
   if constexpr (U > 8) {
@@ -169,34 +173,33 @@ __device__ __forceinline__ void dec_products_n(const uint8_t *const (&codes)[TW]
   if (s < s1) dec_steps<TW, MU, NR, 1>(codes, scales, x, rows, s, lds, acc);
 }
 
-// The same for n = 1 .. kDecRows activation rows; rows past n repeat one.
+// The same for n = 1 .. kDecRows activation rows; rows past n repeat one.  ONE
+// is the n that single rows of an expert come with (gate/up: 1, down: 2).
 // A row's sums do not depend on n: the steps are taken in one order.
-template <int TW, int MU>
+template <int TW, int MU, int ONE>
 __device__ __forceinline__ void dec_products(const uint8_t *const (&codes)[TW],
                                              const uint8_t *const (&scales)[TW], const uint16_t *x,
                                              const uint32_t (&rows)[kDecRows], int n, int s0,
                                              int s1, uint8_t *lds, f32x4 (&acc)[TW]) {
-  if (n == 1)
-    dec_products_n<TW, MU, 1>(codes, scales, x, rows, s0, s1, lds, acc);
+  if (n == ONE)
+    dec_products_n<TW, MU, ONE>(codes, scales, x, rows, s0, s1, lds, acc);
   else
     dec_products_n<TW, MU, kDecRows>(codes, scales, x, rows, s0, s1, lds, acc);
 }
 
-// The next activation rows of an expert's routes `set`, which loses them:
-// route[m], and the rows' starts (elements) in [.., width] rows indexed by
-// route / per.  Past n they repeat the first.
-__device__ __forceinline__ int dec_next_rows(uint64_t &set, int per, int width,
-                                             int (&route)[kDecRows], uint32_t (&rows)[kDecRows]) {
+// The next N of an expert's routes `set`, which loses them; past the result's
+// count they repeat the first.
+template <int N>
+__device__ __forceinline__ int dec_next_routes(uint64_t &set, int (&route)[N]) {
   int n = 0;
 #pragma unroll
-  for (int m = 0; m < kDecRows; ++m) {
+  for (int m = 0; m < N; ++m) {
     route[m] = route[0];
     if (m == 0 || set) {
       route[m] = dec_first(set);
       set &= set - 1;
       ++n;
     }
-    rows[m] = (uint32_t)(route[m] / per) * (uint32_t)width;
   }
   return n;
 }
@@ -220,10 +223,12 @@ __global__ __launch_bounds__(kDecGuWaves *kWave) void decode_gate_up_kernel(Deco
   const uint8_t *scales[2] = {a.sg + row * (a.d / 32), a.su + row * (a.d / 32)};
   while (set) {
     int route[kDecRows];
+    const int n = dec_next_routes(set, route);
     uint32_t rows[kDecRows];
-    const int n = dec_next_rows(set, a.k, a.d, route, rows);
+#pragma unroll
+    for (int m = 0; m < kDecRows; ++m) rows[m] = (uint32_t)(route[m] / a.k) * (uint32_t)a.d;
     f32x4 acc[2] = {};
-    dec_products<2, kDecGuSteps>(codes, scales, a.x, rows, n, s0, s1, lds[wv], acc);
+    dec_products<2, kDecGuSteps, 1>(codes, scales, a.x, rows, n, s0, s1, lds[wv], acc);
     // the waves' parts of the sums, where their activation rows were
     f32x4 *part = reinterpret_cast<f32x4 *>(lds[wv]);
     part[lane] = acc[0];
@@ -240,12 +245,19 @@ __global__ __launch_bounds__(kDecGuWaves *kWave) void decode_gate_up_kernel(Deco
     const int m = lane & 15;
     if (m < n) {
       const int r = m == 0 ? route[0] : m == 1 ? route[1] : m == 2 ? route[2] : route[3];
-      a.h[(size_t)r * a.f + n0 + 4 * (lane >> 4) + wv] = f32_to_bf16_bits(swiglu(g, u));
+      const size_t at = (size_t)r * a.f + n0 + 4 * (lane >> 4) + wv;
+      const float v = swiglu(g, u);
+      const uint16_t top = f32_to_bf16_bits(v);
+      a.h[at] = top;
+      // what rounding took, rounded; nothing beside an infinity or a NaN
+      const bool finite = (top & 0x7f80u) != 0x7f80u;
+      a.h[(size_t)a.R * a.f + at] =
+          finite ? f32_to_bf16_bits(v - bf16_bits_to_f32(top)) : (uint16_t)0;
     }
     __syncthreads();  // the parts make room for the next rows
   }
 }
-static_assert(kDecGuWaves == 4 && kDecRows == 4, "the epilogue's mapping");
+static_assert(kDecGuWaves == 4 && kDecRows == 4, "the epilogues' mapping");
 
 // out[t, n0 .. n0 + 15] for every token t: the experts go round the waves,
 // and the routes' sums meet in LDS.
@@ -279,16 +291,20 @@ __global__ __launch_bounds__(kDecDnWaves *kWave) void decode_down_kernel(DecodeA
     const uint8_t *scales[1] = {a.sd + row * (a.f / 32)};
     uint64_t set = dec_readlane64(same, r0);
     while (set) {
-      int route[kDecRows];
+      // rows 2 m and 2 m + 1: the two parts of h of route m
+      int route[kDecRows / 2];
+      const int n = dec_next_routes(set, route);
       uint32_t rows[kDecRows];
-      const int n = dec_next_rows(set, 1, a.f, route, rows);
+#pragma unroll
+      for (int m = 0; m < kDecRows; ++m)
+        rows[m] = (uint32_t)(route[m / 2] + (m % 2) * a.R) * (uint32_t)a.f;
       f32x4 acc[1] = {};
-      dec_products<1, kDecDnSteps>(codes, scales, a.h, rows, n, 0, steps, lds[wv], acc);
+      dec_products<1, kDecDnSteps, 2>(codes, scales, a.h, rows, 2 * n, 0, steps, lds[wv], acc);
+      f32x4 y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = acc[0][i] + __shfl_xor(acc[0][i], 1);
       const int m = lane & 15;
-      if (m < n) {
-        const int r = m == 0 ? route[0] : m == 1 ? route[1] : m == 2 ? route[2] : route[3];
-        ys[r][lane >> 4] = acc[0];
-      }
+      if (m % 2 == 0 && m / 2 < n) ys[m == 0 ? route[0] : route[1]][lane >> 4] = y;
     }
   }
   __syncthreads();

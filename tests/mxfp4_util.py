@@ -25,3 +25,16 @@ def as_bf16_bits(codes, scales):
 def bf16_source(W):
     """The oracle's expert source over the same weights."""
     return lambda e: {n: as_bf16_bits(W[n][e], W["s" + n[1]][e]) for n in ("wg", "wu", "wd")}
+
+
+def unrounded_ref(x, ids, w, mask, W):
+    """The layer in 64 bits, h not rounded; x fp64 [T, d]."""
+    out = np.zeros_like(x)
+    E = W["wg"].shape[0]
+    on = (ids >= 0) & (ids < E) & (True if mask is None else mask != 0)
+    for e in np.unique(ids[on]):
+        t, j = np.nonzero(on & (ids == e))
+        g, u, d = (nx.mxfp4_decode(W["w" + n][e], W["s" + n][e]) for n in "gud")
+        y = (nx.silu(x[t] @ g.T) * (x[t] @ u.T)) @ d.T
+        np.add.at(out, t, w[t, j].astype(np.float64)[:, None] * y)
+    return out

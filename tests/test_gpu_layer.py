@@ -10,7 +10,7 @@ from oracle import moe as omoe
 from oracle import numerics as nx
 from oracle.router import route_topk as topk_ref
 from gpu_util import np_dev, rel_frob, routing_with_counts
-from mxfp4_util import bf16_source, mx_weights
+from mxfp4_util import bf16_source, mx_weights, unrounded_ref
 from test_gpu_ffn import FP8_TOL, _dev_weights, _weights, _x
 from test_gpu_mxfp4 import _close, _dev
 from test_gpu_norm import _check
@@ -54,8 +54,12 @@ def test_mxfp4_layer(T, k, E, d, f):
     _check((y, None, None, None), x, res, w1, 1e-6)
     ids_ref, _ = topk_ref(logits.cpu().numpy(), None, k)
     assert np.array_equal(ids.cpu().numpy(), ids_ref)
-    ref = omoe.moe_ref_blocked(_bits(y), ids.cpu().numpy(), gates.cpu().numpy(), None,
-                               bf16_source(W), E)[0]
+    if layer.decode:  # h not rounded to bf16
+        ref = unrounded_ref(nx.bf16_bits_to_f64(_bits(y)), ids.cpu().numpy(), gates.cpu().numpy(),
+                            None, W)
+    else:
+        ref = omoe.moe_ref_blocked(_bits(y), ids.cpu().numpy(), gates.cpu().numpy(), None,
+                                   bf16_source(W), E)[0]
     got = nx.bf16_bits_to_f64(_bits(out))
     # bf16 rounding of the output on top: at most 2^-8, 2^-9 in the mean
     assert rel_frob(got, ref) <= 1e-3 + 2.0 ** -9
