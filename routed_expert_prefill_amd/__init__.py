@@ -457,8 +457,10 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, 
         dev = torch._C._cuda_getDevice()
         done = native.add_rmsnorm(x, weight, eps, residual, residual_out, y, q, s, want_bf16,
                                   want_fp8, dev, torch._C._cuda_getCurrentRawStream(dev))
-        if done is not None:
+        if type(done) is tuple:
             return done
+        if done is not None:  # the launch's status: the kernel may have run, once is all
+            _lib.check(done, "moe_add_rmsnorm")
     # refusals, no rows, and without the module every call
     lib = _lib.load()
     dev = _on_current(x, "x")
@@ -513,10 +515,13 @@ def decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_
     if (native is not None and out is not None and workspace is not None
             and getattr(x, "is_cuda", False)):
         dev = torch._C._cuda_getDevice()
-        if native.decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_up,
-                             s_down, shared, out, workspace, dev,
-                             torch._C._cuda_getCurrentRawStream(dev)):
+        done = native.decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate,
+                                 s_up, s_down, shared, out, workspace, dev,
+                                 torch._C._cuda_getCurrentRawStream(dev))
+        if done is True:
             return out
+        if done is not None:  # the launch's status, as in add_rmsnorm
+            _lib.check(done, "moe_decode_ffn")
     # outputs to be made, refusals, and without the module every call
     lib = _lib.load()
     dev = _on_current(x, "x")

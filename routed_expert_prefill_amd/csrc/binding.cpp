@@ -5,8 +5,11 @@
 // arguments), more than one token's kernels.
 //
 // Each function returns None for whatever is not a plain good call -- another
-// type, shape or device, an error status -- and the Python code then checks
-// and calls by itself, so that every refusal has one place and one wording.
+// type, shape or device, a status of the argument checks -- and the Python
+// code then checks and calls by itself, so that every refusal has one place and
+// one wording.  A status of the launch itself is returned as it is, for Python
+// to raise: the kernel may have run, and an addition in place must not run
+// again.  For the same reason nothing that can fail follows the call.
 // The library is not linked: bind() takes the entry points of the one loaded.
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -51,11 +54,17 @@ T *ptr(const at::Tensor *t) {
   return t ? static_cast<T *>(t->data_ptr()) : nullptr;
 }
 
+// What a function returns for a status other than MOE_OK.
+PyObject *refused(int status) {
+  if (status == MOE_EHIP) return PyLong_FromLong(status);
+  Py_RETURN_NONE;
+}
+
 bool number(at::ScalarType t) { return t == at::kBFloat16 || t == at::kFloat; }
 int dtype(const at::Tensor &t) { return t.scalar_type() == at::kFloat ? MOE_DT_F32 : MOE_DT_BF16; }
 
 // add_rmsnorm(x, weight, eps, residual, residual_out, y, q, s, want_bf16,
-// want_fp8, device, stream) -> (y, residual_out, q, s) or None
+// want_fp8, device, stream) -> (y, residual_out, q, s), a status or None
 PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (n != 12 || !norm_entry || !PyBool_Check(a[8]) || !PyBool_Check(a[9])) Py_RETURN_NONE;
   Want want{(int)PyLong_AsLong(a[10])};
@@ -88,10 +97,8 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     static const int given[4] = {5, 4, 6, 7};
     for (int i = 0; i < 4; ++i)
       if (!out[i] && made[i].defined()) out[i] = &made[i];
-    const int rc = norm_entry(ptr(x), dtype(*x), ptr(r), ptr(out[1]), dtype(like), ptr(w),
-                              dtype(*w), (float)eps, (int)rows, (int)x->size(1), ptr(out[0]),
-                              ptr<uint8_t>(out[2]), ptr<float>(out[3]), stream);
-    if (rc != MOE_OK) Py_RETURN_NONE;
+    void *to[4];
+    for (int i = 0; i < 4; ++i) to[i] = ptr(out[i]);
     PyObject *result = PyTuple_New(4);
     if (!result) return nullptr;
     for (int i = 0; i < 4; ++i) {
@@ -103,14 +110,19 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (o == a[given[i]]) Py_INCREF(o);
       PyTuple_SET_ITEM(result, i, o);
     }
-    return result;
+    const int rc = norm_entry(ptr(x), dtype(*x), ptr(r), to[1], dtype(like), ptr(w), dtype(*w),
+                              (float)eps, (int)rows, (int)x->size(1), to[0],
+                              static_cast<uint8_t *>(to[2]), static_cast<float *>(to[3]), stream);
+    if (rc == MOE_OK) return result;
+    Py_DECREF(result);
+    return refused(rc);
   } catch (const std::exception &) {
     Py_RETURN_NONE;
   }
 }
 
 // decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate,
-// s_up, s_down, shared, out, workspace, device, stream) -> True or None
+// s_up, s_down, shared, out, workspace, device, stream) -> True, a status or None
 PyObject *decode_ffn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (n != 15 || !decode_entry) Py_RETURN_NONE;
   Want want{(int)PyLong_AsLong(a[13])};
@@ -149,7 +161,7 @@ PyObject *decode_ffn(PyObject *, PyObject *const *a, Py_ssize_t n) {
         &desc, ptr(x), ptr<int32_t>(ids), ptr<float>(w), ptr<uint8_t>(mask), ptr(wg), ptr(wu),
         ptr(wd), ptr(sg), ptr(su), ptr(sd), ptr<float>(shared), f32 ? ptr<float>(out) : nullptr,
         f32 ? nullptr : ptr(out), ptr(ws), (size_t)ws->numel(), stream);
-    if (rc != MOE_OK) Py_RETURN_NONE;
+    if (rc != MOE_OK) return refused(rc);
     Py_RETURN_TRUE;
   } catch (const std::exception &) {
     Py_RETURN_NONE;
