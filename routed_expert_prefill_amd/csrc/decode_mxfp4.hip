@@ -323,10 +323,10 @@ __global__ __launch_bounds__(kDecDnWaves *kWave) void decode_down_kernel(DecodeA
 }
 
 hipError_t launch_decode_mx4(const DecodeArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL(decode_gate_up_kernel, dim3(a.f / 16, a.R), dim3(kDecGuWaves * kWave), 0,
-                     stream, a);
-  hipLaunchKernelGGL(decode_down_kernel, dim3(a.d / 16), dim3(kDecDnWaves * kWave), 0, stream, a);
-  return hipGetLastError();
+  const hipError_t err =
+      launch(decode_gate_up_kernel, dim3(a.f / 16, a.R), dim3(kDecGuWaves * kWave), stream, a);
+  if (err != hipSuccess) return err;
+  return launch(decode_down_kernel, dim3(a.d / 16), dim3(kDecDnWaves * kWave), stream, a);
 }
 
 }  // namespace moe

@@ -1116,10 +1116,13 @@ __global__ __launch_bounds__(kM4Threads, 1) void grouped_gemm_mx4_kernel(Mx4Args
 
 hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream) {
   M4Schedule *sch = reinterpret_cast<M4Schedule *>(L.sch);
-  if (stages & kStagePlan)
-    hipLaunchKernelGGL(mx4_schedule_kernel, dim3(1), dim3(kM4ScheduleThreads), 0, stream, L.offsets,
-                       L.E, min(L.f / (kM4WRows / 2), (L.d + kM4WRows - 1) / kM4WRows), L.num_cus,
-                       sch, L.tiles);
+  hipError_t err = hipSuccess;
+  if (stages & kStagePlan) {
+    err = launch(mx4_schedule_kernel, dim3(1), dim3(kM4ScheduleThreads), stream, L.offsets, L.E,
+                 min(L.f / (kM4WRows / 2), (L.d + kM4WRows - 1) / kM4WRows), L.num_cus, sch,
+                 L.tiles);
+    if (err != hipSuccess) return err;
+  }
   Mx4Args g{};
   g.k = L.k;
   g.tiles = L.tiles;
@@ -1135,8 +1138,8 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
     g.N = L.f;
     g.K = L.d;
     g.heads = &sch->heads[0];
-    hipLaunchKernelGGL(grouped_gemm_mx4_kernel<true>, dim3(L.num_cus), dim3(kM4Threads), 0, stream,
-                       g);
+    err = launch(grouped_gemm_mx4_kernel<true>, dim3(L.num_cus), dim3(kM4Threads), stream, g);
+    if (err != hipSuccess) return err;
   }
   if (stages & kStageDown) {
     g.act = L.h;
@@ -1149,10 +1152,9 @@ hipError_t launch_ffn_mx4(const FfnLaunchMx4 &L, int stages, hipStream_t stream)
     g.N = L.d;
     g.K = L.f;
     g.heads = &sch->heads[1];
-    hipLaunchKernelGGL(grouped_gemm_mx4_kernel<false>, dim3(L.num_cus), dim3(kM4Threads), 0,
-                       stream, g);
+    err = launch(grouped_gemm_mx4_kernel<false>, dim3(L.num_cus), dim3(kM4Threads), stream, g);
   }
-  return hipGetLastError();
+  return err;
 }
 
 }  // namespace moe

@@ -9,6 +9,24 @@
 
 namespace moe {
 
+// Launches a kernel and returns the launch's own status.  (The thread's last
+// error, which a launch in angle brackets leaves as the only sign, may be an
+// earlier call's: the caller would then take a kernel that runs for one that
+// does not.)
+template <typename T>
+struct LaunchArg {
+  typedef T type;
+};
+template <typename... P>
+hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t stream,
+                  typename LaunchArg<P>::type... args) {
+  void *ptrs[] = {const_cast<void *>(static_cast<const void *>(&args))...};
+  const hipError_t err =
+      hipLaunchKernel(reinterpret_cast<const void *>(kernel), grid, block, ptrs, 0, stream);
+  if (err != hipSuccess) (void)hipGetLastError();  // reported here, not again by a later call
+  return err;
+}
+
 hipError_t launch_route_build(const int32_t *ids, const uint8_t *mask, int R, int E,
                               int32_t *counts, int32_t *offsets, int32_t *sorted_routes,
                               int32_t *route_rows, int32_t *ws, hipStream_t stream);

@@ -231,31 +231,24 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
 int norm_max_cols() { return kNmMaxCols; }
 
 template <int NC, bool WIDE>
-static void nm_launch(const NormArgs &a, hipStream_t stream) {
+static hipError_t nm_launch(const NormArgs &a, hipStream_t stream) {
   const dim3 grid(WIDE ? a.rows : (a.rows + kNmWaves - 1) / kNmWaves), block(kNmThreads);
-#define MOE_NORM_CASE(XF, RES)                                                          \
-  if (a.x_f32 == XF && a.res_kind == RES) {                                             \
-    hipLaunchKernelGGL((add_rmsnorm_kernel<NC, WIDE, XF, RES>), grid, block, 0, stream, a); \
-    return;                                                                             \
-  }
+#define MOE_NORM_CASE(XF, RES)             \
+  if (a.x_f32 == XF && a.res_kind == RES) \
+    return launch(add_rmsnorm_kernel<NC, WIDE, XF, RES>, grid, block, stream, a);
   MOE_NORM_CASE(false, 0) MOE_NORM_CASE(false, 1) MOE_NORM_CASE(false, 2)
   MOE_NORM_CASE(true, 0) MOE_NORM_CASE(true, 1) MOE_NORM_CASE(true, 2)
 #undef MOE_NORM_CASE
+  return hipErrorInvalidValue;  // the C ABI passes the kinds above only
 }
 
 hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t stream) {
   const int per = kNmThreads * 8;  // elements of one chunk of every thread of a workgroup
-  if (a.d <= kWave * 8)
-    nm_launch<1, false>(a, stream);
-  else if (a.d <= per)
-    nm_launch<1, true>(a, stream);
-  else if (a.d <= 2 * per)
-    nm_launch<2, true>(a, stream);
-  else if (a.d <= 4 * per)
-    nm_launch<4, true>(a, stream);
-  else
-    nm_launch<8, true>(a, stream);
-  return hipGetLastError();
+  if (a.d <= kWave * 8) return nm_launch<1, false>(a, stream);
+  if (a.d <= per) return nm_launch<1, true>(a, stream);
+  if (a.d <= 2 * per) return nm_launch<2, true>(a, stream);
+  if (a.d <= 4 * per) return nm_launch<4, true>(a, stream);
+  return nm_launch<8, true>(a, stream);
 }
 
 }  // namespace moe
