@@ -82,9 +82,12 @@ __device__ __forceinline__ double nm_wave_sum(double v) {
   return v;
 }
 
+// The larger of two magnitudes; NaN if one is (fmax would drop it).
+__device__ __forceinline__ double nm_max(double a, double b) { return b > a || b != b ? b : a; }
+
 __device__ __forceinline__ double nm_wave_max(double v) {
 #pragma unroll
-  for (int m = kWave / 2; m > 0; m >>= 1) v = fmax(v, __shfl_xor(v, m));
+  for (int m = kWave / 2; m > 0; m >>= 1) v = nm_max(v, __shfl_xor(v, m));
   return v;
 }
 
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
       const double t = (double)v[e];
       sum = __builtin_fma(t, t, sum);
       n[c][e] = v[e] * w[e];
-      if (a.q) top = fmax(top, fabs(sum_of(c, e) * (double)w[e]));
+      if (a.q) top = nm_max(top, fabs(sum_of(c, e) * (double)w[e]));
     }
     if (a.residual_out) nm_store8(a.residual_out, base + i, RES == 2 || (RES == 0 && XF), v);
   }
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int w = 1; w < kNmWaves; ++w) {
       sum += part_sum[w];
-      top = fmax(top, part_max[w]);
+      top = nm_max(top, part_max[w]);
     }
   }
   const float r = nm_rsqrt(sum / a.d + (double)a.eps);
