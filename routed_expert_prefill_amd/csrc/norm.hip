@@ -116,6 +116,28 @@ __device__ __forceinline__ float nm_rsqrt(double m) {
   return (float)(1.0 / sqrt(m));
 }
 
+// Whether multiplying a product v * weight by r may miss n, since one of them
+// has left fp32: r below its smallest normal number, the product beyond the
+// largest one (or no number: then n is none either) or below the smallest
+// normal one, with an r that brings it back among what bf16 holds.  With r up
+// to 2^12 a subnormal product is off by at most 2^-138 in n, an eighth of half
+// a step of the smallest normal bf16.
+__device__ __forceinline__ bool nm_past_fp32(float product, float r) {
+  const float p = fabsf(product);
+  constexpr float kMin = 1.17549435e-38f;
+  return !(p <= 3.40282347e38f) || r < kMin || (p < kMin && r > 4096.0f);
+}
+
+// Largest |n| and scale of a row whose products or root are near the ends of
+// fp32: from 64 bits, each rounded once.
+__device__ __forceinline__ void nm_far_scale(double top, double sum, double m, float *amax,
+                                             float *sc) {
+  // a v beyond fp32 is an infinity there, and n then NaN, whatever top is
+  const double t = sum < __builtin_inf() ? top / sqrt(m) : __builtin_nan("");
+  *amax = (float)t;
+  *sc = *amax == 0.0f ? 1.0f : (float)(t / 448.0);
+}
+
 // NC 8-element chunks per thread.  WIDE: the whole workgroup takes one row;
 // otherwise each of its waves takes a row of its own.
 // XF: x is fp32 (else bf16).  RES: 0 no residual, 1 bf16, 2 fp32.
@@ -143,6 +165,10 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
   // element e of chunk c of x + residual, unrounded
   const auto sum_of = [&](int c, int e) {
     return RES ? (double)xr[c].at(e) + (double)rr[c].at(e) : (double)xr[c].at(e);
+  };
+  const auto weight_at = [&](int i) {
+    return a.w_f32 ? static_cast<const float *>(a.weight)[i]
+                   : bf16_bits_to_f32(static_cast<const uint16_t *>(a.weight)[i]);
   };
   float n[NC][8];
   double sum = 0.0, top = 0.0;
@@ -190,22 +216,36 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
       top = nm_max(top, part_max[w]);
     }
   }
-  const float r = nm_rsqrt(sum / a.d + (double)a.eps);
-  const float sc = q_scale((float)top * r);
+  const double m = sum / a.d + (double)a.eps;
+  const float r = nm_rsqrt(m);
+  float amax = (float)top * r, sc = q_scale(amax);
+  const bool far = !(top >= 1e-28 && top <= 1e38 && r >= 1e-30f);  // near the ends of fp32
+  if (far && a.q) nm_far_scale(top, sum, m, &amax, &sc);
   bool exact;
   const float rcp = quant_rcp(sc, &exact);
-  exact = exact || top < 1e-28;  // products close to the end of fp32
+  exact = exact || far;
   if (a.s && tid == 0) a.s[row] = sc;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int i = (c * TPR + tid) * 8;
     if (i >= a.d) continue;
+    bool ends = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ends = ends || nm_past_fp32(n[c][e], r);
 #pragma unroll
     for (int e = 0; e < 8; ++e) n[c][e] *= r;
+    if (ends) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v = xr[c].at(e);
+        if (RES) v += rr[c].at(e);
+        n[c][e] = (float)((double)v * (double)weight_at(i + e) / sqrt(m));
+      }
+    }
     if (a.y) nm_store8(a.y, base + i, false, n[c]);
     if (!a.q) continue;
     uint2 o = {};
-    if ((float)top * r != 0.0f) {
+    if (amax != 0.0f) {
       bool any = exact;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -218,9 +258,7 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (!exact && !nm_near_midpoint(n[c][e])) continue;
-          const float w = a.w_f32 ? static_cast<const float *>(a.weight)[i + e]
-                                  : bf16_bits_to_f32(static_cast<const uint16_t *>(a.weight)[i + e]);
-          const double t = sum_of(c, e) * (double)w * 448.0 / top;
+          const double t = sum_of(c, e) * (double)weight_at(i + e) * 448.0 / top;
           const uint32_t code = nm_code(sc == sc ? t : (double)sc);
           uint32_t &part = e < 4 ? o.x : o.y;
           part = (part & ~(0xffu << (8 * (e & 3)))) | (code << (8 * (e & 3)));

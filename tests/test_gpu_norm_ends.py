@@ -76,3 +76,62 @@ def test_no_numbers_from_infinities(d):
     s, q = got[3].cpu().numpy(), got[2].cpu().numpy()
     assert np.isnan(s[4]) and s[5] == float("inf") and s[0] == float("inf")
     assert not np.delete(nx.e4m3_decode(q[[0, 5]]), 11, 1).any()
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("xt,rt,wt", [("bf16", None, "bf16"), ("f32", None, "f32"),
+                                      ("bf16", "bf16", "f32"), ("f32", "f32", "bf16")])
+def test_products_beyond_fp32(d, xt, rt, wt):
+    """|v weight| above 3.4e38 where n is an ordinary number; the sum itself stays
+    below it."""
+    import torch
+
+    T = {"bf16": torch.bfloat16, "f32": torch.float32, None: None}
+    x, w = _rows(d, 6, d + 2)
+    x = x.clamp(-3, 3)
+    x[1] *= 1e38 / (3 if rt else 1)
+    x[2] = x[2].sign() * 2e38 / (2 if rt else 1)
+    x[3, 5] = 1.5e38  # one element alone
+    x[4] *= 1e30
+    w = (w + torch.rand(d, generator=torch.Generator().manual_seed(1))) * 2
+    w[:4] = torch.tensor([1e-3, 1e5, -7, 0])
+    x, w = x.to(T[xt]), w.to(T[wt])
+    r = None if rt is None else (x.float() * 0.4).to(T[rt])
+    got = _norm(x, w, residual=r, eps=1e-5)
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[3]).all()
+    _check(got, x, r, w, float(np.float32(1e-5)))
+    one = _norm(x, w, residual=r, eps=1e-5, want_bf16=False)
+    assert torch.equal(one[2], got[2]) and torch.equal(one[3], got[3])
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+def test_products_below_fp32(d):
+    """|v weight| below fp32's numbers where a small eps lets r bring n back."""
+    import torch
+
+    x, w = _rows(d, 6, d + 3)
+    eps = float(np.float32(2e-38))
+    x[0] *= 1e-22
+    x[1] *= 1e-24
+    x[2] *= 1e-30
+    x[3] = 0
+    x[4, 1:] *= 1e-18
+    w = w * 1e-21
+    w[-8:] = 1
+    got = _norm(x, w, eps=eps)
+    _check(got, x, None, w, eps)
+    assert got[3][3] == 1 and not got[2][3].any() and (got[0][:3] != 0).any()
+
+
+def test_a_sum_beyond_fp32_is_no_number():
+    """v is formed in fp32: what overflows there is an infinity."""
+    import torch
+
+    x, w = _rows(640, 3, 9)
+    x[1, 20] = 3e38
+    r = x.clone()
+    y, ro, q, s = (t.cpu() for t in _norm(x, w, residual=r))
+    assert torch.isinf(ro[1, 20]) and torch.isnan(y[1, 20]) and torch.isnan(s[1])
+    assert not y[1, :20].any() and np.isnan(nx.e4m3_decode(q[1].numpy())).all()
+    fine = [0, 2]
+    _check((y[fine], ro[fine], q[fine], s[fine]), x[fine], r[fine], w, float(np.float32(1e-6)))
