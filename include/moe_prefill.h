@@ -373,11 +373,13 @@ int moe_decode_ffn(const moe_ffn_desc *desc /* host */, const void *x, const int
  *   y = bf16_rne(n)
  *   s[i] = max_c |n[i,c]| / 448 (1 for an all-zero row),  q = e4m3_rne_saturate(n / s)
  *
- * Each output is rounded once: residual_out, y and s from fp32, and q (which is
+ * Each output is rounded once: residual_out, y and s from fp32 (y and s from
+ * fp64 where v * weight or the root is near an end of fp32), and q (which is
  * not formed from y) from the quotient v * weight * 448 / max_c |v * weight| in
- * fp64, so that a code is the nearest one.  The mean is taken in fp64.  A row
- * that holds a NaN or an infinity gets NaN where the formulas give it; other
- * rows are unaffected.
+ * fp64, so that a code is the nearest one.  The mean is taken in fp64.  A NaN or
+ * an infinity in a row, or in the weight, gives NaN where the formulas do: with
+ * one NaN among a row's n, s is NaN and so are its codes.  Other rows are
+ * unaffected by a row's values.
  *
  * x            [rows, d], x_dtype (moe_dtype)
  * residual     [rows, d], residual_dtype, or NULL

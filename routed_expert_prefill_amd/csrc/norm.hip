@@ -19,6 +19,11 @@
 // fp64.  Codes taken from fp32 alone were off by one step in about one element
 // of a million.
 //
+// A wave whose products v weight leave fp32, or whose root is far from 1, forms
+// n in fp64, and a row's scale with it.  That it has to costs a maximum for
+// each element that keeps NaN (which the row's own maximum drops), 0.1 to 0.4 us
+// a call: 401 rows of 4096 8.0 -> 8.2, 8192 rows 49.4 -> 50.4.
+//
 // Bound by memory traffic (9 bytes per element with bf16 rows, a bf16
 // residual and both outputs) from a few hundred rows on: 8192 rows of 4096 take
 // 58.5 us on MI355X, 5.2 TB/s, where a large copy reaches 4.8.  Below that by
@@ -82,14 +87,15 @@ __device__ __forceinline__ double nm_wave_sum(double v) {
   return v;
 }
 
-// The larger of two magnitudes; NaN if one is (fmax would drop it).
-__device__ __forceinline__ double nm_max(double a, double b) { return b > a || b != b ? b : a; }
-
-__device__ __forceinline__ double nm_wave_max(double v) {
+// The largest of the lanes' magnitudes, NaN if a lane has `none` (fmax drops it).
+__device__ __forceinline__ double nm_wave_max(double v, bool none) {
 #pragma unroll
-  for (int m = kWave / 2; m > 0; m >>= 1) v = nm_max(v, __shfl_xor(v, m));
-  return v;
+  for (int m = kWave / 2; m > 0; m >>= 1) v = fmax(v, __shfl_xor(v, m));
+  return __any(none) ? __builtin_nan("") : v;
 }
+
+// The same of two.
+__device__ __forceinline__ double nm_max(double a, double b) { return b > a || b != b ? b : a; }
 
 // Whether a value within 8 x 2^-24 of y may have another code than y: it is
 // near a midpoint between codes, which are the patterns with low bits 0x80000
@@ -108,34 +114,6 @@ __device__ __forceinline__ uint32_t nm_code(double t) {
   if (f > fabs(t)) --b;
   if (f != fabs(t)) b |= 1u;
   return f32_to_e4m3(__uint_as_float(b));
-}
-
-// 1 / sqrt(m): in fp32 where m is well inside its range, in fp64 elsewhere.
-__device__ __forceinline__ float nm_rsqrt(double m) {
-  if (m > 1e-30 && m < 1e38) return 1.0f / sqrtf((float)m);
-  return (float)(1.0 / sqrt(m));
-}
-
-// Whether multiplying a product v * weight by r may miss n, since one of them
-// has left fp32: r below its smallest normal number, the product beyond the
-// largest one (or no number: then n is none either) or below the smallest
-// normal one, with an r that brings it back among what bf16 holds.  With r up
-// to 2^12 a subnormal product is off by at most 2^-138 in n, an eighth of half
-// a step of the smallest normal bf16.
-__device__ __forceinline__ bool nm_past_fp32(float product, float r) {
-  const float p = fabsf(product);
-  constexpr float kMin = 1.17549435e-38f;
-  return !(p <= 3.40282347e38f) || r < kMin || (p < kMin && r > 4096.0f);
-}
-
-// Largest |n| and scale of a row whose products or root are near the ends of
-// fp32: from 64 bits, each rounded once.
-__device__ __forceinline__ void nm_far_scale(double top, double sum, double m, float *amax,
-                                             float *sc) {
-  // a v beyond fp32 is an infinity there, and n then NaN, whatever top is
-  const double t = sum < __builtin_inf() ? top / sqrt(m) : __builtin_nan("");
-  *amax = (float)t;
-  *sc = *amax == 0.0f ? 1.0f : (float)(t / 448.0);
 }
 
 // NC 8-element chunks per thread.  WIDE: the whole workgroup takes one row;
@@ -172,6 +150,7 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
   };
   float n[NC][8];
   double sum = 0.0, top = 0.0;
+  float ptop = 0.0f;  // largest |v weight| of this thread in fp32, NaN if one is
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int i = (c * TPR + tid) * 8;
@@ -196,12 +175,14 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
       const double t = (double)v[e];
       sum = __builtin_fma(t, t, sum);
       n[c][e] = v[e] * w[e];
-      if (a.q) top = nm_max(top, fabs(sum_of(c, e) * (double)w[e]));
+      if (a.q) top = fmax(top, fabs(sum_of(c, e) * (double)w[e]));
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ptop = __builtin_elementwise_maximum(ptop, fabsf(n[c][e]));
     if (a.residual_out) nm_store8(a.residual_out, base + i, RES == 2 || (RES == 0 && XF), v);
   }
   sum = nm_wave_sum(sum);
-  top = nm_wave_max(top);
+  top = nm_wave_max(top, ptop != ptop);
   if (WIDE) {
     if (lane_id() == 0) {
       part_sum[wave] = sum;
@@ -217,31 +198,47 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
     }
   }
   const double m = sum / a.d + (double)a.eps;
-  const float r = nm_rsqrt(m);
-  float amax = (float)top * r, sc = q_scale(amax);
-  const bool far = !(top >= 1e-28 && top <= 1e38 && r >= 1e-30f);  // near the ends of fp32
-  if (far && a.q) nm_far_scale(top, sum, m, &amax, &sc);
+  float amax, sc, rcp = 0.0f;
   bool exact;
-  const float rcp = quant_rcp(sc, &exact);
-  exact = exact || far;
+  // Where fp32 may not do.  For n = (v weight) r: with a product of this wave
+  // beyond the largest number (or none), or a root far from 1.  (A subnormal product is off
+  // by at most 2^-150 r in n: with r below 2^12 an eighth of half a step of the
+  // smallest normal bf16.)  For the scale: with largest products near an end too.
+  const bool ends = __any(!(ptop <= 3.40282347e38f) || !(m > 6e-8 && m < 1e38));
+  if (ends || __any(a.q && !(top >= 1e-28 && top <= 1e38))) {
+    const double rd = 1.0 / sqrt(m);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int i = (c * TPR + tid) * 8;
+      if (i >= a.d) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v = xr[c].at(e);
+        if (RES) v += rr[c].at(e);
+        n[c][e] = ends ? (float)((double)v * (double)weight_at(i + e) * rd)
+                       : n[c][e] * (1.0f / sqrtf((float)m));
+      }
+    }
+    // a v beyond fp32 is an infinity there, and its n then NaN, whatever top is
+    const double t = sum < __builtin_inf() ? top * rd : __builtin_nan("");
+    amax = (float)t;
+    sc = amax == 0.0f ? 1.0f : (float)(t * (1.0 / 448.0));
+    exact = true;
+  } else {
+    const float r = 1.0f / sqrtf((float)m);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[c][e] *= r;
+    amax = (float)top * r;
+    sc = q_scale(amax);
+    rcp = quant_rcp(sc, &exact);
+  }
   if (a.s && tid == 0) a.s[row] = sc;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int i = (c * TPR + tid) * 8;
     if (i >= a.d) continue;
-    bool ends = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ends = ends || nm_past_fp32(n[c][e], r);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) n[c][e] *= r;
-    if (ends) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float v = xr[c].at(e);
-        if (RES) v += rr[c].at(e);
-        n[c][e] = (float)((double)v * (double)weight_at(i + e) / sqrt(m));
-      }
-    }
     if (a.y) nm_store8(a.y, base + i, false, n[c]);
     if (!a.q) continue;
     uint2 o = {};

@@ -52,6 +52,12 @@ def test_no_number_in_the_weight(d):
     w[d - 3] = float("nan")
     got = _norm(x, w)
     _no_numbers(got, x, w)
+    x[2, d - 4] = 3e38  # beside a NaN of the same thread: still the formula's number
+    w[d - 4] = 4
+    far = _norm(x, w)
+    _no_numbers(far, x, w)
+    n = _ref(x, None, w, 1e-6)[1][2, d - 4]
+    assert abs(far[0][2, d - 4].item() - n) <= (2.0 ** -8 + 2.0 ** -21) * n
     keep = np.arange(d) != d - 3
     assert np.array_equal(got[0].cpu().double().numpy()[:, keep],
                           clean[0].cpu().double().numpy()[:, keep])
@@ -101,6 +107,12 @@ def test_products_beyond_fp32(d, xt, rt, wt):
     assert torch.isfinite(got[0]).all() and torch.isfinite(got[3]).all()
     _check(got, x, r, w, float(np.float32(1e-5)))
     one = _norm(x, w, residual=r, eps=1e-5, want_bf16=False)
+    import routed_expert_prefill_amd as rep
+
+    dev = torch_dev()
+    y = rep.add_rmsnorm(x.to(dev), w.to(dev), eps=1e-5,
+                        residual=None if r is None else r.to(dev))[0]
+    assert torch.equal(y.view(torch.int16), got[0].view(torch.int16))
     assert torch.equal(one[2], got[2]) and torch.equal(one[3], got[3])
 
 
