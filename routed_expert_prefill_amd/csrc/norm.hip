@@ -37,6 +37,8 @@ namespace moe {
 
 constexpr int kNmThreads = 256;
 constexpr int kNmWaves = kNmThreads / kWave;
+// Workgroups in x: a grid takes fewer than 2^32 threads in each dimension.
+constexpr unsigned kNmLine = 1u << 22;
 constexpr int kNmMaxChunks = 8;  // 8-element chunks per thread
 constexpr int kNmMaxCols = kNmThreads * 8 * kNmMaxChunks;  // 16384
 
@@ -126,8 +128,11 @@ __global__ __launch_bounds__(kNmThreads) void add_rmsnorm_kernel(NormArgs a) {
   __shared__ double part_max[kNmWaves];
   const int wave = threadIdx.x / kWave;
   const int tid = WIDE ? (int)threadIdx.x : lane_id();
-  const int row = WIDE ? (int)blockIdx.x : (int)blockIdx.x * kNmWaves + wave;
-  if (!WIDE && row >= a.rows) return;  // no barrier below without WIDE
+  // the last line of workgroups may end past the rows
+  const unsigned block = blockIdx.y * kNmLine + blockIdx.x;
+  if (WIDE && block >= (unsigned)a.rows) return;
+  const int row = WIDE ? (int)block : (int)(block * kNmWaves) + wave;
+  if (!WIDE && (row < 0 || row >= a.rows)) return;  // no barrier below without WIDE
   const size_t base = (size_t)row * a.d;
 
   NmRaw<XF> xr[NC];
@@ -270,7 +275,9 @@ int norm_max_cols() { return kNmMaxCols; }
 
 template <int NC, bool WIDE>
 static hipError_t nm_launch(const NormArgs &a, hipStream_t stream) {
-  const dim3 grid(WIDE ? a.rows : (a.rows + kNmWaves - 1) / kNmWaves), block(kNmThreads);
+  const unsigned blocks = WIDE ? (unsigned)a.rows : ((unsigned)a.rows + kNmWaves - 1) / kNmWaves;
+  const dim3 grid(blocks < kNmLine ? blocks : kNmLine, (blocks + kNmLine - 1) / kNmLine),
+      block(kNmThreads);
 #define MOE_NORM_CASE(XF, RES)             \
   if (a.x_f32 == XF && a.res_kind == RES) \
     return launch(add_rmsnorm_kernel<NC, WIDE, XF, RES>, grid, block, stream, a);

@@ -147,3 +147,25 @@ def test_a_sum_beyond_fp32_is_no_number():
     assert not y[1, :20].any() and np.isnan(nx.e4m3_decode(q[1].numpy())).all()
     fine = [0, 2]
     _check((y[fine], ro[fine], q[fine], s[fine]), x[fine], r[fine], w, float(np.float32(1e-6)))
+
+
+@pytest.mark.parametrize("rows,d", [((1 << 26) + 5, 8), ((1 << 24) + 3, 520)])
+def test_more_rows_than_one_dimension_of_a_grid(rows, d):
+    """One workgroup of 256 threads to four rows or to one: 2^32 threads and more."""
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    g = torch.Generator("cuda").manual_seed(rows)
+    x = torch.randn(rows, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = (1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16)
+    y = torch.full((rows + 2, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    rep.add_rmsnorm(x, w, y=y[:rows])
+    torch.cuda.synchronize()
+    assert (y[rows:] == 7).all()
+    step = 1 << 22
+    for a in range(0, rows, step):
+        part = rep.add_rmsnorm(x[a:a + step], w)[0]
+        assert torch.equal(part.view(torch.int16), y[a:min(a + step, rows)].view(torch.int16)), a
+    _check((y[rows - 9:rows], None, None, None), x[-9:].cpu(), None, w.cpu(),
+           float(np.float32(1e-6)))
