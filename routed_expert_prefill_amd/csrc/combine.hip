@@ -20,6 +20,8 @@
 namespace moe {
 
 constexpr int kCombThreads = 256;
+// Most workgroups in x: a grid takes fewer than 2^32 threads in each dimension.
+constexpr int kCombLine = 1 << 22;
 
 // K routes per token, known at compile time: the token's masks, rows and
 // gates are read once (uniform, scalar loads), then the rows of every route
@@ -38,11 +40,13 @@ __global__ __launch_bounds__(kCombThreads) void combine_kernel(const float *__re
                                                                const uint8_t *__restrict__ mask,
                                                                const int32_t *__restrict__ row_limit,
                                                                const float *__restrict__ shared,
-                                                               int T, int d, int slices,
+                                                               int T, int d, int slices, int per,
                                                                float *__restrict__ out,
                                                                uint16_t *__restrict__ out_bf16) {
-  const int t = blockIdx.x / slices;
-  const int c = ((blockIdx.x - t * slices) * kCombThreads + threadIdx.x) * 4;
+  const int tl = blockIdx.x / slices;
+  const int t = blockIdx.y * per + tl;
+  if (t >= T) return;  // the last line may end past the tokens
+  const int c = ((blockIdx.x - tl * slices) * kCombThreads + threadIdx.x) * 4;
   const int lim = row_limit != nullptr ? *row_limit : INT_MAX;
   const size_t r0 = (size_t)t * K;
   // lane j of every wave loads route j's mask, row and gate (one load of
@@ -105,12 +109,14 @@ hipError_t launch_combine(const float *y, const int32_t *route_rows, const float
                           hipStream_t stream) {
   const int per_block = kCombThreads * 4;
   const int slices = (d + per_block - 1) / per_block;
-  const dim3 grid((unsigned)T * slices), block(kCombThreads);
+  const int most = kCombLine / slices > 0 ? kCombLine / slices : 1;
+  const int lines = (int)(((long long)T + most - 1) / most), per = T < most ? T : most;
+  const dim3 grid((unsigned)per * slices, lines), block(kCombThreads);
   switch (k) {
 #define MOE_COMBINE_CASE(K)                                                                     \
   case K:                                                                                      \
     hipLaunchKernelGGL(combine_kernel<K>, grid, block, 0, stream, y, route_rows, topk_w, mask, \
-                       row_limit, shared, T, d, slices, out, out_bf16);                        \
+                       row_limit, shared, T, d, slices, per, out, out_bf16);                   \
     break;
     MOE_COMBINE_CASE(1) MOE_COMBINE_CASE(2) MOE_COMBINE_CASE(3) MOE_COMBINE_CASE(4)
     MOE_COMBINE_CASE(5) MOE_COMBINE_CASE(6) MOE_COMBINE_CASE(7) MOE_COMBINE_CASE(8)
