@@ -302,7 +302,13 @@ __global__ __launch_bounds__(kDecDnWaves *kWave) void decode_down_kernel(DecodeA
       dec_products<1, kDecDnSteps, 2>(codes, scales, a.h, rows, 2 * n, 0, steps, lds[wv], acc);
       f32x4 y;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = acc[0][i] + __shfl_xor(acc[0][i], 1);
+      for (int i = 0; i < 4; ++i) {
+        const float rest = __shfl_xor(acc[0][i], 1);
+        y[i] = acc[0][i];
+        // an infinite weight has made the first part's sum what it is, and times
+        // the second part (zero, or of the other sign) it would make it NaN
+        if (fabsf(y[i]) < __builtin_inff()) y[i] += rest;
+      }
       const int m = lane & 15;
       if (m % 2 == 0 && m / 2 < n) ys[m == 0 ? route[0] : route[1]][lane >> 4] = y;
     }
