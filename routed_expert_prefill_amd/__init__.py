@@ -570,17 +570,37 @@ class MoEPrefill:
 
     weights: "bf16", "fp8" or "mxfp4" (default: by fp8).  out_dtype:
     torch.float32 (default) or torch.bfloat16.  With MXFP4 weights and few
-    routes (DECODE_ROUTES) a pass is decode_ffn, unless stage events are asked
-    for or self.decode is set to False: self.rt and self.y are then not written."""
+    routes (_decodes) a pass is decode_ffn, unless stage events are asked
+    for or self.decode is set to False: self.rt and self.y are then not written.
+    decode_ffn keeps 16 bits of h, the grouped path 8: a token's output differs
+    by up to about 2^-8 of its norm between the two, on top of the order of sums.
+    A program that needs one answer for both sets decode to False."""
 
-    # At most this many routes go through decode_ffn, its own limit, and from 33
-    # on no more than four for each expert there is.  Over 256 experts, d 4096,
-    # f 2048, 6 routes take 21 us (grouped: 48), 24 take 62 (76) and 60 take 144
-    # (172); over 16 experts, d 1024, f 512, 64 routes 20 (28).  Where experts
-    # have many routes decode_ffn reads their weights again for every two or
-    # four: 8 experts, d 4096, f 2048, 16 routes 27 us (47), 32 routes 46 (47),
-    # 64 routes 63 (48).
-    DECODE_ROUTES = 64
+    DECODE_ROUTES = 64  # the most that decode_ffn takes
+
+    @classmethod
+    def _decodes(cls, T: int, k: int, E: int, d: int, f: int) -> bool:
+        """Whether decode_ffn is the faster way, as far as shapes tell.
+
+        It reads an expert's weights again for every four rows (gate/up) and
+        every two (down); the grouped path reads them once and has three
+        launches more.  MI355X, us (grouped in brackets); zipf: routers with
+        favourites; same: every token to the same k experts.
+
+        At d 4096, f 2048 up to 24 tokens and 32 routes it is the faster one
+        whatever the ids: 24 routes over 256 experts 62 (77), same 26 (49);
+        32 over 8 41 (47), zipf 46 (48), same 43 (50); 24 of one expert 59 (62),
+        32 of one 74 (62).  More routes pay while there are experts for them:
+        60 over 256 144 (169), zipf 123 (164), same 57 (50); 40 over 32 81 (82);
+        40 over 16 56 (53); 64 over 16 73 (53), over 8 72 (48).  With more tokens
+        too much hangs on the ids: 64 tokens over 256 experts 148 (172), all
+        to one 150 (65); 32 tokens 82 (90), all to one 77 (62).  Narrow layers are
+        launches mostly: d 1024, f 512, 64 routes over 16 experts 21 (28), zipf 26
+        (29), same 33 (33)."""
+        R = T * k
+        if R > cls.DECODE_ROUTES or T > 32:
+            return False
+        return d * f <= 1 << 19 or 2 * R <= 3 * E or (T <= 24 and R <= 32)
 
     def __init__(self, T: int, k: int, E: int, d: int, f: int, fp8: bool = False, device="cuda",
                  weights: Optional[str] = None, out_dtype=None):
@@ -613,7 +633,7 @@ class MoEPrefill:
         # the route build sends to the trailing bin -- add exact zeros, as
         # masked ones do.
         self.row_limit = self.rt.offsets[E:E + 1]
-        self.decode = self.weights == "mxfp4" and R <= min(self.DECODE_ROUTES, max(32, 4 * E))
+        self.decode = self.weights == "mxfp4" and self._decodes(T, k, E, d, f)
 
     def __call__(self, x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate=None,
                  s_up=None, s_down=None, stage_events=None, shared=None):
