@@ -18,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_prefill.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 HIP_SOURCES = ["route_topk.hip", "route_build.hip", "combine.hip", "quant.hip", "ffn_grouped.hip",
                "ffn_fp8.hip", "norm.hip", "ffn_mxfp4.hip", "decode_mxfp4.hip"]
@@ -67,7 +68,16 @@ def build(verbose: bool = False, defines=(), out: str = LIB, build_dir: str = BU
     _run([cc, "-shared", "--offload-arch=gfx950", "-o", tmp, *objs])
     os.replace(tmp, out)
     if out == LIB:
-        build_binding()
+        # The extension module only shortens two Python calls: without torch's
+        # or Python's headers or a C++ compiler there is none, and those calls
+        # go through ctypes.  A module of older sources is not left behind.
+        try:
+            build_binding()
+        except (ImportError, OSError, RuntimeError) as e:
+            if os.path.exists(BINDING):
+                os.remove(BINDING)
+            print(f"warning: built without the extension module for short calls: {e}",
+                  file=sys.stderr)
     return out
 
 
@@ -79,7 +89,7 @@ def build_binding() -> str:
     import torch
 
     top = os.path.dirname(os.path.abspath(torch.__file__))
-    out = os.path.join(PKG, "_binding.so")
+    out = BINDING
     cc = shutil.which("g++") or shutil.which("c++") or hipcc()
     _run([cc, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-cast-function-type",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
