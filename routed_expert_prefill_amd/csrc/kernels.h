@@ -142,7 +142,7 @@ struct DecodeArgs {
   const uint8_t *mask;  // [T, k] or null
   const uint8_t *wg, *wu, *wd, *sg, *su, *sd;
   const float *shared;  // [T, d] or null
-  uint16_t *h;          // [T * k, f]
+  uint16_t *h;          // [2, T * k, f]: the rounded values, then what that took
   float *out;           // [T, d] or null
   uint16_t *out_bf16;   // [T, d] or null
   int T, k, E, d, f, R;
