@@ -481,8 +481,11 @@ constexpr int kM4DirectAct = kM4Ring - kM4Waves * kM4ScaleWave;  // LDS for acti
 // in different banks.
 __device__ __forceinline__ int m4_direct_stride(int K) { return 2 * K + 16; }
 __device__ __forceinline__ bool m4_direct_fits(int K) {
-  return kM4DirectRows * m4_direct_stride(K) <= kM4DirectAct;  // K <= 4,608
+  return kM4DirectRows * m4_direct_stride(K) <= kM4DirectAct;  // K <= 4,736
 }
+static_assert(kM4DirectRows * (2 * 4736 + 16) <= kM4DirectAct &&
+                  kM4DirectRows * (2 * 4864 + 16) > kM4DirectAct,
+              "the longest multiple of 128 that fits");
 
 // One chunk of a wave's two weight tiles of 16 rows.
 struct M4Chunk {
