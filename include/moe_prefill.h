@@ -340,8 +340,10 @@ int moe_quant_rows_fp8(const void *x, int rows, int cols, uint8_t *q, float *s,
  *
  * A route is read when route_mask[r] != 0 (or route_mask is NULL) and its id
  * lies in [0, E); any other adds an exact zero, its gate is not read, and a
- * token with no route read gets +0.0 (plus its shared row).  The weights of an
- * expert are read for the first route that names it.
+ * token with no route read gets +0.0 (plus its shared row).  The routes that name
+ * one expert share its weights, up to four to a pass over w_gate and w_up and
+ * up to two to one over w_down: routes spread over experts suit this call,
+ * many routes of one expert moe_grouped_ffn.
  *
  * desc        weight_dtype MOE_W_MXFP4, act_dtype MOE_ACT_BF16, T * k at most
  *             MOE_DECODE_MAX_ROUTES

@@ -592,12 +592,13 @@ class MoEPrefill:
         32 over 8 41 (47), zipf 46 (48), same 43 (50); 24 of one expert 59 (62).
         32 tokens of one route each gain while they have experts to go to: over
         8 40 (47), zipf 44 (48), all to one 77 (62); over 4 47 (49), zipf 46
-        (49); over 2 44 (50), zipf 68 (62).  More routes pay while there are experts for them:
-        60 over 256 144 (169), zipf 123 (164), same 57 (50); 40 over 32 81 (82);
-        40 over 16 56 (53); 64 over 16 73 (53), over 8 72 (48).  With more tokens
-        too much hangs on the ids: 64 tokens over 256 experts 148 (172), all
-        to one 150 (65).  Narrow layers are launches mostly: d 1024, f 512, 64 routes over 16 experts 21 (28), zipf 26
-        (29), same 33 (33)."""
+        (49); over 2 44 (50), zipf 68 (62).  More routes pay while there are
+        experts for them: 60 over 256 144 (169), zipf 123 (164), same 57 (50);
+        40 over 32 81 (82); 40 over 16 56 (53); 64 over 16 73 (53), over 8 72
+        (48).  With more tokens too much hangs on the ids: 64 tokens over 256
+        experts 148 (172), all to one 150 (65).  Narrow layers are launches
+        mostly: d 1024, f 512, 64 routes over 16 experts 21 (28), zipf 26 (29),
+        same 33 (33)."""
         R = T * k
         if R > cls.DECODE_ROUTES or T > 32:
             return False

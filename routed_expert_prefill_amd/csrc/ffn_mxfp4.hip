@@ -6,7 +6,12 @@
 //
 // for sorted row i of expert e and token t; h is rounded to bf16 because it is
 // the second product's operand in the matrix unit, as in the bf16 kernels, and
-// nothing else is rounded to fewer than 32 bits.  Weights stay codes until the
+// nothing else is rounded to fewer than 32 bits.  (That costs accuracy: outputs
+// in bf16 are 0.0023 to 0.0024 of their norm from the formulas instead of
+// 0.0017.  A second bf16 part, as the single-token kernels have it, would
+// double the products of down, which is what bounds it from about 48 rows an
+// expert on, and its activation rows, which decide the tile classes below
+// that.)  Weights stay codes until the
 // products: a lane reads 16 bytes of a weight row, 32 codes, exactly one scale
 // group, and converts them in registers, so no pass over expanded weights
 // exists and a weight costs 4.25 bits of memory traffic.  The order of a
@@ -671,7 +676,10 @@ __device__ __forceinline__ void m4_direct(const Mx4Args &a, const Tile &t, int n
 // one on its way while one is multiplied, and the waves meet once per slice.
 // Wave w takes weight rows [64 w, 64 w + 64) of the item's 512, which keeps
 // the reads of activations at half of what LDS can do beside the products, and
-// multiplies with as many 16-row tiles as hold rows (TM).  Against the ring,
+// multiplies with as many 16-row tiles as hold rows (TM), by the 16x16x32
+// instruction, whose rate on this card is 1.24 PFLOP/s where the ring's
+// 32x32x16 has 2.1: the products, not the loads, are the longer part from
+// about 40 rows on.  Against the ring,
 // which multiplies 64 rows always and meets every 128 columns (MI355X, 256
 // experts, d 4096, f 2048, gate/up): 24 rows an expert 670 -> 510 us, 48 rows
 // 735 -> 605, 64 rows 720 -> 690.  At 48 rows the loads alone take 460 us and

@@ -3,9 +3,10 @@
 // 32 columns of a row.
 //
 // Every value below 2^128 that an E2M1 code and an E8M0 scale stand for is a
-// bf16 number (subnormals included; larger ones become infinite), so gfx950's conversion instruction loses nothing and
-// the products go through the bf16 matrix unit: two weights per instruction,
-// checked on MI355X for every byte under every scale.
+// bf16 number (subnormals included; larger ones become infinite), so gfx950's
+// conversion instruction loses nothing and the products go through the bf16
+// matrix unit: two weights per instruction, checked on MI355X for every byte
+// under every scale.
 #pragma once
 
 #include "common.h"

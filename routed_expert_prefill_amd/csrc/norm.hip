@@ -25,11 +25,14 @@
 // a call: 401 rows of 4096 8.0 -> 8.2, 8192 rows 49.4 -> 50.4.
 //
 // Bound by memory traffic (9 bytes per element with bf16 rows, a bf16
-// residual and both outputs) from a few hundred rows on: 8192 rows of 4096 take
+// residual and both outputs) from a few thousand rows on: 8192 rows of 4096 take
 // 58.5 us on MI355X, 5.2 TB/s, where a large copy reaches 4.8.  Below that by
-// the latency of one row's load, reduction and store: one row of 4096 4 us, 401
-// rows 9 us.  A workgroup to a row keeps that latency short; rows of up to 512
-// columns would leave three of its waves idle, so a wave takes one there.
+// the latency of one row's loads, reduction and stores: one row of 4096 4 us, 401
+// rows 8 to 9 us against 3 us of traffic.  Rows of several chunks a thread wait
+// for a store of their own in between: the weight of the next chunk is loaded
+// behind residual_out's store, and stores count among the loads that the wait
+// for it covers.  A workgroup to a row keeps the latency short; rows of up to
+// 512 columns would leave three of its waves idle, so a wave takes one there.
 #include "e4m3.h"
 #include "kernels.h"
 
