@@ -115,9 +115,8 @@ hipError_t launch_combine(const float *y, const int32_t *route_rows, const float
   switch (k) {
 #define MOE_COMBINE_CASE(K)                                                                     \
   case K:                                                                                      \
-    hipLaunchKernelGGL(combine_kernel<K>, grid, block, 0, stream, y, route_rows, topk_w, mask, \
-                       row_limit, shared, T, d, slices, per, out, out_bf16);                   \
-    break;
+    return launch(combine_kernel<K>, grid, block, stream, y, route_rows, topk_w, mask,         \
+                  row_limit, shared, T, d, slices, per, out, out_bf16);
     MOE_COMBINE_CASE(1) MOE_COMBINE_CASE(2) MOE_COMBINE_CASE(3) MOE_COMBINE_CASE(4)
     MOE_COMBINE_CASE(5) MOE_COMBINE_CASE(6) MOE_COMBINE_CASE(7) MOE_COMBINE_CASE(8)
     MOE_COMBINE_CASE(9) MOE_COMBINE_CASE(10) MOE_COMBINE_CASE(11) MOE_COMBINE_CASE(12)
@@ -126,7 +125,6 @@ hipError_t launch_combine(const float *y, const int32_t *route_rows, const float
     default:
       return hipErrorInvalidValue;  // the C ABI accepts 1 <= k <= 16 only
   }
-  return hipGetLastError();
 }
 
 }  // namespace moe

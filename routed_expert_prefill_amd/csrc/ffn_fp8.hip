@@ -468,9 +468,7 @@ hipError_t launch_ffn_fp8(const FfnLaunchFp8 &L, int stages, hipStream_t stream)
     g.counter_s = &L.sch->counter_s[0];
     g.nb = 1;
     g.hmax = L.hmax;
-    hipLaunchKernelGGL(grouped_gemm8_kernel<true>, dim3(L.num_cus), dim3(kG8Threads), 0, stream,
-                       g);
-    err = hipGetLastError();
+    err = launch(grouped_gemm8_kernel<true>, dim3(L.num_cus), dim3(kG8Threads), stream, g);
     if (err != hipSuccess) return err;
   }
   if (stages & kStageDown) {
@@ -496,10 +494,9 @@ hipError_t launch_ffn_fp8(const FfnLaunchFp8 &L, int stages, hipStream_t stream)
     // (MI355X, 8192 tokens: down 0.946 -> 0.877 ms with four, 0.884 with two)
     g.nb = kG8MaxBlocks;
     while (g.nb > 1 && L.d % (128 * g.nb) != 0) g.nb >>= 1;
-    hipLaunchKernelGGL(grouped_gemm8_kernel<false>, dim3(L.num_cus), dim3(kG8Threads), 0, stream,
-                       g);
+    err = launch(grouped_gemm8_kernel<false>, dim3(L.num_cus), dim3(kG8Threads), stream, g);
   }
-  return hipGetLastError();
+  return err;
 }
 
 }  // namespace moe

@@ -590,9 +590,7 @@ __global__ __launch_bounds__(kGgThreads, 1) void grouped_gemm_kernel(GgArgs a) {
 
 hipError_t launch_grouped_schedule(const int32_t *offsets, int E, Schedule *sch, Tile *tiles,
                                    hipStream_t stream) {
-  hipLaunchKernelGGL(grouped_schedule_kernel, dim3(1), dim3(kGsThreads), 0, stream, offsets, E,
-                     sch, tiles);
-  return hipGetLastError();
+  return launch(grouped_schedule_kernel, dim3(1), dim3(kGsThreads), stream, offsets, E, sch, tiles);
 }
 
 // Weight rows per item.  With at most 32 routed rows in all (decode-sized
@@ -638,8 +636,9 @@ static int item_blocks(int wr, int n_out, int mats, int want) {
 }
 
 hipError_t launch_grouped_ffn_bf16(const FfnLaunch &L, int stages, hipStream_t stream) {
+  hipError_t err = hipSuccess;
   if (stages & kStagePlan) {
-    const hipError_t err = launch_grouped_schedule(L.offsets, L.E, L.sch, L.tiles, stream);
+    err = launch_grouped_schedule(L.offsets, L.E, L.sch, L.tiles, stream);
     if (err != hipSuccess) return err;
   }
   GgArgs g{};
@@ -662,7 +661,8 @@ hipError_t launch_grouped_ffn_bf16(const FfnLaunch &L, int stages, hipStream_t s
     g.nb = 1;
     g.nb_skinny = 1;
     g.static_items = static_items(L);
-    hipLaunchKernelGGL(grouped_gemm_kernel<true>, dim3(L.num_cus), dim3(kGgThreads), 0, stream, g);
+    err = launch(grouped_gemm_kernel<true>, dim3(L.num_cus), dim3(kGgThreads), stream, g);
+    if (err != hipSuccess) return err;
   }
   if (stages & kStageDown) {
     g.act = L.h;
@@ -678,10 +678,9 @@ hipError_t launch_grouped_ffn_bf16(const FfnLaunch &L, int stages, hipStream_t s
     g.nb = item_blocks(g.wr, L.d, 1, 2);
     g.nb_skinny = item_blocks(g.wr, L.d, 1, 4);
     g.static_items = static_items(L);
-    hipLaunchKernelGGL(grouped_gemm_kernel<false>, dim3(L.num_cus), dim3(kGgThreads), 0, stream,
-                       g);
+    err = launch(grouped_gemm_kernel<false>, dim3(L.num_cus), dim3(kGgThreads), stream, g);
   }
-  return hipGetLastError();
+  return err;
 }
 
 }  // namespace moe

@@ -229,15 +229,13 @@ hipError_t launch_quant_rows_known_max(const uint16_t *x, int rows, const int32_
   const long long want = (chunks + kQThreads - 1) / kQThreads;
   const long long cap = (long long)grid_cap * 4;
   const int grid = (int)(want < cap ? want : cap);
-  hipLaunchKernelGGL(quant_rows_known_max_kernel, dim3(grid > 0 ? grid : 1), dim3(kQThreads), 0,
-                     stream, x, rows, rows_dev, cols, amax_bits, q, s);
-  return hipGetLastError();
+  return launch(quant_rows_known_max_kernel, dim3(grid > 0 ? grid : 1), dim3(kQThreads), stream, x,
+                rows, rows_dev, cols, amax_bits, q, s);
 }
 
 hipError_t launch_zero_u32(uint32_t *p, int n, hipStream_t stream) {
   const int grid = (n + kQThreads * 4 - 1) / (kQThreads * 4);
-  hipLaunchKernelGGL(zero_u32_kernel, dim3(grid > 0 ? grid : 1), dim3(kQThreads), 0, stream, p, n);
-  return hipGetLastError();
+  return launch(zero_u32_kernel, dim3(grid > 0 ? grid : 1), dim3(kQThreads), stream, p, n);
 }
 
 hipError_t launch_quant_rows(const uint16_t *x, int rows, const int32_t *rows_dev, int cols,
@@ -251,20 +249,18 @@ hipError_t launch_quant_rows(const uint16_t *x, int rows, const int32_t *rows_de
     const long long cap = (long long)grid_cap * 4;
     const int grid = (int)(want < cap ? want : cap);
     if (nl <= 2)
-      hipLaunchKernelGGL(quant_rows_wave_kernel<2>, dim3(grid > 0 ? grid : 1), dim3(kQThreads), 0,
-                         stream, x, rows, rows_dev, cols, q, s);
+      return launch(quant_rows_wave_kernel<2>, dim3(grid > 0 ? grid : 1), dim3(kQThreads), stream,
+                    x, rows, rows_dev, cols, q, s);
     else if (nl <= 4)
-      hipLaunchKernelGGL(quant_rows_wave_kernel<4>, dim3(grid > 0 ? grid : 1), dim3(kQThreads), 0,
-                         stream, x, rows, rows_dev, cols, q, s);
+      return launch(quant_rows_wave_kernel<4>, dim3(grid > 0 ? grid : 1), dim3(kQThreads), stream,
+                    x, rows, rows_dev, cols, q, s);
     else  // up to 4096 columns: two waves of four loads per lane
-      hipLaunchKernelGGL(quant_rows_pair_kernel<4>, dim3(grid > 0 ? grid : 1), dim3(kQThreads), 0,
-                         stream, x, rows, rows_dev, cols, q, s);
-    return hipGetLastError();
+      return launch(quant_rows_pair_kernel<4>, dim3(grid > 0 ? grid : 1), dim3(kQThreads), stream,
+                    x, rows, rows_dev, cols, q, s);
   }
   const int grid = rows < grid_cap ? rows : grid_cap;
-  hipLaunchKernelGGL(quant_rows_kernel, dim3(grid > 0 ? grid : 1), dim3(kQThreads), 0, stream, x,
-                     rows, rows_dev, cols, q, s);
-  return hipGetLastError();
+  return launch(quant_rows_kernel, dim3(grid > 0 ? grid : 1), dim3(kQThreads), stream, x, rows,
+                rows_dev, cols, q, s);
 }
 
 }  // namespace moe

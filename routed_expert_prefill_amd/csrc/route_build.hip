@@ -272,15 +272,14 @@ hipError_t launch_route_build(const int32_t *ids, const uint8_t *mask, int R, in
   int key_bits = 1;
   while ((1 << key_bits) < E + 1) ++key_bits;
   if (R <= kFusedMaxR) {
-    hipLaunchKernelGGL(rb_fused_kernel, dim3(1), dim3(kFusedThreads), 0, stream, ids, mask, R, E,
-                       key_bits, counts, offsets, sorted_routes, route_rows);
-    return hipGetLastError();
+    return launch(rb_fused_kernel, dim3(1), dim3(kFusedThreads), stream, ids, mask, R, E, key_bits,
+                  counts, offsets, sorted_routes, route_rows);
   }
-  hipLaunchKernelGGL(rb_hist_kernel, dim3(nchunks), dim3(kRbThreads), 0, stream, ids, mask, R, E,
-                     chunk_hist);
-  hipLaunchKernelGGL(rb_scatter_kernel, dim3(nchunks), dim3(kRbThreads), 0, stream, ids, mask, R,
-                     E, key_bits, nchunks, chunk_hist, counts, offsets, sorted_routes, route_rows);
-  return hipGetLastError();
+  const hipError_t err = launch(rb_hist_kernel, dim3(nchunks), dim3(kRbThreads), stream, ids, mask,
+                                R, E, chunk_hist);
+  if (err != hipSuccess) return err;
+  return launch(rb_scatter_kernel, dim3(nchunks), dim3(kRbThreads), stream, ids, mask, R, E,
+                key_bits, nchunks, chunk_hist, counts, offsets, sorted_routes, route_rows);
 }
 
 size_t route_build_ws_bytes(int R, int E) {

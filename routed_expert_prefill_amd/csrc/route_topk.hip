@@ -87,9 +87,8 @@ hipError_t launch_route_topk(const float *logits, const float *bias, int T, int 
                              int32_t *ids, float *gates, int grid_cap, hipStream_t stream) {
   const long long want = ((long long)T + kTkWaves - 1) / kTkWaves;
   const int grid = (int)(want < grid_cap ? want : grid_cap);
-  hipLaunchKernelGGL(route_topk_kernel, dim3(grid), dim3(kTkThreads), 0, stream, logits, bias, T, E,
-                     k, ids, gates);
-  return hipGetLastError();
+  return launch(route_topk_kernel, dim3(grid), dim3(kTkThreads), stream, logits, bias, T, E, k, ids,
+                gates);
 }
 
 }  // namespace moe

@@ -85,3 +85,60 @@ def test_experts(stale):
     torch.cuda.synchronize()
     assert torch.equal(layer.out.view(torch.int32), want.view(torch.int32))
     assert torch.equal(y[:n].view(torch.int32), rows[:n].view(torch.int32))
+
+
+@pytest.mark.parametrize("weights", ["bf16", "fp8"])
+def test_the_path(stale, weights):
+    """Router, route builds, row codes, FFN (fp8: on codes too) and combines."""
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    leave, last = stale
+    T, k, E, d, f = 900, 6, 16, 256, 128  # more routes than one workgroup builds
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn(T, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    shared = torch.randn(T, d, generator=g, device="cuda")
+    shapes = ((E, f, d), (E, f, d), (E, d, f))
+    if weights == "bf16":
+        W = [torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16) * 0.05 for s in shapes]
+        S = [None] * 3
+    else:
+        W = [torch.randint(0, 120, s, generator=g, device="cuda", dtype=torch.uint8) for s in shapes]
+        S = [torch.rand(E, s[1] // 128, s[2] // 128, generator=g, device="cuda") for s in shapes]
+    ids, w = rep.route_topk(logits, k)
+    rt, few = rep.route_build(ids, None, E), rep.route_build(ids[:4].contiguous(), None, E)
+    rbw = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    desc = rep.ffn_desc(T, k, E, d, f, weights=weights)
+    ws = torch.empty(rep.load_library().moe_grouped_ffn_workspace(desc), dtype=torch.uint8,
+                     device="cuda")
+    y, out, both = (torch.zeros(n, d, device="cuda") for n in (T * k, T, T))
+    q, s = rep.quant_rows_fp8(x)
+    yq, ids4 = torch.zeros_like(y), ids[:4].contiguous()
+
+    def calls():
+        rep.route_topk(logits, k, topk_ids=ids, topk_w=w)
+        rep.route_build(ids, None, E, out=rt, workspace=rbw)
+        rep.route_build(ids4, None, E, out=few, workspace=rbw)
+        rep.route_build_noalloc(ids4, None, E, out=few)
+        rep.quant_rows_fp8(x, q=q, s=s)
+        rep.grouped_ffn(x, rt.offsets, rt.sorted_routes, *W, k, *S, y=y, workspace=ws)
+        if weights == "fp8":
+            rep.grouped_ffn_codes(q, s, rt.offsets, rt.sorted_routes, *W, k, *S, y=yq, workspace=ws)
+        rep.combine(y, rt.route_rows, w, None, out=out)
+        rep.combine_shared(y, rt.route_rows, w, None, shared=shared, out=both)
+
+    outputs = [ids, w, *rt, *few, q, s, y, yq, out, both]
+    calls()
+    want = [t.clone() for t in outputs]
+    for t in outputs:
+        t.zero_()
+    torch.cuda.synchronize()
+    bad = leave()
+    calls()
+    assert last() == bad
+    rep.load_library().hipGetLastError()
+    torch.cuda.synchronize()
+    for t, u in zip(outputs, want):
+        assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))
