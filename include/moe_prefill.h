@@ -28,7 +28,9 @@
  *    asynchronous.
  *  - All argument checks run on the host before any HIP call, so a rejected
  *    call touches no device memory.  Return value: MOE_OK (0) or a negative
- *    moe_status.  MOE_EHIP reports a launch error from the HIP runtime.
+ *    moe_status.  MOE_EHIP reports an error of the call's own launches (not one
+ *    that another HIP call left on the thread, which stays there); a call of
+ *    several launches stops at the first that fails.
  *  - Device base pointers must be 16-byte aligned (MOE_EALIGN otherwise):
  *    the kernels use 16-byte vector loads and stores.  This is the
  *    library's alignment admission rule.
