@@ -87,8 +87,8 @@ typedef struct moe_ffn_desc {
   int32_t T;            /* tokens, >= 1 */
   int32_t k;            /* routes per token, 1 <= k <= min(E, 16) */
   int32_t E;            /* experts, 1 <= E <= 256 */
-  int32_t d;            /* model width, multiple of 128 */
-  int32_t f;            /* expert FFN width, multiple of 128 */
+  int32_t d;            /* model width, multiple of 128; at most 2^24 with MXFP4 weights */
+  int32_t f;            /* expert FFN width, the same */
   int32_t weight_dtype; /* moe_weight_dtype */
   int32_t act_dtype;    /* moe_act_dtype; FP8_E4M3_ROW iff weights are FP8_E4M3_B128
                            (bf16 activations with bf16 and MXFP4 weights) */

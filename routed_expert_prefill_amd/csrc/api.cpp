@@ -67,6 +67,10 @@ bool ffn_desc_status(const moe_ffn_desc *d, int *st) {
     *st = MOE_EUNSUPPORTED;
     return false;
   }
+  if (d->weight_dtype == MOE_W_MXFP4 && (d->d > moe::kMx4MaxWidth || d->f > moe::kMx4MaxWidth)) {
+    *st = MOE_EUNSUPPORTED;
+    return false;
+  }
   if (a8 && (d->d > moe::quant_max_cols() || d->f > moe::quant_max_cols())) {
     *st = MOE_EUNSUPPORTED;
     return false;

@@ -117,6 +117,12 @@ struct FfnLaunchFp8 {
 };
 hipError_t launch_ffn_fp8(const FfnLaunchFp8 &L, int stages, hipStream_t stream);
 
+// The widest rows of the MXFP4 kernels, whose loads take 32-bit offsets from a
+// uniform base: 256 weight rows of codes to an item (2^31 bytes), and 128 rows of
+// activations of a single-token call (2^31 elements).  Twice as wide would still
+// do; at 2^26 columns the offsets, and the test for rows that fit LDS, wrap.
+constexpr int kMx4MaxWidth = 1 << 24;
+
 // Grouped FFN with MXFP4 weights and bf16 activations (ffn_mxfp4.hip).
 struct FfnLaunchMx4 {
   const uint16_t *x;

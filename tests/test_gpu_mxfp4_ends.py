@@ -89,3 +89,56 @@ def test_every_code_under_every_scale_is_exact(way, sel):
     got = out[:, :f].cpu().numpy().astype(np.float64)
     assert np.array_equal(got, want)
     assert not out[:, f:].any()
+
+
+@pytest.mark.parametrize("d,f", [(1 << 24, 128), (128, 1 << 24)])
+def test_the_widest_rows(d, f):
+    """Offsets up to 2^31 in either projection, 20 tokens grouped and one by itself.
+    h is rounded to bf16 (2^-8 at most) on the grouped path; fp32 sums of 2^24
+    terms in steps of 16 add less than 2^-12."""
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    gen = torch.Generator("cuda").manual_seed(f)
+    table = torch.tensor([v if c < 8 else -v for c in range(16)
+                          for v in ([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0][c % 8],)],
+                         dtype=torch.float64, device="cuda")
+    T, low = 20, 114 if d > f else 124
+
+    def weights(rows, cols, byte):
+        codes = torch.randint(0, 256, (1, rows, cols // 2), generator=gen, dtype=torch.uint8,
+                              device="cuda")
+        scales = torch.randint(byte, byte + 2, (1, rows, cols // 32), generator=gen,
+                               dtype=torch.uint8, device="cuda")
+        return codes, scales
+
+    def times(a, codes, scales):
+        """a [T, cols] @ w.T in 64 bits, 2^24 weights at a time."""
+        _, rows, half = codes.shape
+        out = torch.zeros(T, rows, dtype=torch.float64, device="cuda")
+        step_c = min(half, 1 << 16)
+        step_r = min(rows, (1 << 23) // step_c)
+        for r in range(0, rows, step_r):
+            for c in range(0, half, step_c):
+                b = codes[0, r:r + step_r, c:c + step_c].long()
+                w = table[torch.stack([b & 15, b >> 4], -1).flatten(1)]
+                s = scales[0, r:r + step_r, c // 16:(c + step_c) // 16].double()
+                w = w * torch.exp2(s - 127).repeat_interleave(32, 1)
+                out[:, r:r + step_r] += a[:, 2 * c:2 * (c + step_c)] @ w.T.contiguous()
+        return out
+
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    (wg, sg), (wu, su), (wd, sd) = weights(f, d, low), weights(f, d, low), weights(d, f, 238 - low)
+    g, u = times(x.double(), wg, sg), times(x.double(), wu, su)
+    want = times(g / (1 + torch.exp(-g)) * u, wd, sd)
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    ones = torch.ones(T, 1, device="cuda")
+    layer = rep.MoEPrefill(T, 1, 1, d, f, weights="mxfp4")
+    layer.decode = False
+    out = layer(x, ids, ones, None, wg, wu, wd, sg, su, sd).double()
+    one = rep.decode_ffn(x[7:8], ids[:1], ones[:1], None, wg, wu, wd, sg, su, sd).double()
+    norm = torch.linalg.vector_norm
+    for got, ref, tol in ((out, want, 2.0 ** -8 + 2.0 ** -12), (one, want[7:8], 2.0 ** -12)):
+        assert torch.isfinite(got).all()
+        assert norm(got - ref) <= tol * norm(ref), (norm(got - ref) / norm(ref)).item()
