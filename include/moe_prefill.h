@@ -403,6 +403,121 @@ int moe_add_rmsnorm(const void *x, int x_dtype, const void *residual, void *resi
                     int residual_dtype, const void *weight, int weight_dtype, float eps, int rows,
                     int d, void *y, uint8_t *q, float *s, moe_stream_t stream);
 
+/* ------------------------------------------------------------ expert selection from scores
+ * The step ahead of moe_route_build for routers that score every expert, bias
+ * the choice alone, and choose by groups:
+ *
+ *   s[t,e] = sigmoid(logits[t,e]), or the softmax of the row's logits
+ *   c[t,e] = s[t,e] + bias[e]                (the bias chooses, it does not weigh)
+ *   groups of E / groups consecutive experts; a group's value is the sum of its
+ *       group_top (1 or 2) largest c; the top_groups groups of largest value are
+ *       kept, and c = -inf outside them (one group, kept: no groups)
+ *   topk_ids[t] = the k largest c[t,.], descending
+ *   topk_w[t,j] = s of the j-th chosen, with renormalise over the sum of the
+ *       chosen ones' s (0 where that is 0), times scale
+ *
+ * Equal values (of groups too) go to the lower index.  Scores, choices, sums and
+ * gates are those of 64 bits, so that the order is that of the formulas; a gate is
+ * rounded once.  An expert whose logit is -inf is out of service: s = 0, c = -inf;
+ * it adds nothing to its group's value (which is -inf if all are out).  A choice
+ * of -inf is taken, lower indices first, when nothing else is left; its gate is 0.
+ * NaN comes before every number, and gives a NaN gate: a NaN logit makes its
+ * sigmoid score NaN, or every softmax score of its row that is not out of service,
+ * as an infinite one does.  ids are always k different ones of [0, E).
+ *
+ * logits [T,E], logits_dtype (moe_dtype); bias fp32 [E] or NULL;
+ * topk_ids int32 [T,k] and topk_w fp32 [T,k] are written in full.
+ * Errors: MOE_EINVAL (null desc, logits or outputs, T, E, k, groups or top_groups
+ *         below 1, T*E overflows int, scale not finite), MOE_EUNSUPPORTED
+ *         (unknown type or scores, E > 256, k > 16, groups > 64 or no divisor of
+ *         E, top_groups > groups, k > top_groups * (E / groups), group_top
+ *         neither 1 nor 2), MOE_EALIGN, MOE_EHIP.
+ */
+typedef enum moe_scores {
+  MOE_SCORES_SOFTMAX = 0,
+  MOE_SCORES_SIGMOID = 1
+} moe_scores;
+
+typedef struct moe_select_desc {
+  int32_t T, E, k;
+  int32_t logits_dtype; /* moe_dtype */
+  int32_t scores;       /* moe_scores */
+  int32_t groups;
+  int32_t top_groups;
+  int32_t group_top;   /* choices that a group's value sums, 1 or 2 */
+  int32_t renormalise; /* nonzero: gates over their sum */
+  float scale;
+} moe_select_desc;
+
+int moe_route_select(const moe_select_desc *desc /* host */, const void *logits, const float *bias,
+                     int32_t *topk_ids, float *topk_w, moe_stream_t stream);
+
+/* ------------------------------------------------------------ fp8 quantisation by blocks
+ * E4M3 codes with one scale for each block of 128 columns of a row, the rule of
+ * moe_quant_rows_fp8 with a block in a row's place:
+ *
+ *   s[i,b] = fp32(max over block b of |x[i,c]|) / 448  (1 for an all-zero block,
+ *            2^-149 where the quotient rounds to 0)
+ *   q[i,c] = e4m3_rne_saturate(x[i,c] / s[i, c/128])   (IEEE fp32 divisions)
+ *
+ * A NaN gets a NaN code and is left out of its block's maximum.
+ * x [rows, cols], x_dtype (moe_dtype); q uint8 [rows, cols]; s fp32 [rows, cols/128].
+ * Errors: MOE_EINVAL (null, rows or cols below 1), MOE_EUNSUPPORTED (unknown
+ *         type, cols not a multiple of 128), MOE_EALIGN, MOE_EHIP.
+ */
+int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t *q, float *s,
+                         moe_stream_t stream);
+
+/* ------------------------------------------------------------ 8-bit product with block scales
+ * The product of a dense layer beside the routed experts, weights as
+ * MOE_W_FP8_E4M3_B128 has them for one matrix, rows with a scale for each block of
+ * 128 columns:
+ *
+ *   y[m,n] = sum over blocks b of  xs[m,b] * ws[n/128,b] *
+ *            sum over columns c of block b of  x[m,c] * w[n,c]
+ *
+ * Products and sums in fp32 (the two scales of a block are multiplied first, in
+ * fp32: their product has to lie in its range); y is rounded once.  One row's
+ * result depends on no other row.
+ *
+ * x, xs      xs given: E4M3 codes uint8 [M,K] and fp32 scales [M,K/128]
+ *            (moe_quant_blocks_fp8); xs NULL: bf16 [M,K], quantised so by the call
+ * w, ws      E4M3 codes uint8 [N,K], fp32 [ceil(N/128), K/128]; N is any
+ * y          [M,N], y_dtype (moe_dtype); overlaps no input
+ * workspace  at least moe_matmul_fp8_workspace(M,N,K) bytes where xs is NULL,
+ *            otherwise not used (NULL is fine); contents on entry are ignored
+ * Errors: MOE_EINVAL (null, a size below 1), MOE_EUNSUPPORTED (K not a multiple of
+ *         128 or above 2^20, M/32 * N/16 (each rounded up) 2^31 or more, unknown
+ *         type), MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
+ */
+size_t moe_matmul_fp8_workspace(int M, int N, int K);
+int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const uint8_t *w,
+                   const float *ws, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
+                   moe_stream_t stream);
+
+/* ------------------------------------------------------------ shared expert
+ * The gated layer that every token passes beside its routed experts; its rows are
+ * the `shared` of moe_combine_shared and moe_decode_ffn:
+ *
+ *   g = Wg . x[t],  u = Wu . x[t],  h = silu(g) * u     (fp32, products as above)
+ *   h quantised as moe_quant_blocks_fp8 does            (from fp32: one rounding)
+ *   out[t] = Wd . h
+ *
+ * x, xs      as for moe_matmul_fp8: bf16 [T,d], or codes [T,d] and scales [T,d/128]
+ * w_gate, w_up  uint8 [f,d], s_gate, s_up fp32 [f/128, d/128]
+ * w_down     uint8 [d,f], s_down fp32 [d/128, f/128]
+ * out        [T,d], out_dtype (moe_dtype); overlaps no input
+ * workspace  at least moe_shared_ffn_workspace(T,d,f) bytes; contents on entry are ignored
+ * Errors: MOE_EINVAL (null, a size below 1), MOE_EUNSUPPORTED (d or f not a
+ *         multiple of 128 or above 2^20, T rows too many for moe_matmul_fp8,
+ *         unknown type), MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
+ */
+size_t moe_shared_ffn_workspace(int T, int d, int f);
+int moe_shared_ffn(const void *x, const float *xs, int T, int d, int f, const uint8_t *w_gate,
+                   const uint8_t *w_up, const uint8_t *w_down, const float *s_gate,
+                   const float *s_up, const float *s_down, void *out, int out_dtype,
+                   void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,14 +9,15 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import NamedTuple, Optional
 
 from . import _lib
 from ._lib import (MOE_ACT_BF16, MOE_ACT_FP8_E4M3_ROW, MOE_W_BF16, MOE_W_FP8_E4M3_B128,
-                   MOE_W_MXFP4, LibraryNotBuilt, MoeFfnDesc)
+                   MOE_SCORES_SIGMOID, MOE_SCORES_SOFTMAX, MOE_W_MXFP4, LibraryNotBuilt, MoeFfnDesc)
 
 __all__ = [
-    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "grouped_ffn_codes", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "decode_ffn", "MoEPrefill", "RouteTable",
+    "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "grouped_ffn_codes", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "decode_ffn", "route_select", "quant_blocks_fp8", "matmul_fp8", "shared_ffn", "MoEPrefill", "RouteTable",
     "ffn_desc", "ffn_plan", "ffn_gate_up", "ffn_down", "LibraryNotBuilt", "load_library",
 ]
 
@@ -63,6 +64,9 @@ def _native():
         else:
             _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                             for f in (lib.moe_add_rmsnorm, lib.moe_decode_ffn)))
+            _binding.bind_dense(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.moe_route_select, lib.moe_quant_blocks_fp8, lib.moe_matmul_fp8_workspace,
+                lib.moe_matmul_fp8, lib.moe_shared_ffn_workspace, lib.moe_shared_ffn)))
         _native_module = _binding
     return _native_module
 
@@ -561,6 +565,238 @@ def decode_ffn(x, topk_ids, topk_w, route_mask, w_gate, w_up, w_down, s_gate, s_
                             None if f32 else out.data_ptr(), workspace.data_ptr(),
                             workspace.numel(), _stream())
     _lib.check(rc, "moe_decode_ffn")
+    return out
+
+
+# scores of route_select by name
+_SCORES = {"softmax": MOE_SCORES_SOFTMAX, "sigmoid": MOE_SCORES_SIGMOID}
+
+
+def _int32(value, name) -> int:
+    """value as the C ABI's ints hold it (ctypes would drop the bits above)."""
+    value = operator.index(value)
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
+def route_select(logits, k: int, scores: str = "sigmoid", bias=None, groups: int = 1,
+                 top_groups: int = 1, group_top: int = 2, renormalise: bool = True,
+                 scale: float = 1.0, topk_ids=None, topk_w=None):
+    """moe_route_select: the k experts of largest score + bias, out of the
+    top_groups best of `groups` groups, and the gates of their scores.
+
+    logits [T, E] are fp32 or bf16 (-inf: out of service), scores "sigmoid" or
+    "softmax" over all E, bias fp32 [E] chooses only.  A group's value is the sum
+    of its group_top (1 or 2) largest choices.  Returns (topk_ids, topk_w), what
+    route_build, combine and MoEPrefill take.  No rows: nothing is launched."""
+    torch = _torch()
+    native = _native()
+    if native is not None and getattr(logits, "is_cuda", False):
+        dev = torch._C._cuda_getDevice()
+        done = native.route_select(logits, k, _SCORES.get(scores), bias, groups, top_groups,
+                                   group_top, bool(renormalise), scale, topk_ids, topk_w, dev,
+                                   torch._C._cuda_getCurrentRawStream(dev))
+        if type(done) is tuple:
+            return done
+        if done is not None:  # the launch's status, as in add_rmsnorm
+            _lib.check(done, "moe_route_select")
+    lib = _lib.load()
+    dev = _on_current(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must have 2 dims, got {logits.dim()}")
+    if scores not in _SCORES:
+        raise ValueError(f"scores must be one of {sorted(_SCORES)}, got {scores!r}")
+    f32 = torch.float32
+    _need_rows(logits, "logits", logits.shape, (f32, torch.bfloat16), dev)
+    T, E = logits.shape
+    k, groups, top_groups, group_top = (
+        _int32(v, n) for v, n in ((k, "k"), (groups, "groups"), (top_groups, "top_groups"),
+                                  (group_top, "group_top")))
+    if k < 1:
+        raise ValueError(f"k must be at least 1, got {k}")
+    if bias is not None:
+        _need_rows(bias, "bias", (E,), (f32,), dev)
+    if topk_ids is None:
+        topk_ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty(T, k, dtype=f32, device=dev)
+    _need_rows(topk_ids, "topk_ids", (T, k), (torch.int32,), dev)
+    _need_rows(topk_w, "topk_w", (T, k), (f32,), dev)
+    if T == 0:
+        return topk_ids, topk_w
+    desc = _lib.MoeSelectDesc(T, _int32(E, "E"), k, int(logits.dtype == f32), _SCORES[scores],
+                              groups, top_groups, group_top, bool(renormalise), scale)
+    rc = lib.moe_route_select(ctypes.byref(desc), logits.data_ptr(), _ptr(bias),
+                              topk_ids.data_ptr(), topk_w.data_ptr(), _stream())
+    _lib.check(rc, "moe_route_select")
+    return topk_ids, topk_w
+
+
+def quant_blocks_fp8(x, q=None, s=None):
+    """moe_quant_blocks_fp8: E4M3 codes (uint8) of bf16 or fp32 rows [rows, cols]
+    and fp32 scales [rows, cols / 128], one for each block of 128 columns.  No
+    rows: nothing is launched."""
+    torch = _torch()
+    native = _native()
+    if native is not None and getattr(x, "is_cuda", False):
+        dev = torch._C._cuda_getDevice()
+        done = native.quant_blocks_fp8(x, q, s, dev, torch._C._cuda_getCurrentRawStream(dev))
+        if type(done) is tuple:
+            return done
+        if done is not None:  # the launch's status, as in add_rmsnorm
+            _lib.check(done, "moe_quant_blocks_fp8")
+    lib = _lib.load()
+    dev = _on_current(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must have 2 dims, got {x.dim()}")
+    rows, cols = x.shape
+    _need_rows(x, "x", x.shape, (torch.bfloat16, torch.float32), dev)
+    if cols % 128 != 0:
+        raise ValueError(f"x must have a multiple of 128 columns, got {cols}")
+    if q is None:
+        q = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
+    if s is None:
+        s = torch.empty(rows, cols // 128, dtype=torch.float32, device=dev)
+    _need_rows(q, "q", (rows, cols), (torch.uint8,), dev)
+    _need_rows(s, "s", (rows, cols // 128), (torch.float32,), dev)
+    if rows == 0:
+        return q, s
+    rc = lib.moe_quant_blocks_fp8(x.data_ptr(), int(x.dtype == torch.float32),
+                                  _int32(rows, "rows"), _int32(cols, "cols"), q.data_ptr(),
+                                  s.data_ptr(), _stream())
+    _lib.check(rc, "moe_quant_blocks_fp8")
+    return q, s
+
+
+def _need_codes(x):
+    """x as (rows, scales or None), checked: bf16 rows, or a pair of E4M3 codes
+    and the scales of their blocks."""
+    torch = _torch()
+    xs = None
+    if isinstance(x, tuple):
+        if len(x) != 2:
+            raise ValueError("x must be bf16 rows or a pair of codes and scales")
+        x, xs = x
+    dev = _on_current(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must have 2 dims, got {x.dim()}")
+    _need_rows(x, "x", x.shape, (torch.bfloat16 if xs is None else torch.uint8,), dev)
+    if x.shape[1] % 128 != 0:
+        raise ValueError(f"x must have a multiple of 128 columns, got {x.shape[1]}")
+    if xs is not None:
+        _need_rows(xs, "the scales of x", (x.shape[0], x.shape[1] // 128), (torch.float32,), dev)
+    return x, xs
+
+
+def _need_blocks(w, s, name, N, K, dev):
+    """E4M3 codes [N, K] and a scale for each block of 128 x 128."""
+    _need_rows(w, "w" + name, (N, K), (_torch().uint8,), dev)
+    _need_rows(s, "s" + name, (-(-N // 128), K // 128), (_torch().float32,), dev)
+
+
+def _need_out(out, out_dtype, shape, dev):
+    torch = _torch()
+    kinds = (torch.float32, torch.bfloat16)
+    if out is None:
+        if out_dtype not in (None, *kinds):
+            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+        out = torch.empty(shape, dtype=out_dtype or torch.float32, device=dev)
+    _need_rows(out, "out", shape, kinds, dev)
+    return out
+
+
+def _need_ws(workspace, need, dev):
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _need_rows(workspace, "workspace", workspace.shape, (torch.uint8,), dev)
+    return workspace
+
+
+def matmul_fp8(x, w, s, out=None, out_dtype=None, workspace=None):
+    """moe_matmul_fp8: x [M, K] times the transpose of 8-bit weights w [N, K].
+
+    x: bf16 rows, quantised by the call, or the pair (codes, scales) of
+    quant_blocks_fp8.  w: E4M3 codes (uint8), s: fp32 [ceil(N / 128), K / 128], a
+    scale for each block of 128 x 128.  out [M, N] is fp32 or bf16; if it is not
+    given, it is made in out_dtype (torch.float32 by default).  workspace is used
+    for bf16 rows only.  No rows: nothing is launched."""
+    torch = _torch()
+    native = _native()
+    rows, xs = x if type(x) is tuple and len(x) == 2 else (x, None)
+    if native is not None and getattr(rows, "is_cuda", False):
+        dev = torch._C._cuda_getDevice()
+        done = native.matmul_fp8(rows, xs, w, s, out, out_dtype in (None, torch.float32),
+                                 out is None and out_dtype not in (None, torch.float32, torch.bfloat16),
+                                 workspace, dev, torch._C._cuda_getCurrentRawStream(dev))
+        if type(done) is int:  # the launch's status, as in add_rmsnorm
+            _lib.check(done, "moe_matmul_fp8")
+        if done is not None:
+            return done
+    lib = _lib.load()
+    x, xs = _need_codes(x)
+    dev = x.device
+    M, K = (_int32(v, "a size of x") for v in x.shape)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a tensor of 2 dims")
+    N = _int32(w.shape[0], "N")
+    _need_blocks(w, s, "", N, K, dev)
+    out = _need_out(out, out_dtype, (M, N), dev)
+    if M == 0:
+        return out
+    if xs is None:
+        workspace = _need_ws(workspace, lib.moe_matmul_fp8_workspace(M, N, K), dev)
+    else:
+        workspace = None
+    rc = lib.moe_matmul_fp8(x.data_ptr(), _ptr(xs), M, N, K, w.data_ptr(), s.data_ptr(),
+                            out.data_ptr(), int(out.dtype == torch.float32), _ptr(workspace),
+                            0 if workspace is None else workspace.numel(), _stream())
+    _lib.check(rc, "moe_matmul_fp8")
+    return out
+
+
+def shared_ffn(x, w_gate, w_up, w_down, s_gate, s_up, s_down, out=None, out_dtype=None,
+               workspace=None):
+    """moe_shared_ffn: the shared expert, Wd . (silu(Wg . x) * (Wu . x)), whose rows
+    are the `shared` of combine_shared, decode_ffn and MoEPrefill.
+
+    x [T, d] and out [T, d] as for matmul_fp8; w_gate, w_up [f, d] and w_down
+    [d, f] E4M3 codes (uint8), their scales fp32 for each block of 128 x 128."""
+    torch = _torch()
+    native = _native()
+    rows, xs = x if type(x) is tuple and len(x) == 2 else (x, None)
+    if native is not None and getattr(rows, "is_cuda", False):
+        dev = torch._C._cuda_getDevice()
+        done = native.shared_ffn(rows, xs, w_gate, w_up, w_down, s_gate, s_up, s_down, out,
+                                 out_dtype in (None, torch.float32),
+                                 out is None and out_dtype not in (None, torch.float32, torch.bfloat16),
+                                 workspace, dev, torch._C._cuda_getCurrentRawStream(dev))
+        if type(done) is int:  # the launch's status, as in add_rmsnorm
+            _lib.check(done, "moe_shared_ffn")
+        if done is not None:
+            return done
+    lib = _lib.load()
+    x, xs = _need_codes(x)
+    dev = x.device
+    T, d = (_int32(v, "a size of x") for v in x.shape)
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate must be a tensor of 2 dims")
+    f = _int32(w_gate.shape[0], "f")
+    if f % 128 != 0:
+        raise ValueError(f"w_gate must have a multiple of 128 rows, got {f}")
+    _need_blocks(w_gate, s_gate, "_gate", f, d, dev)
+    _need_blocks(w_up, s_up, "_up", f, d, dev)
+    _need_blocks(w_down, s_down, "_down", d, f, dev)
+    out = _need_out(out, out_dtype, (T, d), dev)
+    if T == 0:
+        return out
+    workspace = _need_ws(workspace, lib.moe_shared_ffn_workspace(T, d, f), dev)
+    rc = lib.moe_shared_ffn(x.data_ptr(), _ptr(xs), T, d, f, w_gate.data_ptr(), w_up.data_ptr(),
+                            w_down.data_ptr(), s_gate.data_ptr(), s_up.data_ptr(),
+                            s_down.data_ptr(), out.data_ptr(), int(out.dtype == torch.float32),
+                            workspace.data_ptr(), workspace.numel(), _stream())
+    _lib.check(rc, "moe_shared_ffn")
     return out
 
 

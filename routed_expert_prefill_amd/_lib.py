@@ -26,6 +26,8 @@ MOE_DT_BF16 = 0
 MOE_DT_F32 = 1
 MOE_ACT_BF16 = 0
 MOE_ACT_FP8_E4M3_ROW = 1
+MOE_SCORES_SOFTMAX = 0
+MOE_SCORES_SIGMOID = 1
 
 EXPORTED = [
     "moe_status_string", "moe_abi_version",
@@ -35,6 +37,8 @@ EXPORTED = [
     "moe_combine", "moe_quant_rows_fp8", "moe_route_topk", "moe_combine_shared",
     "moe_route_build_noalloc", "moe_add_rmsnorm",
     "moe_decode_ffn_workspace", "moe_decode_ffn", "moe_grouped_ffn_codes",
+    "moe_route_select", "moe_quant_blocks_fp8", "moe_matmul_fp8_workspace", "moe_matmul_fp8",
+    "moe_shared_ffn_workspace", "moe_shared_ffn",
 ]
 
 
@@ -42,6 +46,12 @@ class MoeFfnDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("k", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("f", ctypes.c_int32),
                 ("weight_dtype", ctypes.c_int32), ("act_dtype", ctypes.c_int32)]
+
+
+class MoeSelectDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "logits_dtype", "scores", "groups",
+                                              "top_groups", "group_top", "renormalise")] + [
+        ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -101,6 +111,18 @@ def load() -> ctypes.CDLL:
     lib.moe_decode_ffn.argtypes = [dp] + [vp] * 14 + [sz, vp]
     lib.moe_grouped_ffn_codes.restype = i32
     lib.moe_grouped_ffn_codes.argtypes = [dp] + [vp] * 12 + [sz, vp]
+    lib.moe_route_select.restype = i32
+    lib.moe_route_select.argtypes = [ctypes.POINTER(MoeSelectDesc), vp, vp, vp, vp, vp]
+    lib.moe_quant_blocks_fp8.restype = i32
+    lib.moe_quant_blocks_fp8.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+    lib.moe_matmul_fp8_workspace.restype = sz
+    lib.moe_matmul_fp8_workspace.argtypes = [i32, i32, i32]
+    lib.moe_matmul_fp8.restype = i32
+    lib.moe_matmul_fp8.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, sz, vp]
+    lib.moe_shared_ffn_workspace.restype = sz
+    lib.moe_shared_ffn_workspace.argtypes = [i32, i32, i32]
+    lib.moe_shared_ffn.restype = i32
+    lib.moe_shared_ffn.argtypes = [vp, vp, i32, i32, i32] + [vp] * 7 + [i32, vp, sz, vp]
     _lib = lib
     return lib
 

@@ -487,4 +487,186 @@ int moe_decode_ffn(const moe_ffn_desc *desc, const void *x, const int32_t *topk_
   return status_from(moe::launch_decode_mx4(a, static_cast<hipStream_t>(stream)));
 }
 
+int moe_route_select(const moe_select_desc *desc, const void *logits, const float *bias,
+                     int32_t *topk_ids, float *topk_w, moe_stream_t stream) {
+  if (!desc || !logits || !topk_ids || !topk_w) return MOE_EINVAL;
+  const moe_select_desc &d = *desc;
+  if (d.T < 1 || d.E < 1 || d.k < 1 || d.groups < 1 || d.top_groups < 1 ||
+      (long long)d.T * d.E >= (1LL << 31) || !(d.scale > -3.40282347e38f && d.scale < 3.40282347e38f))
+    return MOE_EINVAL;
+  const bool types = (d.logits_dtype == MOE_DT_BF16 || d.logits_dtype == MOE_DT_F32) &&
+                     (d.scores == MOE_SCORES_SOFTMAX || d.scores == MOE_SCORES_SIGMOID);
+  if (!types || d.E > MOE_MAX_EXPERTS || d.k > MOE_MAX_TOPK || d.groups > moe::kSelectMaxGroups ||
+      d.E % d.groups != 0 || d.top_groups > d.groups || d.k > d.top_groups * (d.E / d.groups) ||
+      (d.group_top != 1 && d.group_top != 2))
+    return MOE_EUNSUPPORTED;
+  if (misaligned(logits) || misaligned(topk_ids) || misaligned(topk_w) || (bias && misaligned(bias)))
+    return MOE_EALIGN;
+  moe::SelectArgs a{};
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = topk_ids;
+  a.gates = topk_w;
+  a.T = d.T;
+  a.E = d.E;
+  a.k = d.k;
+  a.groups = d.groups;
+  a.top_groups = d.top_groups;
+  a.group_top = d.group_top;
+  a.scale = d.scale;
+  a.f32 = d.logits_dtype == MOE_DT_F32;
+  a.softmax = d.scores == MOE_SCORES_SOFTMAX;
+  a.renormalise = d.renormalise != 0;
+  return status_from(moe::launch_route_select(a, num_cus_current_device() * 8,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t *q, float *s,
+                         moe_stream_t stream) {
+  if (!x || !q || !s || rows < 1 || cols < 1) return MOE_EINVAL;
+  if ((x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F32) || cols % 128 != 0) return MOE_EUNSUPPORTED;
+  if (misaligned(x) || misaligned(q) || misaligned(s)) return MOE_EALIGN;
+  return status_from(moe::launch_quant_blocks(x, x_dtype == MOE_DT_F32, (long long)rows * (cols / 128),
+                                              q, s, grid_cap_for_current_device(),
+                                              static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int matmul_status(int M, int N, int K) {
+  if (M < 1 || N < 1 || K < 1) return MOE_EINVAL;
+  // a workgroup to at least 32 rows by 16 columns, fewer than 2^31 of them
+  const long long most = (((long long)M + 31) / 32) * (((long long)N + 15) / 16);
+  if (K % 128 != 0 || K > moe::kMatmulMaxK || most >= (1LL << 31)) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// Codes and scales of M rows of K columns, from offset `at` on.
+struct CodesLayout {
+  size_t q, s, end;
+};
+CodesLayout codes_layout(size_t at, int M, int K) {
+  CodesLayout L{};
+  L.q = at;
+  L.s = L.q + align_up((size_t)M * K);
+  L.end = L.s + align_up((size_t)M * (K / 128) * 4);
+  return L;
+}
+
+struct SharedLayout {
+  CodesLayout x, h;
+  size_t g, u, total;
+};
+SharedLayout shared_layout(int T, int d, int f) {
+  SharedLayout L{};
+  L.x = codes_layout(0, T, d);
+  L.h = codes_layout(L.x.end, T, f);
+  L.g = L.h.end;
+  L.u = L.g + align_up((size_t)T * f * 4);
+  L.total = L.u + align_up((size_t)T * f * 4);
+  return L;
+}
+
+int shared_status(int T, int d, int f) {
+  if (T < 1 || d < 1 || f < 1) return MOE_EINVAL;
+  if (d % 128 != 0 || f % 128 != 0) return MOE_EUNSUPPORTED;
+  const int st = matmul_status(T, f, d);
+  return st != MOE_OK ? st : matmul_status(T, d, f);
+}
+
+moe::MatmulArgs matmul_args(const uint8_t *x, const float *xs, int M, int N, int K,
+                            const uint8_t *w, const float *ws, void *y, int y_dtype) {
+  moe::MatmulArgs a{};
+  a.x = x;
+  a.xs = xs;
+  a.w = w;
+  a.ws = ws;
+  a.y = y;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.f32 = y_dtype == MOE_DT_F32;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_matmul_fp8_workspace(int M, int N, int K) {
+  return matmul_status(M, N, K) == MOE_OK ? codes_layout(0, M, K).end : 0;
+}
+
+int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const uint8_t *w,
+                   const float *ws, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
+                   moe_stream_t stream) {
+  if (!x || !w || !ws || !y) return MOE_EINVAL;
+  const int st = matmul_status(M, N, K);
+  if (st != MOE_OK) return st;
+  if (y_dtype != MOE_DT_BF16 && y_dtype != MOE_DT_F32) return MOE_EUNSUPPORTED;
+  const void *ptrs[] = {x, xs, w, ws, y, workspace};
+  for (const void *p : ptrs)
+    if (p && misaligned(p)) return MOE_EALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const uint8_t *q = static_cast<const uint8_t *>(x);
+  if (!xs) {
+    const CodesLayout L = codes_layout(0, M, K);
+    if (!workspace || workspace_bytes < L.end) return MOE_EWORKSPACE;
+    char *base = static_cast<char *>(workspace);
+    uint8_t *to = reinterpret_cast<uint8_t *>(base + L.q);
+    float *scales = reinterpret_cast<float *>(base + L.s);
+    const hipError_t err = moe::launch_quant_blocks(x, false, (long long)M * (K / 128), to, scales,
+                                                    grid_cap_for_current_device(), s);
+    if (err != hipSuccess) return status_from(err);
+    q = to;
+    xs = scales;
+  }
+  return status_from(moe::launch_matmul_fp8(matmul_args(q, xs, M, N, K, w, ws, y, y_dtype), s));
+}
+
+size_t moe_shared_ffn_workspace(int T, int d, int f) {
+  return shared_status(T, d, f) == MOE_OK ? shared_layout(T, d, f).total : 0;
+}
+
+int moe_shared_ffn(const void *x, const float *xs, int T, int d, int f, const uint8_t *w_gate,
+                   const uint8_t *w_up, const uint8_t *w_down, const float *s_gate,
+                   const float *s_up, const float *s_down, void *out, int out_dtype,
+                   void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (!x || !w_gate || !w_up || !w_down || !s_gate || !s_up || !s_down || !out) return MOE_EINVAL;
+  const int st = shared_status(T, d, f);
+  if (st != MOE_OK) return st;
+  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32) return MOE_EUNSUPPORTED;
+  const void *ptrs[] = {x, xs, w_gate, w_up, w_down, s_gate, s_up, s_down, out, workspace};
+  for (const void *p : ptrs)
+    if (p && misaligned(p)) return MOE_EALIGN;
+  const SharedLayout L = shared_layout(T, d, f);
+  if (!workspace || workspace_bytes < L.total) return MOE_EWORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char *base = static_cast<char *>(workspace);
+  const int cap = grid_cap_for_current_device();
+  const uint8_t *q = static_cast<const uint8_t *>(x);
+  hipError_t err = hipSuccess;
+  if (!xs) {
+    uint8_t *to = reinterpret_cast<uint8_t *>(base + L.x.q);
+    float *scales = reinterpret_cast<float *>(base + L.x.s);
+    err = moe::launch_quant_blocks(x, false, (long long)T * (d / 128), to, scales, cap, s);
+    q = to;
+    xs = scales;
+  }
+  float *g = reinterpret_cast<float *>(base + L.g), *u = reinterpret_cast<float *>(base + L.u);
+  uint8_t *hq = reinterpret_cast<uint8_t *>(base + L.h.q);
+  float *hs = reinterpret_cast<float *>(base + L.h.s);
+  if (err == hipSuccess)
+    err = moe::launch_matmul_fp8(matmul_args(q, xs, T, f, d, w_gate, s_gate, g, MOE_DT_F32), s);
+  if (err == hipSuccess)
+    err = moe::launch_matmul_fp8(matmul_args(q, xs, T, f, d, w_up, s_up, u, MOE_DT_F32), s);
+  if (err == hipSuccess)
+    err = moe::launch_quant_swiglu(g, u, (long long)T * (f / 128), hq, hs, cap, s);
+  if (err == hipSuccess)
+    err = moe::launch_matmul_fp8(matmul_args(hq, hs, T, d, f, w_down, s_down, out, out_dtype), s);
+  return status_from(err);
+}
+
 }  // extern "C"

@@ -49,6 +49,40 @@ hipError_t launch_combine(const float *y, const int32_t *route_rows, const float
 hipError_t launch_route_topk(const float *logits, const float *bias, int T, int E, int k,
                              int32_t *ids, float *gates, int grid_cap, hipStream_t stream);
 
+// Selection of experts from router scores (route_select.hip).
+struct SelectArgs {
+  const void *logits;  // [T, E] fp32, or bf16 without f32
+  const float *bias;   // [E] or null
+  int32_t *ids;        // [T, k]
+  float *gates;        // [T, k]
+  int T, E, k, groups, top_groups, group_top;
+  float scale;
+  bool f32, softmax, renormalise;
+};
+constexpr int kSelectMaxGroups = 64;
+hipError_t launch_route_select(const SelectArgs &a, int grid_cap, hipStream_t stream);
+
+// E4M3 codes and scales of blocks of 128 elements (quant_blocks.hip), and the
+// same of silu(g) * u.
+hipError_t launch_quant_blocks(const void *x, bool f32, long long blocks, uint8_t *q, float *s,
+                               int grid_cap, hipStream_t stream);
+hipError_t launch_quant_swiglu(const float *g, const float *u, long long blocks, uint8_t *q,
+                               float *s, int grid_cap, hipStream_t stream);
+
+// Product of E4M3 rows and weights with block scales (matmul_fp8.hip).  Columns
+// are bounded so that 32-bit offsets reach the rows of a tile.
+constexpr int kMatmulMaxK = 1 << 20;
+struct MatmulArgs {
+  const uint8_t *x;  // [M, K]
+  const float *xs;   // [M, K / 128]
+  const uint8_t *w;  // [N, K]
+  const float *ws;   // [ceil(N / 128), K / 128]
+  void *y;           // [M, N] fp32, or bf16 without f32
+  int M, N, K;
+  bool f32;
+};
+hipError_t launch_matmul_fp8(const MatmulArgs &a, hipStream_t stream);
+
 int quant_max_cols();
 hipError_t launch_quant_rows(const uint16_t *x, int rows, const int32_t *rows_dev, int cols,
                              uint8_t *q, float *s, int grid_cap, hipStream_t stream);
