@@ -22,7 +22,7 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 HIP_SOURCES = ["route_topk.hip", "route_build.hip", "combine.hip", "quant.hip", "ffn_grouped.hip",
                "ffn_fp8.hip", "norm.hip", "ffn_mxfp4.hip", "decode_mxfp4.hip",
-               "route_select.hip", "quant_blocks.hip", "matmul_fp8.hip"]
+               "route_select.hip", "quant_blocks.hip", "matmul_fp8.hip", "matvec_fp8.hip"]
 HOST_SOURCES = ["api.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -557,15 +557,14 @@ CodesLayout codes_layout(size_t at, int M, int K) {
 
 struct SharedLayout {
   CodesLayout x, h;
-  size_t g, u, total;
+  size_t hf, total;  // h in fp32
 };
 SharedLayout shared_layout(int T, int d, int f) {
   SharedLayout L{};
   L.x = codes_layout(0, T, d);
   L.h = codes_layout(L.x.end, T, f);
-  L.g = L.h.end;
-  L.u = L.g + align_up((size_t)T * f * 4);
-  L.total = L.u + align_up((size_t)T * f * 4);
+  L.hf = L.h.end;
+  L.total = L.hf + align_up((size_t)T * f * 4);
   return L;
 }
 
@@ -576,19 +575,96 @@ int shared_status(int T, int d, int f) {
   return st != MOE_OK ? st : matmul_status(T, d, f);
 }
 
-moe::MatmulArgs matmul_args(const uint8_t *x, const float *xs, int M, int N, int K,
-                            const uint8_t *w, const float *ws, void *y, int y_dtype) {
+// A product of a call whose arguments are checked; without xs x is bf16, or fp32
+// with x_f32, and is quantised into `codes` (K columns' layout at `room`) where the
+// kernel does not do so itself.
+struct Product {
+  const void *x;
+  const float *xs;
+  bool x_f32;
+  int M, N, K;
+  char *room;
+  CodesLayout codes;
+};
+
+hipError_t quantise(Product *p, hipStream_t s) {
+  uint8_t *q = reinterpret_cast<uint8_t *>(p->room + p->codes.q);
+  float *scales = reinterpret_cast<float *>(p->room + p->codes.s);
+  const hipError_t err = moe::launch_quant_blocks(p->x, p->x_f32, (long long)p->M * (p->K / 128), q,
+                                                  scales, grid_cap_for_current_device(), s);
+  p->x = q;
+  p->xs = scales;
+  return err;
+}
+
+moe::MatmulArgs matmul_args(const Product &p, const uint8_t *w, const float *ws) {
   moe::MatmulArgs a{};
-  a.x = x;
-  a.xs = xs;
+  a.x = static_cast<const uint8_t *>(p.x);
+  a.xs = p.xs;
   a.w = w;
   a.ws = ws;
-  a.y = y;
-  a.M = M;
-  a.N = N;
-  a.K = K;
-  a.f32 = y_dtype == MOE_DT_F32;
+  a.M = p.M;
+  a.N = p.N;
+  a.K = p.K;
   return a;
+}
+
+moe::MatvecArgs matvec_args(const Product &p, const uint8_t *w, const float *ws, void *y, bool f32) {
+  moe::MatvecArgs a{};
+  a.x = p.x;
+  a.xs = p.xs;
+  a.w0 = w;
+  a.s0 = ws;
+  a.y = y;
+  a.M = p.M;
+  a.N = p.N;
+  a.K = p.K;
+  a.x_f32 = p.x_f32;
+  a.f32 = f32;
+  return a;
+}
+
+// y = x w
+hipError_t product(Product p, const uint8_t *w, const float *ws, void *y, bool f32, hipStream_t s) {
+  const bool few = moe::product_is_matvec(p.M, p.N, p.K, false, p.xs != nullptr);
+  hipError_t err = hipSuccess;
+  if (!p.xs && !(few && moe::matvec_quantises(p.M, p.K))) err = quantise(&p, s);
+  if (err != hipSuccess) return err;
+  if (few) return moe::launch_matvec_fp8(matvec_args(p, w, ws, y, f32), s);
+  moe::MatmulArgs a = matmul_args(p, w, ws);
+  a.y = y;
+  a.f32 = f32;
+  return moe::launch_matmul_fp8(a, s);
+}
+
+// down's rows = silu(x w0) * (x w1), in fp32 in h or as codes in down's room.
+hipError_t gate_up(Product p, const uint8_t *w0, const float *s0, const uint8_t *w1,
+                   const float *s1, float *h, Product *down, hipStream_t s) {
+  const bool few = moe::product_is_matvec(p.M, p.N, p.K, true, p.xs != nullptr);
+  hipError_t err = hipSuccess;
+  if (!p.xs && !(few && moe::matvec_quantises(p.M, p.K))) err = quantise(&p, s);
+  if (err != hipSuccess) return err;
+  down->x = h;
+  down->xs = nullptr;
+  down->x_f32 = true;
+  if (few) {
+    moe::MatvecArgs a = matvec_args(p, w0, s0, h, true);
+    a.w1 = w1;
+    a.s1 = s1;
+    return moe::launch_matvec_fp8(a, s);
+  }
+  moe::MatmulArgs a = matmul_args(p, w0, s0);
+  a.w1 = w1;
+  a.ws1 = s1;
+  if (moe::gateup_quantises(p.M, p.N, p.K)) {
+    a.hq = reinterpret_cast<uint8_t *>(down->room + down->codes.q);
+    a.hs = reinterpret_cast<float *>(down->room + down->codes.s);
+    down->x = a.hq;
+    down->xs = a.hs;
+  } else {
+    a.y = h;
+  }
+  return moe::launch_gateup_fp8(a, s);
 }
 
 }  // namespace
@@ -609,21 +685,11 @@ int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const ui
   const void *ptrs[] = {x, xs, w, ws, y, workspace};
   for (const void *p : ptrs)
     if (p && misaligned(p)) return MOE_EALIGN;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const uint8_t *q = static_cast<const uint8_t *>(x);
-  if (!xs) {
-    const CodesLayout L = codes_layout(0, M, K);
-    if (!workspace || workspace_bytes < L.end) return MOE_EWORKSPACE;
-    char *base = static_cast<char *>(workspace);
-    uint8_t *to = reinterpret_cast<uint8_t *>(base + L.q);
-    float *scales = reinterpret_cast<float *>(base + L.s);
-    const hipError_t err = moe::launch_quant_blocks(x, false, (long long)M * (K / 128), to, scales,
-                                                    grid_cap_for_current_device(), s);
-    if (err != hipSuccess) return status_from(err);
-    q = to;
-    xs = scales;
-  }
-  return status_from(moe::launch_matmul_fp8(matmul_args(q, xs, M, N, K, w, ws, y, y_dtype), s));
+  const CodesLayout L = codes_layout(0, M, K);
+  if (!xs && (!workspace || workspace_bytes < L.end)) return MOE_EWORKSPACE;
+  const Product p = {x, xs, false, M, N, K, static_cast<char *>(workspace), L};
+  return status_from(product(p, w, ws, y, y_dtype == MOE_DT_F32,
+                             static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_shared_ffn_workspace(int T, int d, int f) {
@@ -645,27 +711,11 @@ int moe_shared_ffn(const void *x, const float *xs, int T, int d, int f, const ui
   if (!workspace || workspace_bytes < L.total) return MOE_EWORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char *base = static_cast<char *>(workspace);
-  const int cap = grid_cap_for_current_device();
-  const uint8_t *q = static_cast<const uint8_t *>(x);
-  hipError_t err = hipSuccess;
-  if (!xs) {
-    uint8_t *to = reinterpret_cast<uint8_t *>(base + L.x.q);
-    float *scales = reinterpret_cast<float *>(base + L.x.s);
-    err = moe::launch_quant_blocks(x, false, (long long)T * (d / 128), to, scales, cap, s);
-    q = to;
-    xs = scales;
-  }
-  float *g = reinterpret_cast<float *>(base + L.g), *u = reinterpret_cast<float *>(base + L.u);
-  uint8_t *hq = reinterpret_cast<uint8_t *>(base + L.h.q);
-  float *hs = reinterpret_cast<float *>(base + L.h.s);
-  if (err == hipSuccess)
-    err = moe::launch_matmul_fp8(matmul_args(q, xs, T, f, d, w_gate, s_gate, g, MOE_DT_F32), s);
-  if (err == hipSuccess)
-    err = moe::launch_matmul_fp8(matmul_args(q, xs, T, f, d, w_up, s_up, u, MOE_DT_F32), s);
-  if (err == hipSuccess)
-    err = moe::launch_quant_swiglu(g, u, (long long)T * (f / 128), hq, hs, cap, s);
-  if (err == hipSuccess)
-    err = moe::launch_matmul_fp8(matmul_args(hq, hs, T, d, f, w_down, s_down, out, out_dtype), s);
+  const Product up = {x, xs, false, T, f, d, base, L.x};
+  Product down = {nullptr, nullptr, true, T, d, f, base, L.h};
+  hipError_t err = gate_up(up, w_gate, s_gate, w_up, s_up, reinterpret_cast<float *>(base + L.hf),
+                           &down, s);
+  if (err == hipSuccess) err = product(down, w_down, s_down, out, out_dtype == MOE_DT_F32, s);
   return status_from(err);
 }
 

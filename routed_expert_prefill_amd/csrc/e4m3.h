@@ -100,4 +100,57 @@ __device__ __forceinline__ float quant_rcp(float sc, bool *exact) {
   return r;
 }
 
+// ---- blocks of 128 columns, a scale for each ----
+
+// amax / 448 of a block.  fp32 rows may be so small that the quotient rounds to
+// zero: the smallest number then, so that codes stand for multiples of something.
+__device__ __forceinline__ float qb_scale(float amax) {
+  return amax == 0.0f ? 1.0f : fmaxf(amax / 448.0f, __uint_as_float(1u));
+}
+
+constexpr int kQbLanes = 16;  // lanes to a block, eight consecutive elements each
+
+enum : int { kQbBf16 = 0, kQbF32 = 1 };
+
+// Eight elements from element `at` of rows of the given kind.
+template <int KIND>
+__device__ __forceinline__ void qb_load(const void *x, size_t at, float (&v)[8]) {
+  if constexpr (KIND == kQbBf16) {
+    const i32x4 raw = *reinterpret_cast<const i32x4 *>(static_cast<const uint16_t *>(x) + at);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      v[2 * w] = __uint_as_float((uint32_t)raw[w] << 16);
+      v[2 * w + 1] = __uint_as_float((uint32_t)raw[w] & 0xffff0000u);
+    }
+  } else {
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(static_cast<const float *>(x) + at);
+    const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = lo[e];
+      v[4 + e] = hi[e];
+    }
+  }
+}
+
+// Codes of the eight elements that a lane of a block's sixteen holds, and the
+// block's scale.  All sixteen lanes call it together.
+__device__ __forceinline__ uint2 qb_codes(const float (&v)[8], float *scale) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+#pragma unroll
+  for (int m = kQbLanes / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+  const bool zero = amax == 0.0f;
+  const float sc = qb_scale(amax);
+  bool exact;
+  const float rcp = quant_rcp(sc, &exact);
+  const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+  uint2 out;
+  out.x = quant_e4m3_x4(lo, sc, rcp, exact, zero);
+  out.y = quant_e4m3_x4(hi, sc, rcp, exact, zero);
+  *scale = sc;
+  return out;
+}
+
 }  // namespace moe

@@ -62,12 +62,9 @@ struct SelectArgs {
 constexpr int kSelectMaxGroups = 64;
 hipError_t launch_route_select(const SelectArgs &a, int grid_cap, hipStream_t stream);
 
-// E4M3 codes and scales of blocks of 128 elements (quant_blocks.hip), and the
-// same of silu(g) * u.
+// E4M3 codes and scales of blocks of 128 elements (quant_blocks.hip).
 hipError_t launch_quant_blocks(const void *x, bool f32, long long blocks, uint8_t *q, float *s,
                                int grid_cap, hipStream_t stream);
-hipError_t launch_quant_swiglu(const float *g, const float *u, long long blocks, uint8_t *q,
-                               float *s, int grid_cap, hipStream_t stream);
 
 // Product of E4M3 rows and weights with block scales (matmul_fp8.hip).  Columns
 // are bounded so that 32-bit offsets reach the rows of a tile.
@@ -80,8 +77,34 @@ struct MatmulArgs {
   void *y;           // [M, N] fp32, or bf16 without f32
   int M, N, K;
   bool f32;
+  // launch_gateup_fp8: the second matrix (w is gate, w1 up), and codes and scales of h
+  const uint8_t *w1;
+  const float *ws1;
+  uint8_t *hq;  // [M, N]
+  float *hs;    // [M, N / 128]
 };
 hipError_t launch_matmul_fp8(const MatmulArgs &a, hipStream_t stream);
+// h = silu(x w) * (x w1): with gateup_quantises(M, N) codes and scales in hq and hs,
+// otherwise fp32 in y.  N is a multiple of 128.
+bool gateup_quantises(int M, int N, int K);
+hipError_t launch_gateup_fp8(const MatmulArgs &a, hipStream_t stream);
+
+// The same for at most kMatvecRows rows (matvec_fp8.hip).  With w1 and s1 (same
+// sizes as w0, s0; N a multiple of 8): y = silu(x w0) * (x w1) in fp32.
+constexpr int kMatvecRows = 16;
+struct MatvecArgs {
+  const void *x;    // codes [M, K] with xs, else bf16 or (x_f32) fp32, quantised on the way
+  const float *xs;  // [M, K / 128] or null, where matvec_quantises(M, K)
+  const uint8_t *w0, *w1;
+  const float *s0, *s1;
+  void *y;  // [M, N] fp32, or bf16 without f32
+  int M, N, K;
+  bool x_f32, f32;
+};
+bool matvec_quantises(int M, int K);
+// Whether the matvec kernel is the faster one; codes: x is quantised already.
+bool product_is_matvec(int M, int N, int K, bool gateup, bool codes);
+hipError_t launch_matvec_fp8(const MatvecArgs &a, hipStream_t stream);
 
 int quant_max_cols();
 hipError_t launch_quant_rows(const uint16_t *x, int rows, const int32_t *rows_dev, int cols,
