@@ -517,8 +517,7 @@ int moe_route_select(const moe_select_desc *desc, const void *logits, const floa
   a.f32 = d.logits_dtype == MOE_DT_F32;
   a.softmax = d.scores == MOE_SCORES_SOFTMAX;
   a.renormalise = d.renormalise != 0;
-  return status_from(moe::launch_route_select(a, num_cus_current_device() * 8,
-                                              static_cast<hipStream_t>(stream)));
+  return status_from(moe::launch_route_select(a, static_cast<hipStream_t>(stream)));
 }
 
 int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t *q, float *s,

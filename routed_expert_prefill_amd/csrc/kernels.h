@@ -60,7 +60,7 @@ struct SelectArgs {
   bool f32, softmax, renormalise;
 };
 constexpr int kSelectMaxGroups = 64;
-hipError_t launch_route_select(const SelectArgs &a, int grid_cap, hipStream_t stream);
+hipError_t launch_route_select(const SelectArgs &a, hipStream_t stream);
 
 // E4M3 codes and scales of blocks of 128 elements (quant_blocks.hip).
 hipError_t launch_quant_blocks(const void *x, bool f32, long long blocks, uint8_t *q, float *s,

@@ -7,11 +7,20 @@
 //   c = -inf outside the top_groups groups of largest value
 //   ids: the k largest c, descending;  gates: s of the chosen, over their sum, times scale
 //
-// Equal values go to the lower index, NaN comes before every number.  All of it
-// is taken in fp64, so that neighbours in the order stand in the order of the
-// formulas; a gate is rounded once.
+// Equal values go to the lower index, NaN comes before every number.  The order is
+// that of choices in fp64, a gate is formed in fp64 and rounded once.
 //
-// One wave per token: lane l holds experts l, l + 64, l + 128, l + 192.
+// One wave per token.  Choices are first taken in fp32, with a bound on how far they
+// may be off; where every pair of neighbours that decides something (the chosen ones,
+// the first one left out, the last group kept and the first one dropped) is further
+// apart than that, the order is the one of fp64.  Otherwise, for about one token in two
+// thousand of ordinary logits and for ties, the wave does the token again in fp64; and
+// for infinities, NaN and too few experts in service a third time, with those cases'
+// rules.  (A kernel waits for its slowest wave: with the third form for every such
+// token 8192 tokens of 256 experts in groups took 21.0 us.)
+//
+// Bound by instructions, about 450 to a token: 8192 tokens of 256 experts read 8.4 MB,
+// 1.7 us at a copy's rate.
 #include <math.h>
 
 #include "kernels.h"
@@ -20,6 +29,8 @@ namespace moe {
 
 constexpr int kSelThreads = 256;
 constexpr int kSelWaves = kSelThreads / kWave;
+// Workgroups in x: a grid takes fewer than 2^32 threads in each dimension.
+constexpr unsigned kSelLine = 1u << 22;
 constexpr int kSelPerLane = 4;  // 64 lanes x 4 >= 256 experts
 
 // v as a number that orders as the choice does: NaN first.  Above 0.
@@ -35,130 +46,405 @@ __device__ __forceinline__ double sel_wave_sum(double v) {
   return v;
 }
 
-__global__ __launch_bounds__(kSelThreads) void route_select_kernel(SelectArgs a) {
-  __shared__ double choice[kSelWaves][kSelPerLane * kWave];
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
+// Any token, in fp64: lane l holds experts l, l + 64, l + 128, l + 192.
+__device__ __forceinline__ void select_any(const SelectArgs &a, long long t, double *choice) {
+  const int lane = lane_id();
   const int per = a.E / a.groups;
-  const long long nwaves = (long long)gridDim.x * kSelWaves;
-  for (long long t = (long long)blockIdx.x * kSelWaves + wave; t < a.T; t += nwaves) {
-    double s[kSelPerLane], c[kSelPerLane];
-    double top = -INFINITY;
+  double s[kSelPerLane], c[kSelPerLane];
+  double top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kSelPerLane; ++i) {
-      const int e = lane + kWave * i;
-      s[i] = -INFINITY;  // no expert, as one out of service
-      if (e < a.E) {
-        const size_t at = (size_t)t * a.E + e;
-        s[i] = a.f32 ? (double)static_cast<const float *>(a.logits)[at]
-                     : (double)bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[at]);
-      }
-      top = fmax(top, s[i]);
+  for (int i = 0; i < kSelPerLane; ++i) {
+    const int e = lane + kWave * i;
+    s[i] = -INFINITY;  // no expert, as one out of service
+    if (e < a.E) {
+      const size_t at = (size_t)t * a.E + e;
+      s[i] = a.f32 ? (double)static_cast<const float *>(a.logits)[at]
+                   : (double)bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[at]);
     }
-    if (a.softmax) {
-#pragma unroll
-      for (int m = kWave / 2; m > 0; m >>= 1) top = fmax(top, __shfl_xor(top, m));
-    }
-    double sum = 0.0;
-    bool gone[kSelPerLane];
-#pragma unroll
-    for (int i = 0; i < kSelPerLane; ++i) {
-      gone[i] = s[i] == -INFINITY;
-      if (gone[i])
-        s[i] = 0.0;
-      else
-        s[i] = a.softmax ? exp(s[i] - top) : 1.0 / (1.0 + exp(-s[i]));
-      sum += s[i];
-    }
-    if (a.softmax) {
-      sum = sel_wave_sum(sum);
-#pragma unroll
-      for (int i = 0; i < kSelPerLane; ++i)
-        if (!gone[i]) s[i] /= sum;
-    }
-#pragma unroll
-    for (int i = 0; i < kSelPerLane; ++i) {
-      const int e = lane + kWave * i;
-      c[i] = gone[i] ? -INFINITY : s[i] + (a.bias ? (double)a.bias[e] : 0.0);
-    }
-    if (a.groups > 1) {
-#pragma unroll
-      for (int i = 0; i < kSelPerLane; ++i) choice[wave][lane + kWave * i] = c[i];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      // lane g: the value of group g, its two largest choices in order of keys
-      double v = 0.0;
-      if (lane < a.groups) {
-        double one = -INFINITY, two = -INFINITY;
-        for (int i = 0; i < per; ++i) {
-          const double x = choice[wave][lane * per + i];
-          if (sel_key(x) > sel_key(one)) {
-            two = one;
-            one = x;
-          } else if (sel_key(x) > sel_key(two)) {
-            two = x;
-          }
-        }
-        v = a.group_top == 1 || two == -INFINITY ? one : one + two;
-      }
-      const unsigned long long mine = sel_key(v);
-      int ahead = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const unsigned long long other = __shfl(mine, g);
-        ahead += other > mine || (other == mine && g < lane);
-      }
-      const unsigned long long kept = __ballot(lane < a.groups && ahead < a.top_groups);
-#pragma unroll
-      for (int i = 0; i < kSelPerLane; ++i) {
-        const int e = lane + kWave * i;
-        if (e < a.E && !((kept >> (e / per)) & 1)) c[i] = -INFINITY;
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // read before the next token's
-    }
-    unsigned long long key[kSelPerLane];
-#pragma unroll
-    for (int i = 0; i < kSelPerLane; ++i) key[i] = lane + kWave * i < a.E ? sel_key(c[i]) : 0;
-    double gate = 0.0;  // lane j keeps the j-th
-    for (int j = 0; j < a.k; ++j) {
-      unsigned long long bk = 0;
-      int bi = 0x7fffffff;
-      double bs = 0.0;
-#pragma unroll
-      for (int i = 0; i < kSelPerLane; ++i) {
-        if (key[i] > bk) {
-          bk = key[i];
-          bi = lane + kWave * i;
-          bs = c[i] == -INFINITY ? 0.0 : s[i];
-        }
-      }
-#pragma unroll
-      for (int m = 1; m < kWave; m <<= 1) {
-        const unsigned long long ok = __shfl_xor(bk, m);
-        const int oi = __shfl_xor(bi, m);
-        const double os = __shfl_xor(bs, m);
-        if (ok > bk || (ok == bk && oi < bi)) {
-          bk = ok;
-          bi = oi;
-          bs = os;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kSelPerLane; ++i)
-        if (lane + kWave * i == bi) key[i] = 0;
-      if (lane == j) gate = bs;
-      if (lane == 0) a.ids[(size_t)t * a.k + j] = bi;
-    }
-    if (a.renormalise) {
-      double total = 0.0;
-      for (int j = 0; j < a.k; ++j) total += __shfl(gate, j);
-      gate = total == 0.0 ? 0.0 : gate / total;
-    }
-    if (lane < a.k) a.gates[(size_t)t * a.k + lane] = (float)(gate * (double)a.scale);
+    top = fmax(top, s[i]);
   }
+  if (a.softmax) {
+#pragma unroll
+    for (int m = kWave / 2; m > 0; m >>= 1) top = fmax(top, __shfl_xor(top, m));
+  }
+  double sum = 0.0;
+  bool gone[kSelPerLane];
+#pragma unroll
+  for (int i = 0; i < kSelPerLane; ++i) {
+    gone[i] = s[i] == -INFINITY;
+    if (gone[i])
+      s[i] = 0.0;
+    else
+      s[i] = a.softmax ? exp(s[i] - top) : 1.0 / (1.0 + exp(-s[i]));
+    sum += s[i];
+  }
+  if (a.softmax) {
+    sum = sel_wave_sum(sum);
+#pragma unroll
+    for (int i = 0; i < kSelPerLane; ++i)
+      if (!gone[i]) s[i] /= sum;
+  }
+#pragma unroll
+  for (int i = 0; i < kSelPerLane; ++i) {
+    const int e = lane + kWave * i;
+    c[i] = gone[i] ? -INFINITY : s[i] + (a.bias ? (double)a.bias[e] : 0.0);
+  }
+  if (a.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < kSelPerLane; ++i) choice[lane + kWave * i] = c[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // lane g: the value of group g, its two largest choices in order of keys
+    double v = 0.0;
+    if (lane < a.groups) {
+      double one = -INFINITY, two = -INFINITY;
+      for (int i = 0; i < per; ++i) {
+        const double x = choice[lane * per + i];
+        if (sel_key(x) > sel_key(one)) {
+          two = one;
+          one = x;
+        } else if (sel_key(x) > sel_key(two)) {
+          two = x;
+        }
+      }
+      v = a.group_top == 1 || two == -INFINITY ? one : one + two;
+    }
+    const unsigned long long mine = sel_key(v);
+    int ahead = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const unsigned long long other = __shfl(mine, g);
+      ahead += other > mine || (other == mine && g < lane);
+    }
+    const unsigned long long kept = __ballot(lane < a.groups && ahead < a.top_groups);
+#pragma unroll
+    for (int i = 0; i < kSelPerLane; ++i) {
+      const int e = lane + kWave * i;
+      if (e < a.E && !((kept >> (e / per)) & 1)) c[i] = -INFINITY;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // read before the next token's
+  }
+  unsigned long long key[kSelPerLane];
+#pragma unroll
+  for (int i = 0; i < kSelPerLane; ++i) key[i] = lane + kWave * i < a.E ? sel_key(c[i]) : 0;
+  double gate = 0.0;  // lane j keeps the j-th
+  for (int j = 0; j < a.k; ++j) {
+    unsigned long long bk = 0;
+    int bi = 0x7fffffff;
+    double bs = 0.0;
+#pragma unroll
+    for (int i = 0; i < kSelPerLane; ++i) {
+      if (key[i] > bk) {
+        bk = key[i];
+        bi = lane + kWave * i;
+        bs = c[i] == -INFINITY ? 0.0 : s[i];
+      }
+    }
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1) {
+      const unsigned long long ok = __shfl_xor(bk, m);
+      const int oi = __shfl_xor(bi, m);
+      const double os = __shfl_xor(bs, m);
+      if (ok > bk || (ok == bk && oi < bi)) {
+        bk = ok;
+        bi = oi;
+        bs = os;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSelPerLane; ++i)
+      if (lane + kWave * i == bi) key[i] = 0;
+    if (lane == j) gate = bs;
+    if (lane == 0) a.ids[(size_t)t * a.k + j] = bi;
+  }
+  if (a.renormalise) {
+    double total = 0.0;
+    for (int j = 0; j < a.k; ++j) total += __shfl(gate, j);
+    gate = total == 0.0 ? 0.0 : gate / total;
+  }
+  if (lane < a.k) a.gates[(size_t)t * a.k + lane] = (float)(gate * (double)a.scale);
 }
 
-hipError_t launch_route_select(const SelectArgs &a, int grid_cap, hipStream_t stream) {
-  const long long want = ((long long)a.T + kSelWaves - 1) / kSelWaves;
-  const int grid = (int)(want < grid_cap ? want : grid_cap);
-  return launch(route_select_kernel, dim3(grid), dim3(kSelThreads), stream, a);
+// v as the lane that CTRL names has it; lanes of rows outside ROWS keep their own.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float sel_dpp(float v) {
+  const int b = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double sel_dpp(double v) {
+  const int lo = __double2loint(v), hi = __double2hiint(v);
+  return __hiloint2double(__builtin_amdgcn_update_dpp(hi, hi, CTRL, ROWS, 0xf, false),
+                          __builtin_amdgcn_update_dpp(lo, lo, CTRL, ROWS, 0xf, false));
+}
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;  // within 16 lanes
+constexpr int kBcast15 = 0x142, kBcast31 = 0x143;  // lane 15 (31) to the 16 (32) lanes behind
+
+__device__ __forceinline__ float sel_lane(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double sel_lane(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+__device__ __forceinline__ float sel_max(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double sel_max(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float sel_min(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double sel_min(double a, double b) { return fmin(a, b); }
+
+// The largest of the wave's values, in scalar registers.
+template <typename R>
+__device__ __forceinline__ R sel_wave_max(R v) {
+  v = sel_max(v, sel_dpp<kXor1>(v));
+  v = sel_max(v, sel_dpp<kXor2>(v));
+  v = sel_max(v, sel_dpp<kHalfMirror>(v));
+  v = sel_max(v, sel_dpp<kMirror>(v));
+  v = sel_max(v, sel_dpp<kBcast15, 0xa>(v));
+  v = sel_max(v, sel_dpp<kBcast31, 0xc>(v));
+  return sel_lane(v, kWave - 1);
+}
+
+__device__ __forceinline__ float sel_wave_sum(float v) {
+#pragma unroll
+  for (int m = kWave / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// The two largest of 2 * 2 values in descending pairs.
+template <typename R>
+__device__ __forceinline__ void sel_merge(R &one, R &two, R o1, R o2) {
+  two = sel_max(sel_min(one, o1), sel_max(two, o2));
+  one = sel_max(one, o1);
+}
+
+// A token with choices in fp32 or fp64: lane l holds experts 4 l .. 4 l + 3.  False,
+// and nothing written, where fp32 does not tell the order of fp64, and for NaN,
+// infinities and a token with too few experts in service.
+//
+// How far an fp32 score may be off, with an exponential and 1 / x of a step (2^-23)
+// each and the argument's rounding, a half step of |z|: a sigmoid by 2^-23 (s (1 - s)
+// (|z| / 2 + 1) + 1.5 s), below 2^-22; a softmax score by 27 x 2^-24 of the largest
+// (its argument s |d| / top <= 0.37, the sum of 256 with its own arguments' 5.5), below
+// 2^-19.  The bias' addition rounds once more.
+template <bool SOFTMAX, typename R>
+__device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R *choice) {
+  constexpr bool F64 = sizeof(R) == 8;
+  constexpr R kNone = -INFINITY;
+  const int lane = lane_id();
+  float z[4];
+  const size_t row = (size_t)t * a.E;
+  const int e0 = lane * 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = -INFINITY;
+  if (a.E % 4 == 0) {
+    if (e0 < a.E) {
+      if (a.f32) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.logits) + row + e0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = v[i];
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.logits) + row + e0);
+        z[0] = __uint_as_float(v.x << 16);
+        z[1] = __uint_as_float(v.x & 0xffff0000u);
+        z[2] = __uint_as_float(v.y << 16);
+        z[3] = __uint_as_float(v.y & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e0 + i < a.E)
+        z[i] = a.f32 ? static_cast<const float *>(a.logits)[row + e0 + i]
+                     : bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[row + e0 + i]);
+  }
+  R x[4];
+  float top = 0.f, off = 0x1p-22f, most = 1.f;
+  double sum = 0.0;  // fp64 softmax
+  if (SOFTMAX) {
+    top = sel_wave_max(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+    R part = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F64)
+        x[i] = exp((double)z[i] - (double)top);
+      else
+        x[i] = __expf(z[i] - top);  // 0 for -inf
+      part += x[i];
+    }
+    if constexpr (F64) {
+      sum = sel_wave_sum(part);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] /= sum;
+    } else {
+      most = __builtin_amdgcn_rcpf(sel_wave_sum(part));
+      off = most * 0x1p-19f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] *= most;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F64)
+        x[i] = 1.0 / (1.0 + exp(-(double)z[i]));
+      else
+        x[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));
+    }
+  }
+  if (a.bias) {
+    float large = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e0 + i < a.E) x[i] += (R)a.bias[e0 + i];
+      if (!F64 && z[i] != -INFINITY) large = fmaxf(large, fabsf((float)x[i]));
+    }
+    if (!F64) most = sel_wave_max(large);
+  }
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    odd = odd || !(z[i] < INFINITY) || !(x[i] < (R)INFINITY);
+    if (z[i] == -INFINITY) x[i] = kNone;
+  }
+  if (__any(odd)) return false;
+  const R apart = F64 ? 0 : 2.0f * off + most * 0x1p-23f;
+
+  // this lane's choices in descending order, equal ones with the lower index first;
+  // their places among the four packed alike
+  uint32_t place = 0x03020100u;
+  auto sort2 = [&](int i, int j) {
+    const uint32_t pi = place >> (8 * i) & 0xff, pj = place >> (8 * j) & 0xff;
+    const bool swap = x[j] > x[i] || (F64 && x[j] == x[i] && pj < pi);
+    const R hi = swap ? x[j] : x[i], lo = swap ? x[i] : x[j];
+    x[i] = hi;
+    x[j] = lo;
+    place ^= swap ? (pi ^ pj) << (8 * i) | (pi ^ pj) << (8 * j) : 0u;
+  };
+  auto sort4 = [&]() {
+    sort2(0, 1);
+    sort2(2, 3);
+    sort2(0, 2);
+    sort2(1, 3);
+    sort2(1, 2);
+  };
+  sort4();
+
+  if (a.groups > 1) {
+    const int per = a.E / a.groups, lanes = per / 4;
+    const bool runs = per % 4 == 0 && (lanes & (lanes - 1)) == 0;  // of 1, 2, 4 .. 32 lanes
+    R one = x[0], two = x[1];
+    const int group = runs ? lane / lanes : lane;  // that this lane has the value of
+    if (runs) {
+      if (lanes >= 2) sel_merge(one, two, sel_dpp<kXor1>(one), sel_dpp<kXor1>(two));
+      if (lanes >= 4) sel_merge(one, two, sel_dpp<kXor2>(one), sel_dpp<kXor2>(two));
+      if (lanes >= 8) sel_merge(one, two, sel_dpp<kHalfMirror>(one), sel_dpp<kHalfMirror>(two));
+      if (lanes >= 16) sel_merge(one, two, sel_dpp<kMirror>(one), sel_dpp<kMirror>(two));
+      if (lanes >= 32) sel_merge(one, two, (R)__shfl_xor(one, 16), (R)__shfl_xor(two, 16));
+    } else {
+      // lane g looks through group g
+#pragma unroll
+      for (int i = 0; i < 4; ++i) choice[e0 + (place >> (8 * i) & 0xff)] = x[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      one = two = kNone;
+      if (lane < a.groups)
+        for (int i = 0; i < per; ++i) sel_merge(one, two, choice[lane * per + i], kNone);
+    }
+    const R value = a.group_top == 1 || two == kNone ? one : one + two;
+    int ahead = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const R other = sel_lane(value, runs ? g * lanes : g);
+      ahead += other > value || (other == value && g < group);
+    }
+    const bool is = group < a.groups, keep = is && ahead < a.top_groups;
+    if (!F64 && a.top_groups < a.groups) {
+      const R low = -sel_wave_max(keep ? -value : kNone);
+      const R high = sel_wave_max(is && !keep ? value : kNone);
+      if (!(low - high > 2 * apart)) return false;
+    }
+    if (runs) {
+      if (!keep) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = kNone;
+      }
+    } else {
+      const unsigned long long kept = __ballot(keep);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + (int)(place >> (8 * i) & 0xff);
+        if (e >= a.E || !((kept >> (e / per)) & 1)) x[i] = kNone;
+      }
+      sort4();
+    }
+  }
+
+  bool sure = true;
+  R before = INFINITY;
+  int id = 0;  // lane j keeps the j-th
+  for (int j = 0; j <= a.k; ++j) {
+    if (F64 && j == a.k) break;
+    const R best = sel_wave_max(x[0]);
+    sure = sure && (F64 ? best != kNone : before - best > apart);
+    before = best;
+    if (j == a.k) break;
+    const int from = __ffsll(__ballot(x[0] == best)) - 1;
+    const int e = from * 4 + (__builtin_amdgcn_readlane((int)place, from) & 0xff);
+    if (lane == j) id = e;
+    if (lane == from) {
+      x[0] = x[1];
+      x[1] = x[2];
+      x[2] = x[3];
+      x[3] = kNone;
+      place >>= 8;
+    }
+  }
+  if (!sure) return false;
+
+  // gates, in fp64 from the logits of the chosen
+  double gate = 0.0;
+  if (lane < a.k) {
+    const double v = a.f32 ? (double)static_cast<const float *>(a.logits)[row + id]
+                           : (double)bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[row + id]);
+    gate = SOFTMAX ? exp(v - (double)top) : 1.0 / (1.0 + exp(-v));
+  }
+  if (a.renormalise) {  // at most 16: the first 16 lanes
+    double total = gate;
+    total += sel_dpp<kXor1>(total);
+    total += sel_dpp<kXor2>(total);
+    total += sel_dpp<kHalfMirror>(total);
+    total += sel_dpp<kMirror>(total);
+    gate = total == 0.0 ? 0.0 : gate / total;
+  } else if (SOFTMAX) {
+    if (!F64) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += exp((double)z[i] - (double)top);
+      sum = sel_wave_sum(sum);
+    }
+    gate /= sum;
+  }
+  if (lane < a.k) {
+    a.ids[(size_t)t * a.k + lane] = id;
+    a.gates[(size_t)t * a.k + lane] = (float)(gate * (double)a.scale);
+  }
+  return true;
+}
+
+// (No loop over tokens: the constants of the fp64 exponentials would be kept across
+// it, in more scalar registers than there are.)
+template <bool SOFTMAX>
+__global__ __launch_bounds__(kSelThreads) void route_select_kernel(SelectArgs a) {
+  __shared__ double choice[kSelWaves][kSelPerLane * kWave];
+  const int wave = threadIdx.x / kWave;
+  // the last line of workgroups may end past the tokens
+  const long long t = ((long long)blockIdx.y * kSelLine + blockIdx.x) * kSelWaves + wave;
+  if (t >= a.T) return;
+  if (select_fast<SOFTMAX, float>(a, t, reinterpret_cast<float *>(choice[wave]))) return;
+  if (select_fast<SOFTMAX, double>(a, t, choice[wave])) return;
+  select_any(a, t, choice[wave]);
+}
+
+hipError_t launch_route_select(const SelectArgs &a, hipStream_t stream) {
+  const unsigned blocks = ((unsigned)a.T + kSelWaves - 1) / kSelWaves;
+  const dim3 grid(blocks < kSelLine ? blocks : kSelLine, (blocks + kSelLine - 1) / kSelLine),
+      block(kSelThreads);
+  if (a.softmax) return launch(route_select_kernel<true>, grid, block, stream, a);
+  return launch(route_select_kernel<false>, grid, block, stream, a);
 }
 
 }  // namespace moe
