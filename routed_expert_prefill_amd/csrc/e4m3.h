@@ -133,22 +133,72 @@ __device__ __forceinline__ void qb_load(const void *x, size_t at, float (&v)[8])
   }
 }
 
+// Correctly rounded quotients by fused multiply-adds, where `rcp` is 1 / d correctly
+// rounded (qb_rcp): y = v rcp is within 1.5 steps of v / d, one step of refinement
+// brings it within one, and a second rounds it correctly (Markstein's theorem; the
+// residuals v - y d are exact).  d has no mantissa of ones only, and nothing here
+// leaves the normal range: qb_plain.
+__device__ __forceinline__ float qb_div(float v, float d, float rcp) {
+  float y = v * rcp;
+  y = __builtin_fmaf(__builtin_fmaf(-y, d, v), rcp, y);
+  return __builtin_fmaf(__builtin_fmaf(-y, d, v), rcp, y);
+}
+// 1 / d of the same: the hardware's is within a step.
+__device__ __forceinline__ float qb_rcp(float d) {
+  const float y = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-y, d, 1.0f), y, y);
+}
+// Whether a block's scale, from its largest magnitude's bits, allows that.  The
+// quotients of elements far below the largest may leave the normal range; their codes
+// are zeros all the same, 2^-10 being the least that is none.
+__device__ __forceinline__ bool qb_plain(uint32_t top, float sc) {
+  return top - 0x20000000u < 0x40000000u  // 2^-63 .. 2^65
+         && (__float_as_uint(sc) & 0x7fffffu) != 0x7fffffu;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t qb_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+
 // Codes of the eight elements that a lane of a block's sixteen holds, and the
-// block's scale.  All sixteen lanes call it together.
+// block's scale, by the rule of quant.hip.  All lanes of the wave call it together.
 __device__ __forceinline__ uint2 qb_codes(const float (&v)[8], float *scale) {
-  float amax = 0.0f;
+  // the largest magnitude by its bits; a NaN's are above an infinity's
+  uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  top = max(top, qb_dpp<0xb1>(top));   // lanes ^ 1
+  top = max(top, qb_dpp<0x4e>(top));   // ^ 2
+  top = max(top, qb_dpp<0x141>(top));  // 7 - lane, of eight
+  top = max(top, qb_dpp<0x140>(top));  // 15 - lane, of sixteen
+  float sc = qb_div(__uint_as_float(top), 448.0f, 1.0f / 448.0f);
+  uint2 out = {0, 0};
+  const bool plain = qb_plain(top, sc);
+  if (plain) {
+    const float rcp = qb_rcp(sc);
+    float y[8];
 #pragma unroll
-  for (int m = kQbLanes / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
-  const bool zero = amax == 0.0f;
-  const float sc = qb_scale(amax);
-  bool exact;
-  const float rcp = quant_rcp(sc, &exact);
-  const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-  uint2 out;
-  out.x = quant_e4m3_x4(lo, sc, rcp, exact, zero);
-  out.y = quant_e4m3_x4(hi, sc, rcp, exact, zero);
+    for (int e = 0; e < 8; ++e) y[e] = qb_div(v[e], sc, rcp);
+    out.x = cvt_e4m3_x2<true>(y[2], y[3], cvt_e4m3_x2<false>(y[0], y[1], 0u));
+    out.y = cvt_e4m3_x2<true>(y[6], y[7], cvt_e4m3_x2<false>(y[4], y[5], 0u));
+  }
+  if (__any(!plain)) {  // zeros, NaN, infinities, very large and very small blocks
+    float amax = 0.0f;  // which leaves NaN out
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+#pragma unroll
+    for (int m = kQbLanes / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+    if (!plain) {
+      const bool zero = amax == 0.0f;
+      sc = qb_scale(amax);
+      bool exact;
+      const float rcp = quant_rcp(sc, &exact);
+      const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+      out.x = quant_e4m3_x4(lo, sc, rcp, exact, zero);
+      out.y = quant_e4m3_x4(hi, sc, rcp, exact, zero);
+    }
+  }
   *scale = sc;
   return out;
 }

@@ -493,7 +493,7 @@ constexpr MmCost kMmCosts[kMmTiles] = {
     {128, 256, 1, {37.5f, 63.0f, 0, 66.0f}},
     {256, 256, 1, {69.5f, 0, 0, 0}},
 };
-constexpr double kMmLaunch = 3.7;  // a launch more: rows, or h, quantised on their own
+constexpr double kMmLaunch = 2.4;  // a launch more: rows, or h, quantised on their own
 
 // The time of tiles i, beside what every kernel takes.
 static double mm_time(int i, int mode, int M, int N, int K) {
