@@ -487,8 +487,8 @@ int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t
  * workspace  at least moe_matmul_fp8_workspace(M,N,K) bytes where xs is NULL,
  *            otherwise not used (NULL is fine); contents on entry are ignored
  * Errors: MOE_EINVAL (null, a size below 1), MOE_EUNSUPPORTED (K not a multiple of
- *         128 or above 2^20, M/32 * N/16 (each rounded up) 2^31 or more, unknown
- *         type), MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
+ *         128 or above 2^20, M/32 * N/32 (each rounded up) 2^31 or more, M or N
+ *         above 2^31 - 257, unknown type), MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
  */
 size_t moe_matmul_fp8_workspace(int M, int N, int K);
 int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const uint8_t *w,

@@ -536,9 +536,11 @@ namespace {
 
 int matmul_status(int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1) return MOE_EINVAL;
-  // a workgroup to at least 32 rows by 16 columns, fewer than 2^31 of them
-  const long long most = (((long long)M + 31) / 32) * (((long long)N + 15) / 16);
+  // a workgroup to 32 rows by 32 columns at the least, fewer than 2^31 of them
+  const long long most = (((long long)M + 31) / 32) * (((long long)N + 31) / 32);
   if (K % 128 != 0 || K > moe::kMatmulMaxK || most >= (1LL << 31)) return MOE_EUNSUPPORTED;
+  // a tile's rows and columns are counted in 32 bits
+  if (M > INT32_MAX - 256 || N > INT32_MAX - 256) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 

@@ -42,6 +42,12 @@ __device__ __forceinline__ i32x8 mm_lds(const uint8_t *p0, const uint8_t *p1) {
   return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
+// Barrier of the ring (ring.h) behind this wave's LDS reads: what they read may be
+// overwritten once every wave is here.
+__device__ __forceinline__ void mm_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Where in a panel of scales row r has that of stage s: 32 rows of one stage lie in
 // 32 banks.
 __device__ __forceinline__ int panel_at(int r, int s) { return r * 8 + (s ^ ((r >> 3) & 7)); }
@@ -217,7 +223,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
       wait_vm_imm<(NS - 2) * (JA + JW)>();
     else
       wait_vm_imm<0>();
-    ring_barrier();  // stage s is in LDS for everyone; stage s - 1 is consumed
+    mm_barrier();  // stage s is in LDS for everyone; stage s - 1 is consumed
     const int ahead = s + NS - 1, to = slot == 0 ? NS - 1 : slot - 1;
     const int panel = s / kMmPanel;
     if (s % kMmPanel < JA && (panel + 1) * kMmPanel < nst) issue_scales(panel + 1, s % kMmPanel);
@@ -303,7 +309,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
     constexpr int kTile = TT * TW * 16 * kWave;
     static_assert((KS - 1) * NW * kTile * 4 <= KS * L::kPanels + NS * SLOT, "room for the sums");
     float *const sums = reinterpret_cast<float *>(lds);
-    ring_barrier();  // every wave is done with the ring (no load is under way)
+    mm_barrier();  // every wave is done with the ring (no load is under way)
     if (group != 0) {
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
@@ -351,7 +357,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
     static_assert(kSums + BM * WN * 4 + BM * LINE <= kLds, "room for maxima and codes");
     float *const tops = reinterpret_cast<float *>(lds + kSums);
     uint8_t *const codes = lds + kSums + BM * WN * 4;
-    if (KS == 1) ring_barrier();  // every wave is done with the ring (no load is under way)
+    if (KS == 1) mm_barrier();  // every wave is done with the ring (no load is under way)
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
       float top = 0.f;
@@ -408,7 +414,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
   static_assert(kSums + NW * 32 * LINE <= kLds, "every wave has room");
   const int nw = n0 + wt0 * TF;  // first column of this wave
   if ((long long)a.N * ES % 16 == 0) {
-    if (KS == 1) ring_barrier();  // every wave is done with the ring (no load is under way)
+    if (KS == 1) mm_barrier();  // every wave is done with the ring (no load is under way)
     uint8_t *const mine = lds + kSums + wv * 32 * LINE;
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {

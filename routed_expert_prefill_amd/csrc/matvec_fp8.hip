@@ -13,8 +13,10 @@
 //
 // Few elements of x that come in bf16 or fp32 are quantised by every workgroup for
 // itself, into LDS, while its first weights are under way: 16 elements to a thread
-// at most.  A launch of its own costs 3.5 to 4 us; 8 elements cost 1.8 us, 16 3.3,
-// 32 7 (MI355X, 4096 x 4096, from one row to four).
+// at most (MI355X, 4096 x 4096: one row 0.7 us, where a launch of its own takes 2.2).
+//
+// Bound by the weights' stream and its start: one row by 4096 x 4096 5.5 us in a row of
+// launches, of which an empty one is 2.2 and 16.8 MB at 6.2 TB/s 2.7.
 #include "e4m3.h"
 #include "kernels.h"
 
@@ -22,8 +24,6 @@ namespace moe {
 
 constexpr int kMvWaves = 8;
 constexpr int kMvThreads = kMvWaves * kWave;
-// Workgroups in x: a grid takes fewer than 2^32 threads in each dimension.
-constexpr unsigned kMvLine = 1u << 22;
 constexpr int kMvAhead = 4;  // blocks of a wave that are loaded together
 // Elements of x that a workgroup quantises, eight to a thread at a time.
 constexpr int kMvPasses = 2;
@@ -48,9 +48,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_fp8_kernel(MatvecArgs a) {
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int row = lane & 15, quarter = lane >> 4;
   const int K = a.K, KB = K / 128;
-  const long long at0 = ((long long)blockIdx.y * kMvLine + blockIdx.x) * FEAT;
-  if (at0 >= a.N) return;  // the last line of workgroups may end past the weights
-  const int n0 = (int)at0;
+  const int n0 = blockIdx.x * FEAT;  // N is some thousands at the most: product_is_matvec
 
   // this lane's weight row, and the scales of the rows that its sums belong to
   const uint8_t *w;
@@ -167,9 +165,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_fp8_kernel(MatvecArgs a) {
 
 template <int KIND, bool GATEUP>
 static hipError_t mv_launch(const MatvecArgs &a, hipStream_t stream) {
-  const unsigned groups = ((unsigned)a.N + (GATEUP ? 7 : 15)) / (GATEUP ? 8 : 16);
-  const dim3 grid(groups < kMvLine ? groups : kMvLine, (groups + kMvLine - 1) / kMvLine),
-      block(kMvThreads);
+  const dim3 grid(((unsigned)a.N + (GATEUP ? 7 : 15)) / (GATEUP ? 8 : 16)), block(kMvThreads);
   return launch(matvec_fp8_kernel<KIND, GATEUP>, grid, block, stream, a);
 }
 
