@@ -526,8 +526,7 @@ int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t
   if ((x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F32) || cols % 128 != 0) return MOE_EUNSUPPORTED;
   if (misaligned(x) || misaligned(q) || misaligned(s)) return MOE_EALIGN;
   return status_from(moe::launch_quant_blocks(x, x_dtype == MOE_DT_F32, (long long)rows * (cols / 128),
-                                              q, s, grid_cap_for_current_device(),
-                                              static_cast<hipStream_t>(stream)));
+                                              q, s, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -592,7 +591,7 @@ hipError_t quantise(Product *p, hipStream_t s) {
   uint8_t *q = reinterpret_cast<uint8_t *>(p->room + p->codes.q);
   float *scales = reinterpret_cast<float *>(p->room + p->codes.s);
   const hipError_t err = moe::launch_quant_blocks(p->x, p->x_f32, (long long)p->M * (p->K / 128), q,
-                                                  scales, grid_cap_for_current_device(), s);
+                                                  scales, s);
   p->x = q;
   p->xs = scales;
   return err;

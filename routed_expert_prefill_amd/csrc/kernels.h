@@ -64,7 +64,7 @@ hipError_t launch_route_select(const SelectArgs &a, hipStream_t stream);
 
 // E4M3 codes and scales of blocks of 128 elements (quant_blocks.hip).
 hipError_t launch_quant_blocks(const void *x, bool f32, long long blocks, uint8_t *q, float *s,
-                               int grid_cap, hipStream_t stream);
+                               hipStream_t stream);
 
 // Product of E4M3 rows and weights with block scales (matmul_fp8.hip).  Columns
 // are bounded so that 32-bit offsets reach the rows of a tile.

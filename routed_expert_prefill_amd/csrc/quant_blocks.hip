@@ -44,17 +44,12 @@ __global__ __launch_bounds__(kQbThreads) void quant_blocks_kernel(const void *__
   }
 }
 
-static int qb_grid(long long blocks, int grid_cap) {
-  const long long want = (blocks + kQbBlocks - 1) / kQbBlocks;
-  const long long cap = (long long)grid_cap * 4;
-  return (int)(want < cap ? want : cap);
-}
-
 hipError_t launch_quant_blocks(const void *x, bool f32, long long blocks, uint8_t *q, float *s,
-                               int grid_cap, hipStream_t stream) {
-  const dim3 grid(qb_grid(blocks, grid_cap)), block(kQbThreads);
-  if (f32)
-    return launch(quant_blocks_kernel<kQbF32>, grid, block, stream, x, blocks, q, s);
+                               hipStream_t stream) {
+  // sixteen workgroups to each of 256 compute units at the most, each looping over blocks
+  const long long want = (blocks + kQbBlocks - 1) / kQbBlocks;
+  const dim3 grid((unsigned)(want < 4096 ? want : 4096)), block(kQbThreads);
+  if (f32) return launch(quant_blocks_kernel<kQbF32>, grid, block, stream, x, blocks, q, s);
   return launch(quant_blocks_kernel<kQbBf16>, grid, block, stream, x, blocks, q, s);
 }
 

@@ -185,20 +185,36 @@ __device__ __forceinline__ double sel_lane(double v, int lane) {
   return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
                           __builtin_amdgcn_readlane(__double2loint(v), lane));
 }
-__device__ __forceinline__ float sel_max(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double sel_max(double a, double b) { return fmax(a, b); }
-__device__ __forceinline__ float sel_min(float a, float b) { return fminf(a, b); }
 __device__ __forceinline__ double sel_min(double a, double b) { return fmin(a, b); }
+// (in fp32 the instruction itself: fmaxf and fminf quiet each operand first, and a
+// lane move of theirs is one more)
+__device__ __forceinline__ float sel_max(float a, float b) {
+  asm("v_max_f32 %0, %0, %1" : "+v"(a) : "v"(b));
+  return a;
+}
 
 // The largest of the wave's values, in scalar registers.
-template <typename R>
-__device__ __forceinline__ R sel_wave_max(R v) {
+__device__ __forceinline__ double sel_wave_max(double v) {
   v = sel_max(v, sel_dpp<kXor1>(v));
   v = sel_max(v, sel_dpp<kXor2>(v));
   v = sel_max(v, sel_dpp<kHalfMirror>(v));
   v = sel_max(v, sel_dpp<kMirror>(v));
   v = sel_max(v, sel_dpp<kBcast15, 0xa>(v));
   v = sel_max(v, sel_dpp<kBcast31, 0xc>(v));
+  return sel_lane(v, kWave - 1);
+}
+// (s_nop 1: two wait states between a vector instruction and a lane move of its result)
+#define MOE_DPP_ALL " row_mask:0xf bank_mask:0xf\n\ts_nop 1\n\t"
+__device__ __forceinline__ float sel_wave_max(float v) {
+  asm("s_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 quad_perm:[1,0,3,2]" MOE_DPP_ALL
+      "v_max_f32_dpp %0, %0, %0 quad_perm:[2,3,0,1]" MOE_DPP_ALL
+      "v_max_f32_dpp %0, %0, %0 row_half_mirror" MOE_DPP_ALL
+      "v_max_f32_dpp %0, %0, %0 row_mirror" MOE_DPP_ALL
+      "v_max_f32_dpp %0, %0, %0 row_bcast:15 row_mask:0xa bank_mask:0xf\n\ts_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_bcast:31 row_mask:0xc bank_mask:0xf\n\ts_nop 1"
+      : "+v"(v));
   return sel_lane(v, kWave - 1);
 }
 
@@ -209,11 +225,35 @@ __device__ __forceinline__ float sel_wave_sum(float v) {
 }
 
 // The two largest of 2 * 2 values in descending pairs.
-template <typename R>
-__device__ __forceinline__ void sel_merge(R &one, R &two, R o1, R o2) {
+__device__ __forceinline__ void sel_merge(double &one, double &two, double o1, double o2) {
   two = sel_max(sel_min(one, o1), sel_max(two, o2));
   one = sel_max(one, o1);
 }
+__device__ __forceinline__ void sel_merge(float &one, float &two, float o1, float o2) {
+  float low = one;
+  asm("v_min_f32 %0, %0, %1" : "+v"(low) : "v"(o1));
+  two = sel_max(low, sel_max(two, o2));
+  one = sel_max(one, o1);
+}
+// The same with the pair of the lane that CTRL names.
+#define MOE_SEL_MERGE(NAME, CTRL, HOW)                                                 \
+  __device__ __forceinline__ void NAME(double &one, double &two) {                     \
+    sel_merge(one, two, sel_dpp<CTRL>(one), sel_dpp<CTRL>(two));                       \
+  }                                                                                    \
+  __device__ __forceinline__ void NAME(float &one, float &two) {                       \
+    float low;                                                                         \
+    asm("s_nop 1\n\t"                                                                  \
+        "v_min_f32_dpp %2, %0, %0 " HOW " row_mask:0xf bank_mask:0xf\n\t"              \
+        "v_max_f32_dpp %1, %1, %1 " HOW " row_mask:0xf bank_mask:0xf\n\t"              \
+        "v_max_f32_dpp %0, %0, %0 " HOW " row_mask:0xf bank_mask:0xf\n\t"              \
+        "v_max_f32 %1, %1, %2"                                                         \
+        : "+v"(one), "+v"(two), "=&v"(low));                                           \
+  }
+MOE_SEL_MERGE(sel_merge_xor1, kXor1, "quad_perm:[1,0,3,2]")
+MOE_SEL_MERGE(sel_merge_xor2, kXor2, "quad_perm:[2,3,0,1]")
+MOE_SEL_MERGE(sel_merge_half, kHalfMirror, "row_half_mirror")
+MOE_SEL_MERGE(sel_merge_row, kMirror, "row_mirror")
+#undef MOE_SEL_MERGE
 
 // A token with choices in fp32 or fp64: lane l holds experts 4 l .. 4 l + 3.  False,
 // and nothing written, where fp32 does not tell the order of fp64, and for NaN,
@@ -332,10 +372,10 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R 
     R one = x[0], two = x[1];
     const int group = runs ? lane / lanes : lane;  // that this lane has the value of
     if (runs) {
-      if (lanes >= 2) sel_merge(one, two, sel_dpp<kXor1>(one), sel_dpp<kXor1>(two));
-      if (lanes >= 4) sel_merge(one, two, sel_dpp<kXor2>(one), sel_dpp<kXor2>(two));
-      if (lanes >= 8) sel_merge(one, two, sel_dpp<kHalfMirror>(one), sel_dpp<kHalfMirror>(two));
-      if (lanes >= 16) sel_merge(one, two, sel_dpp<kMirror>(one), sel_dpp<kMirror>(two));
+      if (lanes >= 2) sel_merge_xor1(one, two);
+      if (lanes >= 4) sel_merge_xor2(one, two);
+      if (lanes >= 8) sel_merge_half(one, two);
+      if (lanes >= 16) sel_merge_row(one, two);
       if (lanes >= 32) sel_merge(one, two, (R)__shfl_xor(one, 16), (R)__shfl_xor(two, 16));
     } else {
       // lane g looks through group g
