@@ -21,6 +21,12 @@
  *                     selection", lucebox8 gfx1151 A/B; exact-zero masked
  *                     routes: "... by expert", Summary).
  *
+ * Beside the path stand the calls that a served layer makes around it: another
+ * selection of experts (moe_route_select), the norm in front (moe_add_rmsnorm),
+ * the layer for single tokens (moe_decode_ffn), the shared expert
+ * (moe_shared_ffn), and the 8-bit product and quantisation of dense layers
+ * (moe_matmul_fp8, moe_quant_blocks_fp8).
+ *
  * Conventions for every call:
  *  - Pointers are DEVICE pointers unless marked "host".  The caller owns every
  *    buffer; the library never allocates, frees or synchronises.  Work is
@@ -476,9 +482,14 @@ int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t
  *   y[m,n] = sum over blocks b of  xs[m,b] * ws[n/128,b] *
  *            sum over columns c of block b of  x[m,c] * w[n,c]
  *
- * Products and sums in fp32 (the two scales of a block are multiplied first, in
- * fp32: their product has to lie in its range); y is rounded once.  One row's
- * result depends on no other row.
+ * fp32 results: products are exact and their sums fp32's.  bf16 results of more
+ * than a few rows take the 8-bit matrix instruction, which of the products of
+ * eight neighbouring columns drops what lies more than 13 bits below the largest
+ * (1.5e-5 of the result's norm over random codes, beside the rounding's 1.7e-3).
+ * The two scales of a block are multiplied first, in fp32: their product has to
+ * lie in its range.  y is rounded once.  One row's result depends on no other
+ * row, but its last bits on how many there are: a kernel is chosen by the sizes,
+ * and sums are added in its order.
  *
  * x, xs      xs given: E4M3 codes uint8 [M,K] and fp32 scales [M,K/128]
  *            (moe_quant_blocks_fp8); xs NULL: bf16 [M,K], quantised so by the call
@@ -499,7 +510,7 @@ int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const ui
  * The gated layer that every token passes beside its routed experts; its rows are
  * the `shared` of moe_combine_shared and moe_decode_ffn:
  *
- *   g = Wg . x[t],  u = Wu . x[t],  h = silu(g) * u     (fp32, products as above)
+ *   g = Wg . x[t],  u = Wu . x[t],  h = silu(g) * u     (products as for fp32 results)
  *   h quantised as moe_quant_blocks_fp8 does            (from fp32: one rounding)
  *   out[t] = Wd . h
  *

@@ -2,6 +2,7 @@
 // (all before any HIP call), workspace layout and launch sequencing.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -492,7 +493,7 @@ int moe_route_select(const moe_select_desc *desc, const void *logits, const floa
   if (!desc || !logits || !topk_ids || !topk_w) return MOE_EINVAL;
   const moe_select_desc &d = *desc;
   if (d.T < 1 || d.E < 1 || d.k < 1 || d.groups < 1 || d.top_groups < 1 ||
-      (long long)d.T * d.E >= (1LL << 31) || !(d.scale > -3.40282347e38f && d.scale < 3.40282347e38f))
+      (long long)d.T * d.E >= (1LL << 31) || !std::isfinite(d.scale))
     return MOE_EINVAL;
   const bool types = (d.logits_dtype == MOE_DT_BF16 || d.logits_dtype == MOE_DT_F32) &&
                      (d.scores == MOE_SCORES_SOFTMAX || d.scores == MOE_SCORES_SIGMOID);
@@ -525,8 +526,9 @@ int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t
   if (!x || !q || !s || rows < 1 || cols < 1) return MOE_EINVAL;
   if ((x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F32) || cols % 128 != 0) return MOE_EUNSUPPORTED;
   if (misaligned(x) || misaligned(q) || misaligned(s)) return MOE_EALIGN;
-  return status_from(moe::launch_quant_blocks(x, x_dtype == MOE_DT_F32, (long long)rows * (cols / 128),
-                                              q, s, static_cast<hipStream_t>(stream)));
+  const long long blocks = (long long)rows * (cols / 128);
+  return status_from(moe::launch_quant_blocks(x, x_dtype == MOE_DT_F32, blocks, q, s,
+                                              static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -609,7 +611,8 @@ moe::MatmulArgs matmul_args(const Product &p, const uint8_t *w, const float *ws)
   return a;
 }
 
-moe::MatvecArgs matvec_args(const Product &p, const uint8_t *w, const float *ws, void *y, bool f32) {
+moe::MatvecArgs matvec_args(const Product &p, const uint8_t *w, const float *ws, void *y,
+                            bool f32) {
   moe::MatvecArgs a{};
   a.x = p.x;
   a.xs = p.xs;

@@ -17,6 +17,12 @@
 // A workgroup computes BM rows by BN weight rows.  A stage of its LDS ring
 // (ring.h) is one block of 128 columns: a 128-byte line of each row, and the
 // rows' scales for that block.
+//
+// Bound by the matrix unit and its clock where tiles are many: 8192 rows by 4096 x 4096
+// take 132 us in bf16 (the products alone, without loads, 98) and 254 in fp32, where
+// converting codes is half of the instructions beside the products.  Bound by what a
+// stage waits for where they are few: 777 rows by 1416 x 1152 take 8.1 us, their bytes
+// 1.5 (MI355X).
 #include <type_traits>
 
 #include "e4m3.h"
@@ -332,7 +338,8 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const f32x4 v = *reinterpret_cast<const f32x4 *>(
-                sums + ((g - 1) * NW + wv) * kTile + (((tt * TW + tw) * 4 + j / 4) * kWave + lane) * 4);
+                sums + ((g - 1) * NW + wv) * kTile +
+                (((tt * TW + tw) * 4 + j / 4) * kWave + lane) * 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[tt][tw][j + e] += v[e];
           }
@@ -425,7 +432,8 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
           const f32x16 &v = acc[tt][tw];
           uint8_t *to = mine + rr * LINE + (tw * TF + g * 8 + rh * 4) * ES;
           if (ES == 4) {
-            *reinterpret_cast<f32x4 *>(to) = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+            *reinterpret_cast<f32x4 *>(to) =
+                f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
           } else {
             uint2 b;
             b.x = f32_to_bf16_bits(v[4 * g]) | (uint32_t)f32_to_bf16_bits(v[4 * g + 1]) << 16;
@@ -480,9 +488,10 @@ static hipError_t mm_launch(const MatmulArgs &a, hipStream_t stream) {
 // waves shorten; large ones move less for each product.  At 4096 columns of both:
 // 100 rows 9 us in tiles of 32 x 64 with four groups (13 with one), 14 in 64 x 128;
 // 401 rows 15.4 in 64 x 128 with two groups, 21 in 64 x 64, 29 in 32 x 64; 2048 rows
-// 40 in 128 x 256, 49 in 64 x 128, 61 in 256 x 256; 8192 rows 142 in 256 x 256
-// (1.9 PFLOP/s), 152 in 128 x 256, 185 in 64 x 128.  fp32 results in tiles of 256 x 256
-// would spill registers.
+// 40 in 128 x 256, 48 in 64 x 128, 60 in 256 x 256; 8192 rows 132 to 143 in 256 x 256
+// (1.9 to 2.1 PFLOP/s), 155 in 128 x 256, 186 in 64 x 128.  fp32 results in tiles of
+// 256 x 256 would spill registers; with codes converted again for every product they
+// do not, and 8192 rows take 296, in 128 x 256 257.
 struct MmCost {
   int bm, bn;
   int per;                          // workgroups to a compute unit in a full round

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_fp8_kernel(MatvecArgs a) {
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int row = lane & 15, quarter = lane >> 4;
   const int K = a.K, KB = K / 128;
-  const int n0 = blockIdx.x * FEAT;  // N is some thousands at the most: product_is_matvec
+  const int n0 = blockIdx.x * FEAT;  // N is below a million: product_is_matvec
 
   // this lane's weight row, and the scales of the rows that its sums belong to
   const uint8_t *w;
@@ -115,7 +115,8 @@ __global__ __launch_bounds__(kMvThreads) void matvec_fp8_kernel(MatvecArgs a) {
       i32x4 xr[2];
       float xsc;
       if constexpr (QUANT) {
-        const i32x4 *p = reinterpret_cast<const i32x4 *>(room + m * stride + b * 128 + quarter * 16);
+        const uint8_t *from = room + m * stride + b * 128 + quarter * 16;
+        const i32x4 *p = reinterpret_cast<const i32x4 *>(from);
         xr[0] = p[0];
         xr[1] = p[4];
         xsc = scales[m * KB + b];

@@ -19,8 +19,12 @@
 // rules.  (A kernel waits for its slowest wave: with the third form for every such
 // token 8192 tokens of 256 experts in groups took 21.0 us.)
 //
-// Bound by instructions, about 450 to a token: 8192 tokens of 256 experts read 8.4 MB,
-// 1.7 us at a copy's rate.
+// Bound by instructions, about 450 to a token: 8192 tokens of 256 experts in groups
+// take 11.4 us on MI355X, of which the 8.4 MB that they read are 1.7 at a copy's rate;
+// one token takes 5.0 in a row of launches, an empty one 2.2.  Choices in fp64 only
+// took 35 and 12.8; maxima through __shfl_xor, where lanes now move inside the vector
+// instruction, 12.5.  Two and four tokens to a wave, one after the other or in step:
+// 13.9 and 17.
 #include <math.h>
 
 #include "kernels.h"
@@ -260,8 +264,9 @@ MOE_SEL_MERGE(sel_merge_row, kMirror, "row_mirror")
 // infinities and a token with too few experts in service.
 //
 // How far an fp32 score may be off, with an exponential and 1 / x of a step (2^-23)
-// each and the argument's rounding, a half step of |z|: a sigmoid by 2^-23 (s (1 - s)
-// (|z| / 2 + 1) + 1.5 s), below 2^-22; a softmax score by 27 x 2^-24 of the largest
+// each and the argument's, 0.61 |z| of them (the product with log2 e, and that
+// constant's own): a sigmoid by 2^-23 (s (1 - s)
+// (0.61 |z| + 1) + 1.5 s), below 1.57 x 2^-23; a softmax score by 27 x 2^-24 of the largest
 // (its argument s |d| / top <= 0.37, the sum of 256 with its own arguments' 5.5), below
 // 2^-19.  The bias' addition rounds once more.
 template <bool SOFTMAX, typename R>
@@ -277,11 +282,13 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R 
   if (a.E % 4 == 0) {
     if (e0 < a.E) {
       if (a.f32) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.logits) + row + e0);
+        const float *from = static_cast<const float *>(a.logits) + row + e0;
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(from);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = v[i];
       } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.logits) + row + e0);
+        const uint16_t *from = static_cast<const uint16_t *>(a.logits) + row + e0;
+        const uint2 v = *reinterpret_cast<const uint2 *>(from);
         z[0] = __uint_as_float(v.x << 16);
         z[1] = __uint_as_float(v.x & 0xffff0000u);
         z[2] = __uint_as_float(v.y << 16);
@@ -296,7 +303,7 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R 
                      : bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[row + e0 + i]);
   }
   R x[4];
-  float top = 0.f, off = 0x1p-22f, most = 1.f;
+  float top = 0.f, off = 0x1.ap-23f, most = 1.f;
   double sum = 0.0;  // fp64 softmax
   if (SOFTMAX) {
     top = sel_wave_max(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
@@ -396,7 +403,9 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R 
     if (!F64 && a.top_groups < a.groups) {
       const R low = -sel_wave_max(keep ? -value : kNone);
       const R high = sel_wave_max(is && !keep ? value : kNone);
-      if (!(low - high > 2 * apart)) return false;
+      // (each of two values: two choices' errors and the rounding of their sum, twice a
+      // choice's size)
+      if (!(low - high > 2 * apart + most * 0x1p-22f)) return false;
     }
     if (runs) {
       if (!keep) {
@@ -439,8 +448,9 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R 
   // gates, in fp64 from the logits of the chosen
   double gate = 0.0;
   if (lane < a.k) {
-    const double v = a.f32 ? (double)static_cast<const float *>(a.logits)[row + id]
-                           : (double)bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[row + id]);
+    const size_t at = row + id;
+    const double v = a.f32 ? static_cast<const float *>(a.logits)[at]
+                           : bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[at]);
     gate = SOFTMAX ? exp(v - (double)top) : 1.0 / (1.0 + exp(-v));
   }
   if (a.renormalise) {  // at most 16: the first 16 lanes

@@ -190,3 +190,23 @@ def test_own_stream_graph_replays_and_no_module(monkeypatch):
         assert all(torch.equal(a, b) for a, b in zip(cap, want[i]))
     monkeypatch.setattr(rep, "_native", lambda: None)
     assert all(torch.equal(a, b) for a, b in zip(call(zs[2]), want[2]))
+
+
+def test_groups_whose_sums_round_apart():
+    """Two groups of nearly one value under a bias of 128: choices half a step (2^-17)
+    from fp32 numbers, of one group just above and of the other below, whose sums are
+    halfway between fp32 numbers too.  Four roundings, all of the largest size, move the
+    groups' fp32 values 2^-14 apart; scores of the last place decide."""
+    rng = np.random.default_rng(128)
+    T, u = 20000, 2.0 ** -16
+    m1 = rng.integers(int(0.55 / u), int(0.6 / u), T)
+    m2 = rng.integers(int(0.8 / u), int(0.85 / u), T)
+    m2 += (1 - m1 - m2) % 4
+    shift = rng.integers(0, 20, T)
+    m = np.stack([m1, m2, m1 + shift, m2 - shift], 1)
+    near = rng.integers(-3, 4, (T, 4)) * 2.0 ** -24
+    s = (m + 0.5) * u + near
+    z = np.log(s / (1 - s)).astype(np.float32)
+    turned = rng.random(T) < 0.5
+    z[turned] = z[turned][:, [2, 3, 0, 1]]
+    _check(z, 2, np.full(4, 128.0, np.float32), groups=2, top_groups=1)
