@@ -377,3 +377,46 @@ def test_two_streams_at_once():
                 got[i].append(rep.shared_ffn(xs[i], *W))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+
+
+def test_made_outputs_are_as_torch_makes_them():
+    import torch
+
+    import routed_expert_prefill_amd as rep
+
+    z = torch.randn(3, 64, device="cuda")
+    x = torch.randn(3, 256, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(256, 256, dtype=torch.uint8, device="cuda")
+    s = torch.ones(2, 2, device="cuda")
+
+    def calls():
+        return (*rep.route_select(z, 4), *rep.quant_blocks_fp8(x), rep.matmul_fp8(x, w, s),
+                rep.shared_ffn(x, w, w, w, s, s, s, out_dtype=torch.bfloat16))
+
+    def look(outs):
+        kinds = (torch.int32, torch.float32, torch.uint8, torch.float32, torch.float32,
+                 torch.bfloat16)
+        for o, kind in zip(outs, kinds, strict=True):
+            like = torch.empty(o.shape, dtype=kind, device="cuda")
+            assert type(o) is type(like) and o.dtype == kind and o.device == like.device
+            assert o.is_contiguous() and not o.requires_grad
+            assert o.is_inference() == like.is_inference()
+            assert o.untyped_storage().nbytes() == like.untyped_storage().nbytes()
+            assert o.untyped_storage().device == like.device
+        return [o.clone() for o in outs]
+
+    kept = look(calls())
+    with torch.inference_mode():
+        again = look(calls())
+    z.requires_grad_()
+    for a, b, c in zip(kept, again, look(calls()), strict=True):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    before = torch.cuda.memory_allocated()
+    outs = calls()
+    assert torch.cuda.memory_allocated() > before  # the allocator's own blocks
+    del outs
+    assert torch.cuda.memory_allocated() == before
+    with torch.cuda.stream(torch.cuda.Stream()):
+        other = calls()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(kept, other, strict=True))
