@@ -466,7 +466,8 @@ int moe_route_select(const moe_select_desc *desc /* host */, const void *logits,
  *            2^-149 where the quotient rounds to 0)
  *   q[i,c] = e4m3_rne_saturate(x[i,c] / s[i, c/128])   (IEEE fp32 divisions)
  *
- * A NaN gets a NaN code and is left out of its block's maximum.
+ * A NaN gets a NaN code and is left out of its block's maximum (a block of NaN, or
+ * of NaN and zeros, has the scale 1).
  * x [rows, cols], x_dtype (moe_dtype); q uint8 [rows, cols]; s fp32 [rows, cols/128].
  * Errors: MOE_EINVAL (null, rows or cols below 1), MOE_EUNSUPPORTED (unknown
  *         type, cols not a multiple of 128), MOE_EALIGN, MOE_EHIP.

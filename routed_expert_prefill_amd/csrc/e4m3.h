@@ -162,7 +162,9 @@ __device__ __forceinline__ uint32_t qb_dpp(uint32_t v) {
 }
 
 // Codes of the eight elements that a lane of a block's sixteen holds, and the
-// block's scale, by the rule of quant.hip.  All lanes of the wave call it together.
+// block's scale, by the rule of quant.hip, except that a block of NaN, or of NaN and
+// zeros, is not one of zeros: its scale is 1 as well, but a NaN keeps a NaN's code.
+// All lanes of the wave call it together.
 __device__ __forceinline__ uint2 qb_codes(const float (&v)[8], float *scale) {
   // the largest magnitude by its bits; a NaN's are above an infinity's
   uint32_t top = 0;
@@ -190,7 +192,7 @@ __device__ __forceinline__ uint2 qb_codes(const float (&v)[8], float *scale) {
 #pragma unroll
     for (int m = kQbLanes / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
     if (!plain) {
-      const bool zero = amax == 0.0f;
+      const bool zero = top == 0;  // (amax is 0 of NaN too)
       sc = qb_scale(amax);
       bool exact;
       const float rcp = quant_rcp(sc, &exact);

@@ -382,7 +382,8 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < WN; ++i) top = fmaxf(top, tops[row * WN + i]);
-      const bool zero = top == 0.0f;
+      // (maxima leave NaN out: where top is 0 the block may hold NaN, which gets a NaN's
+      // code under the scale 1 as zeros get zeros')
       const float sc = qb_scale(top);
       bool exact;
       const float rcp = quant_rcp(sc, &exact);
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
           const f32x16 &v = acc[tt][tw];
           const float four[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
           *reinterpret_cast<uint32_t *>(codes + row * LINE + (wt0 + tw) * 16 + g * 8 + rh * 4) =
-              quant_e4m3_x4(four, sc, rcp, exact, zero);
+              quant_e4m3_x4(four, sc, rcp, exact, false);
         }
       if (wv % WN == 0 && rh == 0 && m0 + row < a.M)
         a.hs[(size_t)(m0 + row) * (a.N / 128) + n0 / 128] = sc;
