@@ -483,10 +483,12 @@ int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t
  *   y[m,n] = sum over blocks b of  xs[m,b] * ws[n/128,b] *
  *            sum over columns c of block b of  x[m,c] * w[n,c]
  *
- * fp32 results: products are exact and their sums fp32's.  bf16 results of more
- * than a few rows take the 8-bit matrix instruction, which of the products of
- * eight neighbouring columns drops what lies more than 13 bits below the largest
- * (1.5e-5 of the result's norm over random codes, beside the rounding's 1.7e-3).
+ * Products are exact and their sums fp32's.  With MOE_DT_BF16 | MOE_SHORT_SUMS for
+ * y_dtype, bf16 results of more than a few rows may take the 8-bit matrix
+ * instruction, twice as fast for thousands of rows: of the products of eight
+ * neighbouring columns it drops what lies more than 13 bits below the largest (over
+ * random codes 1.5e-5 of the result's norm, beside the rounding's 1.7e-3; more of
+ * results whose largest terms cancel).
  * The two scales of a block are multiplied first, in fp32: their product has to
  * lie in its range.  y is rounded once.  One row's result depends on no other
  * row, but its last bits on how many there are: a kernel is chosen by the sizes,
@@ -495,13 +497,14 @@ int moe_quant_blocks_fp8(const void *x, int x_dtype, int rows, int cols, uint8_t
  * x, xs      xs given: E4M3 codes uint8 [M,K] and fp32 scales [M,K/128]
  *            (moe_quant_blocks_fp8); xs NULL: bf16 [M,K], quantised so by the call
  * w, ws      E4M3 codes uint8 [N,K], fp32 [ceil(N/128), K/128]; N is any
- * y          [M,N], y_dtype (moe_dtype); overlaps no input
+ * y          [M,N], y_dtype (moe_dtype, or MOE_DT_BF16 | MOE_SHORT_SUMS); overlaps no input
  * workspace  at least moe_matmul_fp8_workspace(M,N,K) bytes where xs is NULL,
  *            otherwise not used (NULL is fine); contents on entry are ignored
  * Errors: MOE_EINVAL (null, a size below 1), MOE_EUNSUPPORTED (K not a multiple of
  *         128 or above 2^20, M/32 * N/32 (each rounded up) 2^31 or more, M or N
  *         above 2^31 - 257, unknown type), MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
  */
+#define MOE_SHORT_SUMS 0x100 /* beside MOE_DT_BF16 */
 size_t moe_matmul_fp8_workspace(int M, int N, int K);
 int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const uint8_t *w,
                    const float *ws, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
@@ -511,14 +514,14 @@ int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const ui
  * The gated layer that every token passes beside its routed experts; its rows are
  * the `shared` of moe_combine_shared and moe_decode_ffn:
  *
- *   g = Wg . x[t],  u = Wu . x[t],  h = silu(g) * u     (products as for fp32 results)
+ *   g = Wg . x[t],  u = Wu . x[t],  h = silu(g) * u     (sums in fp32)
  *   h quantised as moe_quant_blocks_fp8 does            (from fp32: one rounding)
- *   out[t] = Wd . h
+ *   out[t] = Wd . h                                     (as moe_matmul_fp8)
  *
  * x, xs      as for moe_matmul_fp8: bf16 [T,d], or codes [T,d] and scales [T,d/128]
  * w_gate, w_up  uint8 [f,d], s_gate, s_up fp32 [f/128, d/128]
  * w_down     uint8 [d,f], s_down fp32 [d/128, f/128]
- * out        [T,d], out_dtype (moe_dtype); overlaps no input
+ * out        [T,d], out_dtype as y_dtype there; overlaps no input
  * workspace  at least moe_shared_ffn_workspace(T,d,f) bytes; contents on entry are ignored
  * Errors: MOE_EINVAL (null, a size below 1), MOE_EUNSUPPORTED (d or f not a
  *         multiple of 128 or above 2^20, T rows too many for moe_matmul_fp8,

@@ -14,7 +14,8 @@ from typing import NamedTuple, Optional
 
 from . import _lib
 from ._lib import (MOE_ACT_BF16, MOE_ACT_FP8_E4M3_ROW, MOE_W_BF16, MOE_W_FP8_E4M3_B128,
-                   MOE_SCORES_SIGMOID, MOE_SCORES_SOFTMAX, MOE_W_MXFP4, LibraryNotBuilt, MoeFfnDesc)
+                   MOE_SCORES_SIGMOID, MOE_SCORES_SOFTMAX, MOE_SHORT_SUMS, MOE_W_MXFP4,
+                   LibraryNotBuilt, MoeFfnDesc)
 
 __all__ = [
     "route_topk", "route_build", "route_build_noalloc", "grouped_ffn", "grouped_ffn_codes", "combine", "combine_shared", "quant_rows_fp8", "add_rmsnorm", "decode_ffn", "route_select", "quant_blocks_fp8", "matmul_fp8", "shared_ffn", "MoEPrefill", "RouteTable",
@@ -706,6 +707,14 @@ def _need_out(out, out_dtype, shape, dev):
     return out
 
 
+def _result_type(out, short) -> int:
+    """out's type with the flag for short sums, as the C ABI takes them."""
+    f32 = out.dtype == _torch().float32
+    if short and f32:
+        raise ValueError("short_sums is for bf16 results")
+    return int(f32) | (MOE_SHORT_SUMS if short else 0)
+
+
 def _need_ws(workspace, need, dev):
     torch = _torch()
     if workspace is None:
@@ -714,21 +723,25 @@ def _need_ws(workspace, need, dev):
     return workspace
 
 
-def matmul_fp8(x, w, s, out=None, out_dtype=None, workspace=None):
+def matmul_fp8(x, w, s, out=None, out_dtype=None, workspace=None, short_sums: bool = False):
     """moe_matmul_fp8: x [M, K] times the transpose of 8-bit weights w [N, K].
 
     x: bf16 rows, quantised by the call, or the pair (codes, scales) of
     quant_blocks_fp8.  w: E4M3 codes (uint8), s: fp32 [ceil(N / 128), K / 128], a
     scale for each block of 128 x 128.  out [M, N] is fp32 or bf16; if it is not
     given, it is made in out_dtype (torch.float32 by default).  workspace is used
-    for bf16 rows only.  No rows: nothing is launched."""
+    for bf16 rows only.  No rows: nothing is launched.
+
+    Sums are fp32's.  short_sums, for bf16 results: they may keep of eight products
+    what lies within 13 bits of the largest, which is twice as fast for many rows."""
     torch = _torch()
     native = _native()
     rows, xs = x if type(x) is tuple and len(x) == 2 else (x, None)
+    short = bool(short_sums)  # such calls are not worth the module's short way
     if native is not None and getattr(rows, "is_cuda", False):
         dev = torch._C._cuda_getDevice()
         done = native.matmul_fp8(rows, xs, w, s, out, out_dtype in (None, torch.float32),
-                                 out is None and out_dtype not in (None, torch.float32, torch.bfloat16),
+                                 short or (out is None and out_dtype not in (None, torch.float32, torch.bfloat16)),
                                  workspace, dev, torch._C._cuda_getCurrentRawStream(dev))
         if type(done) is int:  # the launch's status, as in add_rmsnorm
             _lib.check(done, "moe_matmul_fp8")
@@ -743,6 +756,7 @@ def matmul_fp8(x, w, s, out=None, out_dtype=None, workspace=None):
     N = _int32(w.shape[0], "N")
     _need_blocks(w, s, "", N, K, dev)
     out = _need_out(out, out_dtype, (M, N), dev)
+    kind = _result_type(out, short)
     if M == 0:
         return out
     if xs is None:
@@ -750,27 +764,29 @@ def matmul_fp8(x, w, s, out=None, out_dtype=None, workspace=None):
     else:
         workspace = None
     rc = lib.moe_matmul_fp8(x.data_ptr(), _ptr(xs), M, N, K, w.data_ptr(), s.data_ptr(),
-                            out.data_ptr(), int(out.dtype == torch.float32), _ptr(workspace),
+                            out.data_ptr(), kind, _ptr(workspace),
                             0 if workspace is None else workspace.numel(), _stream())
     _lib.check(rc, "moe_matmul_fp8")
     return out
 
 
 def shared_ffn(x, w_gate, w_up, w_down, s_gate, s_up, s_down, out=None, out_dtype=None,
-               workspace=None):
+               workspace=None, short_sums: bool = False):
     """moe_shared_ffn: the shared expert, Wd . (silu(Wg . x) * (Wu . x)), whose rows
     are the `shared` of combine_shared, decode_ffn and MoEPrefill.
 
-    x [T, d] and out [T, d] as for matmul_fp8; w_gate, w_up [f, d] and w_down
-    [d, f] E4M3 codes (uint8), their scales fp32 for each block of 128 x 128."""
+    x [T, d], out [T, d] and short_sums (of the down product) as for matmul_fp8;
+    w_gate, w_up [f, d] and w_down [d, f] E4M3 codes (uint8), their scales fp32 for
+    each block of 128 x 128."""
     torch = _torch()
     native = _native()
     rows, xs = x if type(x) is tuple and len(x) == 2 else (x, None)
+    short = bool(short_sums)  # such calls are not worth the module's short way
     if native is not None and getattr(rows, "is_cuda", False):
         dev = torch._C._cuda_getDevice()
         done = native.shared_ffn(rows, xs, w_gate, w_up, w_down, s_gate, s_up, s_down, out,
                                  out_dtype in (None, torch.float32),
-                                 out is None and out_dtype not in (None, torch.float32, torch.bfloat16),
+                                 short or (out is None and out_dtype not in (None, torch.float32, torch.bfloat16)),
                                  workspace, dev, torch._C._cuda_getCurrentRawStream(dev))
         if type(done) is int:  # the launch's status, as in add_rmsnorm
             _lib.check(done, "moe_shared_ffn")
@@ -789,13 +805,14 @@ def shared_ffn(x, w_gate, w_up, w_down, s_gate, s_up, s_down, out=None, out_dtyp
     _need_blocks(w_up, s_up, "_up", f, d, dev)
     _need_blocks(w_down, s_down, "_down", d, f, dev)
     out = _need_out(out, out_dtype, (T, d), dev)
+    kind = _result_type(out, short)
     if T == 0:
         return out
     workspace = _need_ws(workspace, lib.moe_shared_ffn_workspace(T, d, f), dev)
     rc = lib.moe_shared_ffn(x.data_ptr(), _ptr(xs), T, d, f, w_gate.data_ptr(), w_up.data_ptr(),
                             w_down.data_ptr(), s_gate.data_ptr(), s_up.data_ptr(),
-                            s_down.data_ptr(), out.data_ptr(), int(out.dtype == torch.float32),
-                            workspace.data_ptr(), workspace.numel(), _stream())
+                            s_down.data_ptr(), out.data_ptr(), kind, workspace.data_ptr(),
+                            workspace.numel(), _stream())
     _lib.check(rc, "moe_shared_ffn")
     return out
 

@@ -24,6 +24,7 @@ MOE_W_FP8_E4M3_B128 = 1
 MOE_W_MXFP4 = 2
 MOE_DT_BF16 = 0
 MOE_DT_F32 = 1
+MOE_SHORT_SUMS = 0x100  # beside MOE_DT_BF16
 MOE_ACT_BF16 = 0
 MOE_ACT_FP8_E4M3_ROW = 1
 MOE_SCORES_SOFTMAX = 0

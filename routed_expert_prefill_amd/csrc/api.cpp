@@ -627,16 +627,27 @@ moe::MatvecArgs matvec_args(const Product &p, const uint8_t *w, const float *ws,
   return a;
 }
 
+// A result's type with its flag; false where there is no such.
+struct Result {
+  bool f32, short_sums;
+};
+bool result_type(int y_dtype, Result *r) {
+  r->f32 = y_dtype == MOE_DT_F32;
+  r->short_sums = y_dtype == (MOE_DT_BF16 | MOE_SHORT_SUMS);
+  return r->f32 || r->short_sums || y_dtype == MOE_DT_BF16;
+}
+
 // y = x w
-hipError_t product(Product p, const uint8_t *w, const float *ws, void *y, bool f32, hipStream_t s) {
+hipError_t product(Product p, const uint8_t *w, const float *ws, void *y, Result r, hipStream_t s) {
   const bool few = moe::product_is_matvec(p.M, p.N, p.K, false, p.xs != nullptr);
   hipError_t err = hipSuccess;
   if (!p.xs && !(few && moe::matvec_quantises(p.M, p.K))) err = quantise(&p, s);
   if (err != hipSuccess) return err;
-  if (few) return moe::launch_matvec_fp8(matvec_args(p, w, ws, y, f32), s);
+  if (few) return moe::launch_matvec_fp8(matvec_args(p, w, ws, y, r.f32), s);
   moe::MatmulArgs a = matmul_args(p, w, ws);
   a.y = y;
-  a.f32 = f32;
+  a.f32 = r.f32;
+  a.short_sums = r.short_sums;
   return moe::launch_matmul_fp8(a, s);
 }
 
@@ -684,15 +695,15 @@ int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const ui
   if (!x || !w || !ws || !y) return MOE_EINVAL;
   const int st = matmul_status(M, N, K);
   if (st != MOE_OK) return st;
-  if (y_dtype != MOE_DT_BF16 && y_dtype != MOE_DT_F32) return MOE_EUNSUPPORTED;
+  Result type;
+  if (!result_type(y_dtype, &type)) return MOE_EUNSUPPORTED;
   const void *ptrs[] = {x, xs, w, ws, y, workspace};
   for (const void *p : ptrs)
     if (p && misaligned(p)) return MOE_EALIGN;
   const CodesLayout L = codes_layout(0, M, K);
   if (!xs && (!workspace || workspace_bytes < L.end)) return MOE_EWORKSPACE;
   const Product p = {x, xs, false, M, N, K, static_cast<char *>(workspace), L};
-  return status_from(product(p, w, ws, y, y_dtype == MOE_DT_F32,
-                             static_cast<hipStream_t>(stream)));
+  return status_from(product(p, w, ws, y, type, static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_shared_ffn_workspace(int T, int d, int f) {
@@ -706,7 +717,8 @@ int moe_shared_ffn(const void *x, const float *xs, int T, int d, int f, const ui
   if (!x || !w_gate || !w_up || !w_down || !s_gate || !s_up || !s_down || !out) return MOE_EINVAL;
   const int st = shared_status(T, d, f);
   if (st != MOE_OK) return st;
-  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32) return MOE_EUNSUPPORTED;
+  Result type;
+  if (!result_type(out_dtype, &type)) return MOE_EUNSUPPORTED;
   const void *ptrs[] = {x, xs, w_gate, w_up, w_down, s_gate, s_up, s_down, out, workspace};
   for (const void *p : ptrs)
     if (p && misaligned(p)) return MOE_EALIGN;
@@ -718,7 +730,7 @@ int moe_shared_ffn(const void *x, const float *xs, int T, int d, int f, const ui
   Product down = {nullptr, nullptr, true, T, d, f, base, L.h};
   hipError_t err = gate_up(up, w_gate, s_gate, w_up, s_up, reinterpret_cast<float *>(base + L.hf),
                            &down, s);
-  if (err == hipSuccess) err = product(down, w_down, s_down, out, out_dtype == MOE_DT_F32, s);
+  if (err == hipSuccess) err = product(down, w_down, s_down, out, type, s);
   return status_from(err);
 }
 

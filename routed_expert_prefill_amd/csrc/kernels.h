@@ -77,6 +77,7 @@ struct MatmulArgs {
   void *y;           // [M, N] fp32, or bf16 without f32
   int M, N, K;
   bool f32;
+  bool short_sums;  // bf16 y through the 8-bit instruction
   // launch_gateup_fp8: the second matrix (w is gate, w1 up), and codes and scales of h
   const uint8_t *w1;
   const float *ws1;

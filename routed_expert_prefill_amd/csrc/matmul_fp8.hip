@@ -6,13 +6,15 @@
 // A block's sum is a chain of matrix instructions from zero, folded into the fp32
 // accumulator once with the product of the two scales in fp32.
 //
-// fp32 results: codes are turned into bf16, which holds every one of them, and go
-// through the 32x32x16 bf16 instruction.  The 8-bit instructions (both the 32x32x64
-// and the 32x32x16 one) align the products of eight neighbouring columns to the
-// largest of the eight and drop what lies more than 13 bits below it, seen on
-// MI355X with single products beside a large one: over random codes their sums
-// are 1.5e-5 of the result's norm off, where fp32's are 1e-7 to 1e-6.  bf16
-// results, whose own rounding is 1.7e-3, take the 8-bit 32x32x64 one, twice as fast.
+// Codes are turned into bf16, which holds every one of them, and go through the
+// 32x32x16 bf16 instruction: products are exact and sums fp32's, whatever the result's
+// type.  The 8-bit instructions (both the 32x32x64 and the 32x32x16 one) align the
+// products of eight neighbouring columns to the largest of the eight and drop what
+// lies more than 13 bits below it, seen on MI355X with single products beside a large
+// one: over random codes their sums are 1.5e-5 of the result's norm off, which a
+// bf16 result's own rounding of 1.7e-3 hides, but where two large products cancel the
+// small ones beside them are lost.  A caller who can bear that asks for short sums
+// (bf16 results only) and gets the 8-bit 32x32x64 one, twice as fast for many rows.
 //
 // A workgroup computes BM rows by BN weight rows.  A stage of its LDS ring
 // (ring.h) is one block of 128 columns: a 128-byte line of each row, and the
@@ -93,11 +95,14 @@ struct MmTile {
   static_assert(kDepth >= 2, "one stage loads while one is read");
 };
 
-// What a kernel does with its sums: y = x w in bf16 or fp32 (through the 8-bit or
-// the bf16 instruction), or silu(x w) * (x w1) in fp32 or quantised by blocks (both
-// through the bf16 one: sums of 1.5e-5 would have one code of h in five thousand fall
-// the other way, and the layer's bf16 results 2.1e-3 to 2.6e-3 off in place of 1.7e-3).
-enum : int { kMmBf16, kMmF32, kMmSwiglu, kMmSwigluCodes };
+// What a kernel does with its sums: y = x w in bf16 or fp32, silu(x w) * (x w1) in fp32
+// or quantised by blocks, all through the bf16 instruction (short sums would have one
+// code of h in five thousand fall the other way, and the layer's bf16 results 2.1e-3 to
+// 2.6e-3 off in place of 1.7e-3); or y in bf16 with short sums, through the 8-bit one.
+enum : int { kMmBf16, kMmF32, kMmSwiglu, kMmSwigluCodes, kMmShort, kMmModes };
+__host__ __device__ constexpr bool mm_gateup(int mode) {
+  return mode == kMmSwiglu || mode == kMmSwigluCodes;
+}
 
 template <int BM, int BN, int WM, int WN, int KS, int PER, int MODE>
 __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul_fp8_kernel(
@@ -105,7 +110,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
   using L = MmTile<BM, BN, WM, WN, KS, PER>;
   constexpr int TT = L::kTT, TW = L::kTW, NS = L::kDepth, SLOT = L::kSlot, NW = L::kWaves;
   constexpr int JA = L::kJA, JW = L::kJW;
-  constexpr bool WIDE = MODE != kMmBf16, GATEUP = MODE >= kMmSwiglu;
+  constexpr bool WIDE = MODE != kMmShort, GATEUP = mm_gateup(MODE);
   constexpr int BF = GATEUP ? BN / 2 : BN;  // columns of y
   static_assert(!GATEUP || 128 % BF == 0, "a tile's gate (up) rows lie in one block of scales");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[KS * L::kPanels + NS * SLOT];
@@ -413,7 +418,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
   // Register j of a 32x32 tile: weight row 8 (j / 4) + 4 rh + j % 4, row rr.  A wave
   // turns its tiles in LDS, 32 rows at a time, so that its stores are whole lines;
   // rows of y that do not start at multiples of 16 bytes are stored as they lie.
-  constexpr int ES = MODE == kMmBf16 ? 2 : 4;
+  constexpr int ES = MODE == kMmBf16 || MODE == kMmShort ? 2 : 4;
   constexpr int TF = GATEUP ? 16 : 32;    // columns of a tile
   constexpr int CH = TW * TF * ES / 16;   // 16-byte chunks of a row
   constexpr int LINE = CH * 16 + 16;      // of a row in LDS
@@ -474,7 +479,7 @@ __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul
 
 template <int MODE, int BM, int BN, int WM, int WN, int KS, int PER>
 static hipError_t mm_launch(const MatmulArgs &a, hipStream_t stream) {
-  constexpr int BF = MODE >= kMmSwiglu ? BN / 2 : BN;
+  constexpr int BF = mm_gateup(MODE) ? BN / 2 : BN;
   const unsigned long long tiles =
       (((unsigned long long)a.M + BM - 1) / BM) * (((unsigned long long)a.N + BF - 1) / BF);
   const dim3 grid((unsigned)(tiles < kMmLine ? tiles : kMmLine),
@@ -496,18 +501,18 @@ static hipError_t mm_launch(const MatmulArgs &a, hipStream_t stream) {
 struct MmCost {
   int bm, bn;
   int per;                          // workgroups to a compute unit in a full round
-  float round[kMmSwigluCodes + 1];  // by what the kernel does; 0: not in these tiles
+  float round[kMmModes];            // by what the kernel does; 0: not in these tiles
 };
 enum : int { k32x32, k32x64, k64x64, k64x128, k64x128Two, k64x256, k128x256, k256x256, kMmTiles };
 constexpr MmCost kMmCosts[kMmTiles] = {
-    {32, 32, 1, {5.6f, 5.9f, 0, 0}},
-    {32, 64, 1, {6.6f, 8.0f, 8.0f, 0}},
-    {64, 64, 1, {9.4f, 13.0f, 13.0f, 0}},
-    {64, 128, 1, {13.0f, 20.0f, 20.0f, 0}},
-    {64, 128, 2, {23.3f, 38.5f, 0, 0}},
-    {64, 256, 1, {0, 0, 0, 38.0f}},
-    {128, 256, 1, {37.5f, 63.0f, 0, 66.0f}},
-    {256, 256, 1, {69.5f, 0, 0, 0}},
+    {32, 32, 1, {5.9f, 5.9f, 0, 0, 5.6f}},
+    {32, 64, 1, {8.0f, 8.0f, 8.0f, 0, 6.6f}},
+    {64, 64, 1, {13.0f, 13.0f, 13.0f, 0, 9.4f}},
+    {64, 128, 1, {20.0f, 20.0f, 20.0f, 0, 13.0f}},
+    {64, 128, 2, {38.5f, 38.5f, 0, 0, 23.3f}},
+    {64, 256, 1, {0, 0, 0, 38.0f, 0}},
+    {128, 256, 1, {63.0f, 63.0f, 0, 66.0f, 37.5f}},
+    {256, 256, 1, {0, 0, 0, 0, 69.5f}},
 };
 constexpr double kMmLaunch = 2.4;  // a launch more: rows, or h, quantised on their own
 
@@ -515,7 +520,7 @@ constexpr double kMmLaunch = 2.4;  // a launch more: rows, or h, quantised on th
 static double mm_time(int i, int mode, int M, int N, int K) {
   const MmCost &c = kMmCosts[i];
   if (c.round[mode] == 0) return 1e30;
-  const int bf = mode >= kMmSwiglu ? c.bn / 2 : c.bn;
+  const int bf = mm_gateup(mode) ? c.bn / 2 : c.bn;
   const double tiles = (double)((M - 1) / c.bm + 1) * ((N - 1) / bf + 1);
   double rounds = (double)(long long)((tiles - 1) / (256 * c.per)) + 1;
   if (c.per == 2 && tiles <= 256) rounds = 0.65;  // alone on its compute unit
@@ -579,13 +584,14 @@ static hipError_t mm_product(const MatmulArgs &a, hipStream_t stream) {
     case k64x128Two: return mm_launch<MODE, 64, 128, 2, 2, 1, 2>(a, stream);
     case k128x256: return mm_launch<MODE, 128, 256, 2, 4, 1, 1>(a, stream);
     default:
-      if constexpr (MODE == kMmBf16) return mm_launch<MODE, 256, 256, 2, 4, 1, 1>(a, stream);
-      return hipErrorInvalidValue;  // mm_best names no other tiles for fp32
+      if constexpr (MODE == kMmShort) return mm_launch<MODE, 256, 256, 2, 4, 1, 1>(a, stream);
+      return hipErrorInvalidValue;  // mm_best names no other tiles for the others
   }
 }
 
 hipError_t launch_matmul_fp8(const MatmulArgs &a, hipStream_t stream) {
-  return a.f32 ? mm_product<kMmF32>(a, stream) : mm_product<kMmBf16>(a, stream);
+  if (a.f32) return mm_product<kMmF32>(a, stream);
+  return a.short_sums ? mm_product<kMmShort>(a, stream) : mm_product<kMmBf16>(a, stream);
 }
 
 }  // namespace moe
