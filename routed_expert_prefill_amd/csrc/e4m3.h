@@ -137,11 +137,11 @@ __device__ __forceinline__ void qb_load(const void *x, size_t at, float (&v)[8])
 // rounded (qb_rcp): y = v rcp is within 1.5 steps of v / d, one step of refinement
 // brings it within one, and a second rounds it correctly (Markstein's theorem; the
 // residuals v - y d are exact).  d has no mantissa of ones only, and nothing here
-// leaves the normal range: qb_plain.
+// leaves the normal range: qb_plain.  The sign is v's: of v = -0 the sums are +0.
 __device__ __forceinline__ float qb_div(float v, float d, float rcp) {
   float y = v * rcp;
   y = __builtin_fmaf(__builtin_fmaf(-y, d, v), rcp, y);
-  return __builtin_fmaf(__builtin_fmaf(-y, d, v), rcp, y);
+  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-y, d, v), rcp, y), v);
 }
 // 1 / d of the same: the hardware's is within a step.
 __device__ __forceinline__ float qb_rcp(float d) {
