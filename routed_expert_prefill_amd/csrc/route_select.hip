@@ -44,6 +44,16 @@ __device__ __forceinline__ unsigned long long sel_key(double v) {
   return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
+// From -709.8 on down exp(-z) overflows, where the score is a subnormal number still,
+// down to -745: there it is exp(z), which is less than a step off from -37 on.  (Not
+// from there, where fp32 logits lie so near that the two formulas' roundings could turn
+// their order; at -700 neighbours are 6e-5 of a score apart.)
+__device__ __forceinline__ double sel_sigmoid(double z) {
+  const bool far = z <= -700.0;
+  const double e = exp(far ? z : -z);
+  return far ? e : 1.0 / (1.0 + e);
+}
+
 __device__ __forceinline__ double sel_wave_sum(double v) {
 #pragma unroll
   for (int m = kWave / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
@@ -79,7 +89,7 @@ __device__ __forceinline__ void select_any(const SelectArgs &a, long long t, dou
     if (gone[i])
       s[i] = 0.0;
     else
-      s[i] = a.softmax ? exp(s[i] - top) : 1.0 / (1.0 + exp(-s[i]));
+      s[i] = a.softmax ? exp(s[i] - top) : sel_sigmoid(s[i]);
     sum += s[i];
   }
   if (a.softmax) {
@@ -330,7 +340,7 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (F64)
-        x[i] = 1.0 / (1.0 + exp(-(double)z[i]));
+        x[i] = sel_sigmoid(z[i]);
       else
         x[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));
     }
@@ -451,7 +461,7 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, long long t, R 
     const size_t at = row + id;
     const double v = a.f32 ? static_cast<const float *>(a.logits)[at]
                            : bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[at]);
-    gate = SOFTMAX ? exp(v - (double)top) : 1.0 / (1.0 + exp(-v));
+    gate = SOFTMAX ? exp(v - (double)top) : sel_sigmoid(v);
   }
   if (a.renormalise) {  // at most 16: the first 16 lanes
     double total = gate;
