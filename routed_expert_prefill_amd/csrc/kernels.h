@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "dense_rule.h"
 
 namespace moe {
 
@@ -87,12 +88,10 @@ struct MatmulArgs {
 hipError_t launch_matmul_fp8(const MatmulArgs &a, hipStream_t stream);
 // h = silu(x w) * (x w1): with gateup_quantises(M, N) codes and scales in hq and hs,
 // otherwise fp32 in y.  N is a multiple of 128.
-bool gateup_quantises(int M, int N, int K);
 hipError_t launch_gateup_fp8(const MatmulArgs &a, hipStream_t stream);
 
 // The same for at most kMatvecRows rows (matvec_fp8.hip).  With w1 and s1 (same
 // sizes as w0, s0; N a multiple of 8): y = silu(x w0) * (x w1) in fp32.
-constexpr int kMatvecRows = 16;
 struct MatvecArgs {
   const void *x;    // codes [M, K] with xs, else bf16 or (x_f32) fp32, quantised on the way
   const float *xs;  // [M, K / 128] or null, where matvec_quantises(M, K)
@@ -102,9 +101,6 @@ struct MatvecArgs {
   int M, N, K;
   bool x_f32, f32;
 };
-bool matvec_quantises(int M, int K);
-// Whether the matvec kernel is the faster one; codes: x is quantised already.
-bool product_is_matvec(int M, int N, int K, bool gateup, bool codes);
 hipError_t launch_matvec_fp8(const MatvecArgs &a, hipStream_t stream);
 
 int quant_max_cols();

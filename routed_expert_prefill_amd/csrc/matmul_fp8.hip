@@ -95,15 +95,7 @@ struct MmTile {
   static_assert(kDepth >= 2, "one stage loads while one is read");
 };
 
-// What a kernel does with its sums: y = x w in bf16 or fp32, silu(x w) * (x w1) in fp32
-// or quantised by blocks, all through the bf16 instruction (short sums would have one
-// code of h in five thousand fall the other way, and the layer's bf16 results 2.1e-3 to
-// 2.6e-3 off in place of 1.7e-3); or y in bf16 with short sums, through the 8-bit one.
-enum : int { kMmBf16, kMmF32, kMmSwiglu, kMmSwigluCodes, kMmShort, kMmModes };
-__host__ __device__ constexpr bool mm_gateup(int mode) {
-  return mode == kMmSwiglu || mode == kMmSwigluCodes;
-}
-
+// MODE: what the kernel does with its sums (dense_rule.h).
 template <int BM, int BN, int WM, int WN, int KS, int PER, int MODE>
 __global__ __launch_bounds__(KS *WM *WN *kWave, PER *KS *WM *WN / 4) void matmul_fp8_kernel(
     MatmulArgs a) {
@@ -486,78 +478,6 @@ static hipError_t mm_launch(const MatmulArgs &a, hipStream_t stream) {
                   (unsigned)((tiles + kMmLine - 1) / kMmLine));
   return launch(matmul_fp8_kernel<BM, BN, WM, WN, KS, PER, MODE>, grid,
                 dim3(KS * WM * WN * kWave), stream, a);
-}
-
-// The tiles to choose from, and the time of a round of them at 4096 columns (us,
-// MI355X): one workgroup, or kPer, to each of 256 compute units.  Small tiles are
-// bound by what a stage waits for (LDS, chained products), which several groups of
-// waves shorten; large ones move less for each product.  At 4096 columns of both:
-// 100 rows 9 us in tiles of 32 x 64 with four groups (13 with one), 14 in 64 x 128;
-// 401 rows 15.4 in 64 x 128 with two groups, 21 in 64 x 64, 29 in 32 x 64; 2048 rows
-// 40 in 128 x 256, 48 in 64 x 128, 60 in 256 x 256; 8192 rows 132 to 143 in 256 x 256
-// (1.9 to 2.1 PFLOP/s), 155 in 128 x 256, 186 in 64 x 128.  fp32 results in tiles of
-// 256 x 256 would spill registers; with codes converted again for every product they
-// do not, and 8192 rows take 296, in 128 x 256 257.
-struct MmCost {
-  int bm, bn;
-  int per;                          // workgroups to a compute unit in a full round
-  float round[kMmModes];            // by what the kernel does; 0: not in these tiles
-};
-enum : int { k32x32, k32x64, k64x64, k64x128, k64x128Two, k64x256, k128x256, k256x256, kMmTiles };
-constexpr MmCost kMmCosts[kMmTiles] = {
-    {32, 32, 1, {5.9f, 5.9f, 0, 0, 5.6f}},
-    {32, 64, 1, {8.0f, 8.0f, 8.0f, 0, 6.6f}},
-    {64, 64, 1, {13.0f, 13.0f, 13.0f, 0, 9.4f}},
-    {64, 128, 1, {20.0f, 20.0f, 20.0f, 0, 13.0f}},
-    {64, 128, 2, {38.5f, 38.5f, 0, 0, 23.3f}},
-    {64, 256, 1, {0, 0, 0, 38.0f, 0}},
-    {128, 256, 1, {63.0f, 63.0f, 0, 66.0f, 37.5f}},
-    {256, 256, 1, {0, 0, 0, 0, 69.5f}},
-};
-constexpr double kMmLaunch = 2.4;  // a launch more: rows, or h, quantised on their own
-
-// The time of tiles i, beside what every kernel takes.
-static double mm_time(int i, int mode, int M, int N, int K) {
-  const MmCost &c = kMmCosts[i];
-  if (c.round[mode] == 0) return 1e30;
-  const int bf = mm_gateup(mode) ? c.bn / 2 : c.bn;
-  const double tiles = (double)((M - 1) / c.bm + 1) * ((N - 1) / bf + 1);
-  double rounds = (double)(long long)((tiles - 1) / (256 * c.per)) + 1;
-  if (c.per == 2 && tiles <= 256) rounds = 0.65;  // alone on its compute unit
-  return rounds * c.round[mode] * K / 4096;
-}
-
-static int mm_best(int mode, int M, int N, int K, double *time) {
-  int best = -1;
-  for (int i = 0; i < kMmTiles; ++i) {
-    const double t = mm_time(i, mode, M, N, K);
-    if (best < 0 || t < *time) {
-      best = i;
-      *time = t;
-    }
-  }
-  return best;
-}
-
-bool gateup_quantises(int M, int N, int K) {
-  double codes, h;
-  mm_best(kMmSwigluCodes, M, N, K, &codes);
-  mm_best(kMmSwiglu, M, N, K, &h);
-  return codes < h + kMmLaunch;
-}
-
-// matvec_fp8.hip: a round of 256 workgroups takes 3.1 us at 4096 columns and 0.12
-// more for each row (MI355X, us): one row by 4096 5.4, in tiles of 32 x 32 8; 16 rows
-// 7.4 and 8.2; by 16384 one row 14.7, 16 rows 22.4, in tiles of 32 x 64 12.4.
-bool product_is_matvec(int M, int N, int K, bool gateup, bool codes) {
-  if (M > kMatvecRows) return false;
-  double tiles;
-  mm_best(gateup ? kMmSwiglu : kMmBf16, M, N, K, &tiles);
-  const double groups = ((double)N - 1) / (gateup ? 8 : 16) + 1;
-  double few = (3.1 + 0.12 * M) * ((double)(long long)((groups - 1) / 256) + 1) * K / 4096;
-  if (!codes && !matvec_quantises(M, K)) few += kMmLaunch;
-  if (!codes) tiles += kMmLaunch;
-  return few <= tiles;
 }
 
 hipError_t launch_gateup_fp8(const MatmulArgs &a, hipStream_t stream) {

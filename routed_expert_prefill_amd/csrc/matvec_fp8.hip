@@ -28,13 +28,10 @@ constexpr int kMvAhead = 4;  // blocks of a wave that are loaded together
 // Elements of x that a workgroup quantises, eight to a thread at a time.
 constexpr int kMvPasses = 2;
 constexpr int kMvQuant = kMvPasses * kMvThreads * 8;
+static_assert(kMvQuant == kMatvecQuant, "what the rule takes for granted");
 constexpr int kMvPad = 16;  // bytes behind a row of codes: rows start in different banks
 
 enum : int { kMvCodes = 2 };  // beside kQbBf16 and kQbF32
-
-bool matvec_quantises(int M, int K) {
-  return M <= kMatvecRows && (long long)M * K <= kMvQuant;
-}
 
 template <int KIND, bool GATEUP>
 __global__ __launch_bounds__(kMvThreads) void matvec_fp8_kernel(MatvecArgs a) {
