@@ -79,9 +79,11 @@ inline bool gateup_quantises(int M, int N, int K) {
   return codes < h + kMmLaunch;
 }
 
-// The kernel for few rows, matvec_fp8.hip: its rows, and the elements of x that each
-// workgroup quantises by itself.
+// The kernel for few rows, matvec_fp8.hip: its rows, its columns of y (its workgroups
+// lie in one line of fewer than 2^32 threads; times alone end below 2^18 columns), and
+// the elements of x that each workgroup quantises by itself.
 constexpr int kMatvecRows = 16;
+constexpr int kMatvecCols = 1 << 20;
 constexpr int kMatvecQuant = 8192;
 inline bool matvec_quantises(int M, int K) {
   return M <= kMatvecRows && (long long)M * K <= kMatvecQuant;
@@ -92,7 +94,7 @@ inline bool matvec_quantises(int M, int K) {
 // graph): one row by 4096 5.0, in tiles of 32 x 32 6.8; 16 rows 7.3 and 7.0; by 16384
 // one row 14.2, 16 rows 21.4, in tiles of 32 x 64 13.1.
 inline bool product_is_matvec(int M, int N, int K, bool gateup, bool codes) {
-  if (M > kMatvecRows) return false;
+  if (M > kMatvecRows || N > kMatvecCols) return false;
   double tiles;
   mm_best(gateup ? kMmSwiglu : kMmBf16, M, N, K, &tiles);
   const double groups = ((double)N - 1) / (gateup ? 8 : 16) + 1;

@@ -29,6 +29,7 @@ constexpr int kMvAhead = 4;  // blocks of a wave that are loaded together
 constexpr int kMvPasses = 2;
 constexpr int kMvQuant = kMvPasses * kMvThreads * 8;
 static_assert(kMvQuant == kMatvecQuant, "what the rule takes for granted");
+static_assert((long long)kMatvecCols / 8 * kMvThreads < 1LL << 32, "one line of workgroups");
 constexpr int kMvPad = 16;  // bytes behind a row of codes: rows start in different banks
 
 enum : int { kMvCodes = 2 };  // beside kQbBf16 and kQbF32
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_fp8_kernel(MatvecArgs a) {
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int row = lane & 15, quarter = lane >> 4;
   const int K = a.K, KB = K / 128;
-  const int n0 = blockIdx.x * FEAT;  // N is below a million: product_is_matvec
+  const int n0 = blockIdx.x * FEAT;  // of at most kMatvecCols
 
   // this lane's weight row, and the scales of the rows that its sums belong to
   const uint8_t *w;
