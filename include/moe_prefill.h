@@ -432,7 +432,8 @@ int moe_add_rmsnorm(const void *x, int x_dtype, const void *residual, void *resi
  * as an infinite one does.  ids are always k different ones of [0, E).
  *
  * logits [T,E], logits_dtype (moe_dtype); bias fp32 [E] or NULL;
- * topk_ids int32 [T,k] and topk_w fp32 [T,k] are written in full.
+ * topk_ids int32 [T,k] and topk_w fp32 [T,k] are written in full; they overlap no input
+ * and not each other.
  * Errors: MOE_EINVAL (null desc, logits or outputs, T, E, k, groups or top_groups
  *         below 1, T*E overflows int, scale not finite), MOE_EUNSUPPORTED
  *         (unknown type or scores, E > 256, k > 16, groups > 64 or no divisor of
@@ -468,7 +469,8 @@ int moe_route_select(const moe_select_desc *desc /* host */, const void *logits,
  *
  * A NaN gets a NaN code and is left out of its block's maximum (a block of NaN, or
  * of NaN and zeros, has the scale 1).
- * x [rows, cols], x_dtype (moe_dtype); q uint8 [rows, cols]; s fp32 [rows, cols/128].
+ * x [rows, cols], x_dtype (moe_dtype); q uint8 [rows, cols]; s fp32 [rows, cols/128];
+ * q and s overlap neither x nor each other.
  * Errors: MOE_EINVAL (null, rows or cols below 1), MOE_EUNSUPPORTED (unknown
  *         type, cols not a multiple of 128), MOE_EALIGN, MOE_EHIP.
  */
@@ -522,7 +524,8 @@ int moe_matmul_fp8(const void *x, const float *xs, int M, int N, int K, const ui
  * w_gate, w_up  uint8 [f,d], s_gate, s_up fp32 [f/128, d/128]
  * w_down     uint8 [d,f], s_down fp32 [d/128, f/128]
  * out        [T,d], out_dtype as y_dtype there; overlaps no input
- * workspace  at least moe_shared_ffn_workspace(T,d,f) bytes; contents on entry are ignored
+ * workspace  at least moe_shared_ffn_workspace(T,d,f) bytes, which grow with T: one for
+ *            the most rows serves fewer; contents on entry are ignored
  * Errors: MOE_EINVAL (null, a size below 1), MOE_EUNSUPPORTED (d or f not a
  *         multiple of 128 or above 2^20, T rows too many for moe_matmul_fp8,
  *         unknown type), MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.

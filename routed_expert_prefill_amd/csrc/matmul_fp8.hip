@@ -20,11 +20,13 @@
 // (ring.h) is one block of 128 columns: a 128-byte line of each row, and the
 // rows' scales for that block.
 //
-// Bound by the matrix unit and its clock where tiles are many: 8192 rows by 4096 x 4096
-// take 132 us in bf16 (the products alone, without loads, 98) and 254 in fp32, where
-// converting codes is half of the instructions beside the products.  Bound by what a
-// stage waits for where they are few: 777 rows by 1416 x 1152 take 8.1 us, their bytes
-// 1.5 (MI355X).
+// Where tiles are many, bound by matrix and vector instructions, which take turns: 8192
+// rows by 4096 x 4096 take 250 us in bf16 and 248 in fp32, calls one after another; of
+// 529 thousand cycles the matrix unit is busy 262 and the vector instructions, half of
+// them conversions of codes, take 242.  With short sums 131 us; 131 and 106 of 281
+// thousand cycles (the products alone, without loads, 98 us).  Bound by what a stage
+// waits for where tiles are few: 777 rows by 1416 x 1152 take 9.7 us in a trace, their
+// bytes 1.1 (MI355X).
 #include <type_traits>
 
 #include "e4m3.h"

@@ -15,8 +15,8 @@
 // itself, into LDS, while its first weights are under way: 16 elements to a thread
 // at most (MI355X, 4096 x 4096: one row 0.7 us, where a launch of its own takes 2.2).
 //
-// Bound by the weights' stream and its start: one row by 4096 x 4096 5.5 us in a row of
-// launches, of which an empty one is 2.2 and 16.8 MB at 6.2 TB/s 2.7.
+// Bound by the weights' stream and its start: one row by 4096 x 4096 5.0 us in a graph,
+// 5.8 in a trace, of which an empty launch is 2.2 and 16.8 MB at 6.2 TB/s 2.7.
 #include "e4m3.h"
 #include "kernels.h"
 

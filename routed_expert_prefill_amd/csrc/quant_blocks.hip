@@ -7,9 +7,9 @@
 // by row, so a matrix is one run of blocks.  Sixteen lanes hold a block, eight
 // consecutive elements each.
 //
-// Bound by memory: 8192 rows of 4096 take 17.6 us on MI355X in bf16 (5.8 TB/s over what
-// is read and written, where a large copy reaches 5.2) and 31 in fp32 (5.6).  It took 32
-// in bf16 as long as quotients near a midpoint of two codes, which bf16 numbers have
+// Bound by memory: 8192 rows of 4096 take 17.5 us on MI355X in bf16 (5.8 TB/s over what
+// is read and written, where a large copy reaches 5.2) and 29.5 in fp32 (5.7), calls one
+// after another on inputs in turn.  It took 32 in bf16 as long as quotients near a midpoint of two codes, which bf16 numbers have
 // often, were divided behind a branch (quant_e4m3_x4); four fused multiply-adds give
 // every quotient correctly rounded (qb_div).  Two or four blocks to a lane at a time:
 // nothing at this size, 0.2 to 0.8 us slower for 401 rows.  Codes stored past the

@@ -20,10 +20,10 @@
 // token 8192 tokens of 256 experts in groups took 21.0 us.)
 //
 // Bound by instructions, about 450 to a token: 8192 tokens of 256 experts in groups
-// take 11.4 us on MI355X, of which the 8.4 MB that they read are 1.7 at a copy's rate;
-// one token takes 4.4 in a row of launches, an empty one 2.2.  Choices in fp64 only
-// took 35 and 12.8; maxima through __shfl_xor, where lanes now move inside the vector
-// instruction, 12.5.  Two and four tokens to a wave, one after the other or in step:
+// take 10.2 us on MI355X, calls one after another (the kernel 9.6 at the least in a
+// trace), of which the 8.4 MB that they read are 1.4 at 6.2 TB/s; one token 4.2 in a
+// graph, an empty launch 2.2.  Choices in fp64 only took 35 and 12.8; maxima through
+// __shfl_xor, where lanes now move inside the vector instruction, 12.5 (11.4 at the time).  Two and four tokens to a wave, one after the other or in step:
 // 13.9 and 17.
 #include <math.h>
 
